@@ -267,7 +267,7 @@ def _plain_assign(s):
     b = s["table"][r, (t // BLOCK).clamp_max(s["max_blocks"] - 1)].long()
     s["slots"].copy_(torch.where(ok & (b >= 0), b * BLOCK + t % BLOCK, -1))
     s["held_out"].copy_(torch.where(served, torch.maximum(held, lens), held))
-    s["head_out"].copy_(s["head"] + torch.where(served, total, 0).amax())
+    s["head_out"].copy_(s["head"] + torch.where(need > 0, total, 0).amax())
     return _assign_outputs(s)
 
 
