@@ -89,6 +89,13 @@ enum kvtc_status {
 #define KVTC_FLAG_TIMEOUT 2u   /* a bounded mbarrier wait ran out */
 #define KVTC_FLAG_BLOCK 4u     /* block-table id outside [0, num_blocks) */
 #define KVTC_FLAG_FORMAT 8u    /* packed stream inconsistent (field packing) */
+#define KVTC_FLAG_SPACE 16u    /* free list, block table or slot map too short */
+
+/* Element type of a paged pool read by kvtc_paged_attend. */
+enum kvtc_dtype {
+  KVTC_DTYPE_BF16 = 0,
+  KVTC_DTYPE_FP16 = 1
+};
 
 typedef struct kvtc_calib kvtc_calib;
 
@@ -299,6 +306,146 @@ int kvtc_decompress_packed(const kvtc_calib* calib, int layer0, int nlayers,
                            const int64_t* offsets, int64_t T,
                            void* const* dst, int64_t ld, void* cuda_stream,
                            void* const* layer_events);
+
+/*
+ * Paged serving -- the calls around kvtc_decompress_paged in one serving
+ * step: blocks and slots for the requests' tokens, rows of new tokens
+ * written through the slots, and attention of one new token per request
+ * over the pool.  They need no calibration: each takes the device ordinal
+ * that owns its pointers (whatever device is current), allocates nothing,
+ * keeps nothing between calls and never synchronises, so a call can be
+ * captured into a CUDA graph and replayed with other lengths, ids and rows
+ * in the same buffers.  Their kernels report faults into `flags`, a DEVICE
+ * uint32 word of the caller's into which KVTC_FLAG_* bits are ORed (it is
+ * never cleared here; NULL: faults are not reported).  Blocks hold 16
+ * tokens (block_size 16, other sizes ENOTSUP), R <= 4096.
+ */
+
+/* Device workspace bytes kvtc_paged_assign needs (< 0 on error). */
+int64_t kvtc_paged_assign_workspace_bytes(int R);
+
+/*
+ * kvtc_paged_assign -- give R requests the blocks that their tokens need,
+ * in request order, and list the slots of the new tokens.
+ *   held, lens   : DEVICE int32 [R]: tokens of request r that have blocks,
+ *                  and tokens that it is to have; its new tokens are
+ *                  held[r] .. lens[r] - 1 (none when lens[r] <= held[r],
+ *                  negative values count as 0).
+ *   free_blocks  : DEVICE int32 [n_free]: block ids, given out from the
+ *                  front.  May be NULL when n_free is 0.
+ *   head         : DEVICE int64 [1]: how many of them have been given out.
+ *   block_table  : DEVICE int32 [R][max_blocks], as kvtc_decompress_paged
+ *                  reads it: columns ceil(held[r] / 16) ..
+ *                  ceil(lens[r] / 16) - 1 of a served request are written,
+ *                  all others are left as they are.
+ *   slots        : DEVICE int64 [slot_capacity], written whole: new token j
+ *                  of request r at slots[cu[r] + j] is row
+ *                  id * 16 + t % 16 of a pool seen as [num_blocks * 16][D]
+ *                  (t = held[r] + j, id = block_table[r][t / 16]); -1 for a
+ *                  token without a place (request not served, or a
+ *                  negative id in the table) and behind the last token.
+ *                  Tokens past slot_capacity get blocks but no entry.  May
+ *                  be NULL when slot_capacity is 0.
+ *   cu           : DEVICE int64 [R + 1], written: cu[r] = new tokens of the
+ *                  requests before r, served or not; cu[R] = all of them.
+ *   held_out     : DEVICE int32 [R], written: max(held[r], lens[r]) of a
+ *                  served request, held[r] of another.  May be held itself.
+ *   head_out     : DEVICE int64 [1], written: head plus the blocks given
+ *                  out.  May be head itself.
+ * A request is served unless lens[r] > 16 * max_blocks (it then takes no
+ * block), or it needs blocks and the requests up to and including it need
+ * more than free_blocks still holds.  A request with new tokens that is not
+ * served, new tokens past slot_capacity, and head outside [0, n_free] (then
+ * no block is given out) flag KVTC_FLAG_SPACE.  Other than as said, no
+ * output may overlap an input or another output.
+ * workspace: device scratch of kvtc_paged_assign_workspace_bytes bytes, used
+ * only while the call's work runs on cuda_stream.  It, and slots, cu, head
+ * and head_out, are 8-byte aligned, the int32 arrays 4.
+ * Errors: EINVAL, ESIZE, EALIGN, ENOTSUP, ECUDA.
+ */
+int kvtc_paged_assign(int cuda_device, int R, const int32_t* held,
+                      const int32_t* lens, const int32_t* free_blocks,
+                      int64_t n_free, const int64_t* head,
+                      int32_t* block_table, int max_blocks, int block_size,
+                      int64_t* slots, int64_t slot_capacity, int64_t* cu,
+                      int32_t* held_out, int64_t* head_out, void* workspace,
+                      int64_t workspace_bytes, uint32_t* flags,
+                      void* cuda_stream);
+
+/*
+ * kvtc_paged_append -- write rows of new tokens into paged pools: row i of
+ * stream j goes to row slots[i] of cache[j] seen as [num_blocks * 16][D].
+ *   nstreams : streams (K and V of a layer, or of several layers); >= 0.
+ *   src      : HOST array [nstreams] of device pointers, stream j's rows:
+ *              16-bit elements (bf16 or fp16, copied bit for bit) [N][ld].
+ *   ld       : row stride of every src in elements (>= D, % 8 == 0), so the
+ *              streams may be column slices of one projection's rows.
+ *   slots    : DEVICE int64 [N], as kvtc_paged_assign lists them.  Negative:
+ *              the row is skipped.  At or past num_blocks * 16: skipped, and
+ *              KVTC_FLAG_BLOCK is set.  The others must be distinct: of two
+ *              rows with one slot, either may supply each 16 bytes of it.
+ *   cache    : HOST array [nstreams] of device pointers, each 16-bit
+ *              [num_blocks][16][D]; rows that no slot names are untouched.
+ * D % 8 == 0, 8 <= D <= 8192.  src and cache 16-byte aligned, slots 8.  One
+ * kernel launch per 64 streams.
+ * Errors: EINVAL, ESIZE, EALIGN, ENOTSUP, ECUDA.
+ */
+int kvtc_paged_append(int cuda_device, int nstreams, const void* const* src,
+                      int64_t ld, int64_t N, const int64_t* slots, int D,
+                      int block_size, void* const* cache, int64_t num_blocks,
+                      uint32_t* flags, void* cuda_stream);
+
+/* Device workspace bytes kvtc_paged_attend needs (< 0 on error). */
+int64_t kvtc_paged_attend_workspace_bytes(int cuda_device, int R, int heads,
+                                          int kv_heads, int head_dim);
+
+/*
+ * kvtc_paged_attend -- attention of one new token of each of R requests over
+ * its tokens in a paged K and a paged V pool.  For query head h, which reads
+ * KV head h / (heads / kv_heads), and the request's attended tokens t:
+ *     s_t = scale * q_h . k_t,   lse = ln sum_t e^(s_t),
+ *     out_h = sum_t e^(s_t - lse) v_t.
+ * Attended are tokens 0 .. lens[r] - 1; with window > 0, of those only the
+ * first `sink` and the last `window` (the new token's own row, appended
+ * before the call, is the last one).
+ *   q            : DEVICE [R][q_ld], head h of request r at element
+ *                  r * q_ld + h * head_dim; q_ld % 8 == 0, so q may be a
+ *                  column slice of a fused projection's rows.
+ *   k_cache, v_cache : DEVICE pools [num_blocks][16][kv_heads * head_dim].
+ *   block_table  : DEVICE int32 [R][max_blocks], as for
+ *                  kvtc_decompress_paged; requests may share blocks.
+ *   lens         : DEVICE int32 [R] (negative counts as 0; above
+ *                  16 * max_blocks it counts as that and flags
+ *                  KVTC_FLAG_SPACE).
+ *   out          : DEVICE [R][out_ld], laid out as q; elements between the
+ *                  rows are untouched.
+ *   lse          : DEVICE fp32 [R][heads], or NULL: the log-sum-exp, with
+ *                  which results over disjoint tokens can be joined.
+ * q, the pools and out hold `dtype` elements (enum kvtc_dtype).  Tokens in
+ * blocks whose id is outside [0, num_blocks) are left out and flag
+ * KVTC_FLAG_BLOCK.  Rows of a block that are not attended may hold anything
+ * (infinities and NaN included).  A head whose weights e^(s_t) sum to zero
+ * (no attended token, or every s_t = -inf) gets out = 0, lse = -inf; a NaN
+ * or s_t = +inf in the attended tokens gives NaN.  Products are summed, and
+ * the softmax statistics held, in fp32; out is rounded once.  The result
+ * does not depend on timing, so equal calls on one device give equal bits.
+ *   head_dim 64, 128 or 256; kv_heads * head_dim <= 8192; at most 128 query
+ * heads a KV head; num_blocks < 2^31.  out must not overlap an input.
+ * workspace: device scratch of kvtc_paged_attend_workspace_bytes bytes, used
+ * only while the call's work runs on cuda_stream: calls that may run at the
+ * same time need one each.  q, pools, out and workspace 16-byte aligned,
+ * block_table, lens and lse 4.
+ * Errors: EINVAL, ESIZE, EALIGN, ENOTSUP, ECUDA.
+ */
+int kvtc_paged_attend(int cuda_device, int R, int heads, int kv_heads,
+                      int head_dim, int dtype, const void* q, int64_t q_ld,
+                      const void* k_cache, const void* v_cache,
+                      int64_t num_blocks, int block_size,
+                      const int32_t* block_table, int max_blocks,
+                      const int32_t* lens, int sink, int window, float scale,
+                      void* out, int64_t out_ld, float* lse, void* workspace,
+                      int64_t workspace_bytes, uint32_t* flags,
+                      void* cuda_stream);
 
 /*
  * kvtc_calibrate -- the one-time calibration of technical summary 2A, on

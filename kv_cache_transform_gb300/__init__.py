@@ -8,7 +8,9 @@ mirror the C ABI in ``include/kvtc.h``:
     kvtc_compress, kvtc_decompress, kvtc_decompress_paged,
     kvtc_fields_bound, kvtc_fields_workspace_bytes, kvtc_fields_pack,
     kvtc_fields_unpack, kvtc_decompress_packed, kvtc_device_status,
-    kvtc_launch_count, kvtc_strerror
+    kvtc_paged_assign_workspace_bytes, kvtc_paged_assign,
+    kvtc_paged_append, kvtc_paged_attend_workspace_bytes,
+    kvtc_paged_attend, kvtc_launch_count, kvtc_strerror
 
 Tensor arguments are torch CUDA tensors (or raw integer device addresses);
 ``stream`` defaults to torch's current stream.  There is no CPU fallback: if
@@ -38,6 +40,10 @@ KVTC_FLAG_RANGE = 1
 KVTC_FLAG_TIMEOUT = 2
 KVTC_FLAG_BLOCK = 4
 KVTC_FLAG_FORMAT = 8
+KVTC_FLAG_SPACE = 16
+
+KVTC_DTYPE_BF16 = 0
+KVTC_DTYPE_FP16 = 1
 
 _lib_handle = None
 
@@ -95,6 +101,18 @@ def lib() -> ctypes.CDLL:
         "kvtc_decompress_packed": (c_i, [c_vp, c_i, c_i, c_i, c_vp, c_i64,
                                          c_vp, c_i64, c_pp, c_i64, c_vp,
                                          c_pp]),
+        "kvtc_paged_assign_workspace_bytes": (c_i64, [c_i]),
+        "kvtc_paged_assign": (c_i, [c_i, c_i, c_vp, c_vp, c_vp, c_i64, c_vp,
+                                    c_vp, c_i, c_i, c_vp, c_i64, c_vp, c_vp,
+                                    c_vp, c_vp, c_i64, c_vp, c_vp]),
+        "kvtc_paged_append": (c_i, [c_i, c_i, c_pp, c_i64, c_i64, c_vp, c_i,
+                                    c_i, c_pp, c_i64, c_vp, c_vp]),
+        "kvtc_paged_attend_workspace_bytes": (c_i64, [c_i, c_i, c_i, c_i,
+                                                      c_i]),
+        "kvtc_paged_attend": (c_i, [c_i, c_i, c_i, c_i, c_i, c_i, c_vp,
+                                    c_i64, c_vp, c_vp, c_i64, c_i, c_vp, c_i,
+                                    c_vp, c_i, c_i, ctypes.c_float, c_vp,
+                                    c_i64, c_vp, c_vp, c_i64, c_vp, c_vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -133,10 +151,10 @@ def _ptr_array(xs: Sequence) -> ctypes.Array:
     return arr
 
 
-def _stream(stream) -> int:
+def _stream(stream, device=None) -> int:
     if stream is None:
         import torch
-        return int(torch.cuda.current_stream().cuda_stream)
+        return int(torch.cuda.current_stream(device).cuda_stream)
     if isinstance(stream, int):
         return stream
     return int(stream.cuda_stream)
@@ -320,6 +338,65 @@ def kvtc_fields_unpack(calib: Calib, layer0: int, nlayers: int,
                                     _ptr(dst) or None, dst_bytes,
                                     _stream(stream) or None),
            "kvtc_fields_unpack")
+
+
+def kvtc_paged_assign_workspace_bytes(R: int) -> int:
+    return _check(lib().kvtc_paged_assign_workspace_bytes(R),
+                  "kvtc_paged_assign_workspace_bytes")
+
+
+def kvtc_paged_assign(R: int, held, lens, free_blocks, n_free: int, head,
+                      block_table, max_blocks: int, block_size: int, slots,
+                      slot_capacity: int, cu, held_out, head_out, workspace,
+                      workspace_bytes: int, flags=None, device: int = 0,
+                      stream=None) -> None:
+    """Blocks for R requests that grow from held to lens tokens, and the
+    slots of their new tokens; flags: device uint32 word or None."""
+    _check(lib().kvtc_paged_assign(
+        device, R, _ptr(held) or None, _ptr(lens) or None,
+        _ptr(free_blocks) or None, n_free, _ptr(head) or None,
+        _ptr(block_table) or None, max_blocks, block_size,
+        _ptr(slots) or None, slot_capacity, _ptr(cu) or None,
+        _ptr(held_out) or None, _ptr(head_out) or None,
+        _ptr(workspace) or None, workspace_bytes, _ptr(flags) or None,
+        _stream(stream, device) or None), "kvtc_paged_assign")
+
+
+def kvtc_paged_append(src: Sequence, ld: int, N: int, slots, D: int,
+                      block_size: int, cache: Sequence, num_blocks: int,
+                      flags=None, device: int = 0, stream=None) -> None:
+    """Rows src[j] [N][ld] into the pools cache[j] at row slots[i] each."""
+    if len(src) != len(cache):
+        raise ValueError("src and cache differ in length")
+    _check(lib().kvtc_paged_append(
+        device, len(src), _ptr_array(src), ld, N, _ptr(slots) or None, D,
+        block_size, _ptr_array(cache), num_blocks, _ptr(flags) or None,
+        _stream(stream, device) or None), "kvtc_paged_append")
+
+
+def kvtc_paged_attend_workspace_bytes(R: int, heads: int, kv_heads: int,
+                                      head_dim: int, device: int = 0) -> int:
+    return _check(lib().kvtc_paged_attend_workspace_bytes(
+        device, R, heads, kv_heads, head_dim),
+        "kvtc_paged_attend_workspace_bytes")
+
+
+def kvtc_paged_attend(R: int, heads: int, kv_heads: int, head_dim: int,
+                      dtype: int, q, q_ld: int, k_cache, v_cache,
+                      num_blocks: int, block_size: int, block_table,
+                      max_blocks: int, lens, sink: int, window: int,
+                      scale: float, out, out_ld: int, lse, workspace,
+                      workspace_bytes: int, flags=None, device: int = 0,
+                      stream=None) -> None:
+    """One new token's attention per request over its tokens in the pools;
+    lse: device fp32 [R][heads] or None."""
+    _check(lib().kvtc_paged_attend(
+        device, R, heads, kv_heads, head_dim, dtype, _ptr(q) or None, q_ld,
+        _ptr(k_cache) or None, _ptr(v_cache) or None, num_blocks, block_size,
+        _ptr(block_table) or None, max_blocks, _ptr(lens) or None, sink,
+        window, scale, _ptr(out) or None, out_ld, _ptr(lse) or None,
+        _ptr(workspace) or None, workspace_bytes, _ptr(flags) or None,
+        _stream(stream, device) or None), "kvtc_paged_attend")
 
 
 def kvtc_wait_selftest(calib: Calib, limit_us: int, stream=None) -> None:

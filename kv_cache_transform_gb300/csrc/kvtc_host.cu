@@ -1,7 +1,6 @@
 // Host side of the C ABI declared in include/kvtc.h: calibration blob
 // parsing, device operand preparation, argument validation and launches.
 #include <cuda_fp16.h>
-#include <cudaTypedefs.h>
 
 #include <algorithm>
 #include <atomic>
@@ -16,6 +15,7 @@
 #include <vector>
 
 #include "../../include/kvtc.h"
+#include "kvtc_hostutil.cuh"
 #include "kvtc_internal.cuh"
 
 using namespace kvtc;
@@ -107,20 +107,6 @@ struct Reader {
   }
 };
 
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000,
-                                         cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-  });
-  return fn;
-}
-
 // K-block-major operand [nblk][rows][64] (16-bit elements): 3-D map
 // {64, rows, nblk}, box {64, box_rows, box_blk}, 128-byte swizzle; a box
 // lands in shared memory as box_blk [box_rows][64] tiles.
@@ -189,24 +175,7 @@ bool encode_pool_3d(CUtensorMap* m, const void* base, uint64_t D,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-struct DeviceGuard {
-  int prev = -1;
-  bool ok = true;
-  explicit DeviceGuard(int dev) {
-    if (cudaGetDevice(&prev) != cudaSuccess) prev = -1;
-    if (prev != dev) ok = cudaSetDevice(dev) == cudaSuccess;
-  }
-  ~DeviceGuard() {
-    int cur = -1;
-    if (prev >= 0 && cudaGetDevice(&cur) == cudaSuccess && cur != prev)
-      cudaSetDevice(prev);
-  }
-};
-
 inline int64_t align_up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
-inline bool aligned16(const void* p) {
-  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0;
-}
 
 }  // namespace
 
