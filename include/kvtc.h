@@ -427,7 +427,7 @@ int64_t kvtc_paged_attend_workspace_bytes(int cuda_device, int R, int heads,
  * (infinities and NaN included).  A head whose weights e^(s_t) sum to zero
  * (no attended token, or every s_t = -inf) gets out = 0, lse = -inf; a NaN
  * or s_t = +inf in the attended tokens gives NaN, an infinity in V an
- * infinity (or NaN, where its weight is below 2^-24).  Products are summed,
+ * infinity (or NaN, where its weight is below 2^-20).  Products are summed,
  * and the softmax statistics held, in fp32; out is rounded once.  The result
  * does not depend on timing, so equal calls on one device give equal bits.
  *   head_dim 64, 128 or 256; kv_heads * head_dim <= 8192; at most 128 query

@@ -141,7 +141,7 @@ def _ptr(x) -> int:
         return 0
     if isinstance(x, int):
         return x
-    return int(x.data_ptr())
+    return x.data_ptr()
 
 
 def _ptr_array(xs: Sequence) -> ctypes.Array:
@@ -151,13 +151,32 @@ def _ptr_array(xs: Sequence) -> ctypes.Array:
     return arr
 
 
-def _stream(stream, device=None) -> int:
+def _stream(stream) -> int:
     if stream is None:
         import torch
-        return int(torch.cuda.current_stream(device).cuda_stream)
+        return int(torch.cuda.current_stream().cuda_stream)
     if isinstance(stream, int):
         return stream
     return int(stream.cuda_stream)
+
+
+_raw_stream = None
+
+
+def _stream_on(stream, device: int) -> int:
+    """The given stream, or torch's current one on `device`: the form of the
+    per-token calls, which come once a layer and cost what their Python
+    costs (torch's raw query takes 0.1 us, current_stream() 1 to 3)."""
+    global _raw_stream
+    if stream is not None:
+        return stream if isinstance(stream, int) else stream.cuda_stream
+    if _raw_stream is None:
+        import torch
+        torch.cuda.current_stream(device)       # CUDA is initialised
+        _raw_stream = getattr(
+            torch._C, "_cuda_getCurrentRawStream",
+            lambda d: torch.cuda.current_stream(d).cuda_stream)
+    return _raw_stream(device)
 
 
 class Calib:
@@ -353,13 +372,13 @@ def kvtc_paged_assign(R: int, held, lens, free_blocks, n_free: int, head,
     """Blocks for R requests that grow from held to lens tokens, and the
     slots of their new tokens; flags: device uint32 word or None."""
     _check(lib().kvtc_paged_assign(
-        device, R, _ptr(held) or None, _ptr(lens) or None,
-        _ptr(free_blocks) or None, n_free, _ptr(head) or None,
-        _ptr(block_table) or None, max_blocks, block_size,
-        _ptr(slots) or None, slot_capacity, _ptr(cu) or None,
-        _ptr(held_out) or None, _ptr(head_out) or None,
-        _ptr(workspace) or None, workspace_bytes, _ptr(flags) or None,
-        _stream(stream, device) or None), "kvtc_paged_assign")
+        device, R, _ptr(held), _ptr(lens),
+        _ptr(free_blocks), n_free, _ptr(head),
+        _ptr(block_table), max_blocks, block_size,
+        _ptr(slots), slot_capacity, _ptr(cu),
+        _ptr(held_out), _ptr(head_out),
+        _ptr(workspace), workspace_bytes, _ptr(flags),
+        _stream_on(stream, device)), "kvtc_paged_assign")
 
 
 def kvtc_paged_append(src: Sequence, ld: int, N: int, slots, D: int,
@@ -369,9 +388,9 @@ def kvtc_paged_append(src: Sequence, ld: int, N: int, slots, D: int,
     if len(src) != len(cache):
         raise ValueError("src and cache differ in length")
     _check(lib().kvtc_paged_append(
-        device, len(src), _ptr_array(src), ld, N, _ptr(slots) or None, D,
-        block_size, _ptr_array(cache), num_blocks, _ptr(flags) or None,
-        _stream(stream, device) or None), "kvtc_paged_append")
+        device, len(src), _ptr_array(src), ld, N, _ptr(slots), D,
+        block_size, _ptr_array(cache), num_blocks, _ptr(flags),
+        _stream_on(stream, device)), "kvtc_paged_append")
 
 
 def kvtc_paged_attend_workspace_bytes(R: int, heads: int, kv_heads: int,
@@ -391,12 +410,12 @@ def kvtc_paged_attend(R: int, heads: int, kv_heads: int, head_dim: int,
     """One new token's attention per request over its tokens in the pools;
     lse: device fp32 [R][heads] or None."""
     _check(lib().kvtc_paged_attend(
-        device, R, heads, kv_heads, head_dim, dtype, _ptr(q) or None, q_ld,
-        _ptr(k_cache) or None, _ptr(v_cache) or None, num_blocks, block_size,
-        _ptr(block_table) or None, max_blocks, _ptr(lens) or None, sink,
-        window, scale, _ptr(out) or None, out_ld, _ptr(lse) or None,
-        _ptr(workspace) or None, workspace_bytes, _ptr(flags) or None,
-        _stream(stream, device) or None), "kvtc_paged_attend")
+        device, R, heads, kv_heads, head_dim, dtype, _ptr(q), q_ld,
+        _ptr(k_cache), _ptr(v_cache), num_blocks, block_size,
+        _ptr(block_table), max_blocks, _ptr(lens), sink,
+        window, scale, _ptr(out), out_ld, _ptr(lse),
+        _ptr(workspace), workspace_bytes, _ptr(flags),
+        _stream_on(stream, device)), "kvtc_paged_attend")
 
 
 def kvtc_wait_selftest(calib: Calib, limit_us: int, stream=None) -> None:

@@ -1,21 +1,26 @@
 // Attention of one new token per request over paged K and V pools.
 //
 // For a query head, s_t = scale q.k_t over the attended tokens.  With a
-// running maximum m, l = sum 2^(s_t - m) and o = sum 2^(s_t - m) v_t (s in
-// units of log2) are multiplied by 2^(m_old - m_new) when m grows, so K and
-// V are read once; partial results of disjoint tokens join the same way:
+// running reference m near the maximum, l = sum 2^(s_t - m) and o = sum
+// 2^(s_t - m) v_t (s in units of log2) are multiplied by 2^(m_old - m_new)
+// when m grows, so K and V are read once; partial results of disjoint tokens join the same way:
 //     m = max m_i,  l = sum l_i 2^(m_i - m),  o = sum o_i 2^(m_i - m),
 // and out = o / l, lse = (m + log2 l) ln 2.
 //
 // Work.  A request's tokens fall into pages of 16; an item is (request, KV
-// head, tile of query heads), a unit one page of an item, and all units of
-// the call, in order, are dealt out to the grid's warps in equal runs: the
-// kernel reads HBM at the same rate on every SM whatever the lengths are.
-// The lengths are on the device, so each block sums them itself.  A warp
-// writes an item that lies inside its run; parts of items are joined in
-// three steps, each in a fixed order (equal calls give equal bits): the
-// warps of a block through shared memory, then attend_join_kernel, launched
-// behind, over the blocks.
+// head, tile of query heads), a unit one page of an item.  A warp takes a run
+// of consecutive units, and writes an item that lies inside its run; of
+// others it leaves a part.  The parts are joined in a fixed order (equal
+// calls give equal bits), in one of two ways:
+//   many items   all units of the call are dealt out to the warps of one
+//                block per SM in equal runs, so that every SM reads at the
+//                same rate whatever the lengths are (they are on the device:
+//                each block sums them itself).  Parts are joined by the next
+//                warp, by the block, and across blocks by attend_join_kernel
+//                behind.
+//   few items    a cluster of blocks takes one item and joins its parts
+//                through distributed shared memory: one launch, and no
+//                second round through L2.
 //
 // Inside a warp.  Each warp feeds itself: lane j of a batch of 32 units
 // looks up its page's id and issues the two TMA boxes (16 tokens x head_dim
@@ -33,6 +38,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -50,17 +56,23 @@ constexpr int kBlock = 16;           // tokens per pool block (a page)
 constexpr int kMaxReq = 4096;        // requests per call
 constexpr int kMaxGroup = 128;       // query heads per KV head
 constexpr int kCtas = 152;           // one block per SM
-constexpr int kRingBytes = 196608;   // shared memory for pages in flight
+constexpr int kLeast = 2;            // units per warp
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kSlack = 6.f;        // log2; see the reference in the loop
 
-// Warps per block: the ring holds three pages a warp of head_dim 256, three
-// of 128 or six of 64.
-__host__ __device__ constexpr int warps_of(int hd) { return hd == 256 ? 4 : 8; }
-__host__ __device__ constexpr int stage_bytes(int hd) { return hd * 64; }
-__host__ __device__ constexpr int stages_of(int hd) {
-  return kRingBytes / (warps_of(hd) * stage_bytes(hd));
+// Warps per block and pages in a warp's ring, for nt tiles of eight query
+// heads per warp: what fits 227 KB with the parts kept beside the ring, and
+// the registers.
+__host__ __device__ constexpr int warps_of(int hd, int nt) {
+  return hd == 64    ? (nt == 4 ? 8 : 12)
+         : hd == 128 ? (nt == 1 ? 10 : nt == 2 ? 8 : 5)
+                     : (nt == 1 ? 5 : 4);
 }
+__host__ __device__ constexpr int stages_of(int hd, int nt) {
+  return hd == 64 ? (nt == 4 ? 4 : 3) : hd == 128 && nt == 4 ? 3 : 2;
+}
+__host__ __device__ constexpr int stage_bytes(int hd) { return hd * 64; }
 // Floats of a partial result of nt x 8 query heads: o in fragment order
 // ([channel tile][head tile][lane][4]), then m and l per head.
 __host__ __device__ constexpr int slot_floats(int hd, int nt) {
@@ -69,7 +81,7 @@ __host__ __device__ constexpr int slot_floats(int hd, int nt) {
 
 // Where the join finds the parts of an item that began in a block and did
 // not end there; r < 0: there is none.
-struct JoinDesc {
+struct __align__(16) JoinDesc {
   int32_t r, sub, last_cta, pad;
 };
 
@@ -83,8 +95,8 @@ struct AttendParams {
   float* lse;
   unsigned* flags;
   JoinDesc* desc;           // [kCtas]
-  float* cta_slots;         // [kCtas][2] parts that cross blocks
-  float* warp_slots;        // [kCtas * warps] parts that end inside a run
+  float* cta_slots;         // [kCtas][2] parts that cross blocks: 0 of an
+                            // item begun in an earlier block, 1 in this one
   int64_t q_ld, out_ld, num_blocks;
   float scale_log2;
   int32_t R, heads, kv_heads, max_blocks, sink, window;
@@ -92,6 +104,11 @@ struct AttendParams {
 };
 
 // ------------------------------------------------------------ PTX wrappers
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t n;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(n));
+  return n;
+}
 __device__ __forceinline__ void tma_load_page(uint32_t smem_dst,
                                               const void* tmap, int32_t slab,
                                               int32_t block, uint64_t* bar) {
@@ -129,14 +146,49 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return r;
 }
 
+// Loads from this block's shared memory, or from that of the cluster's blocks
+// (which takes several times as long, for an own address too).  Not volatile:
+// what they read was written before the caller's last barrier.
+template <bool across>
+__device__ __forceinline__ float2 lds2(uint32_t addr) {
+  float2 v;
+  if (across)
+    asm("ld.shared::cluster.v2.f32 {%0,%1}, [%2];"
+        : "=f"(v.x), "=f"(v.y)
+        : "r"(addr));
+  else
+    asm("ld.shared.v2.f32 {%0,%1}, [%2];"
+        : "=f"(v.x), "=f"(v.y)
+        : "r"(addr));
+  return v;
+}
+template <bool across>
+__device__ __forceinline__ float4 lds4(uint32_t addr) {
+  float4 v;
+  if (across)
+    asm("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+        : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+        : "r"(addr));
+  else
+    asm("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
+        : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+        : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ float rcp_fast(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 // The two element types: conversion, packing (a in the low half) and
 // D (16 x 8, fp32) += A (16 x 16) B (16 x 8).
 //
 // A weight w > 0 enters the product with V as hi + lo, hi = w kBelow cut to
 // 16 bits and lo = w - hi (exact) rounded to 16 bits: w to 2^-15, and both
 // terms positive, so that an infinite v gives an infinity and not inf - inf
-// or 0 inf.  fp16 holds numbers from 2^-24: there weights are formed 2^15
-// times as large, and what is lost lies 2^-39 below the largest.
+// or 0 inf.  fp16 holds numbers from 2^-24: there weights are formed 2^9
+// times as large, and what is lost lies 2^-33 below the largest.
 template <class T>
 struct Elem;
 template <>
@@ -167,7 +219,7 @@ struct Elem<__nv_bfloat16> {
 template <>
 struct Elem<__half> {
   static constexpr float kBelow = 1.f - 0x1p-12f;
-  static constexpr float kShift = 15.f;   // weights up to 2^15
+  static constexpr float kShift = 9.f;    // weights up to 2^15
   static __device__ __forceinline__ uint32_t pack_down(float a, float b) {
     uint32_t r;
     asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
@@ -197,6 +249,7 @@ struct Elem<__half> {
 // with none still has one unit, which writes its empty result.
 struct Span {
   int32_t len, units, front, gap;
+  bool hole;      // tokens between the sink and the window are left out
 };
 __device__ __forceinline__ Span span_of(const AttendParams& p, int r) {
   Span s;
@@ -206,13 +259,64 @@ __device__ __forceinline__ Span span_of(const AttendParams& p, int r) {
   const int32_t all = (int32_t)(((int64_t)s.len + kBlock - 1) / kBlock);
   s.front = all;
   s.gap = 0;
-  if (p.window && (int64_t)p.sink + p.window < s.len) {
+  s.hole = p.window && (int64_t)p.sink + p.window < s.len;
+  if (s.hole) {
     s.front = (p.sink + kBlock - 1) / kBlock;     // sink < len: no overflow
     s.gap = max((s.len - p.window) / kBlock - s.front, 0);
   }
   s.units = max(all - s.gap, 1);
   return s;
 }
+
+// a / b and the remainder, for a quotient below 2^20 (a float quotient is
+// then off by less than one): a 64-bit division is a hundred instructions.
+__device__ __forceinline__ int small_quotient(int64_t a, int32_t b,
+                                              int32_t* rest) {
+  int q = (int)((float)a / (float)b);
+  int64_t left = a - (int64_t)q * b;
+  if (left < 0) {
+    --q;
+    left += b;
+  } else if (left >= b) {
+    ++q;
+    left -= b;
+  }
+  *rest = (int32_t)left;
+  return q;
+}
+// `total` units in order over the warps of the first `ctas` of `most` blocks:
+// the first `more` warps take least + 1 units, the others `least`.  With few
+// units, blocks are left out until every warp has kLeast of them: what
+// reading on more SMs saves, the join of more blocks costs.
+template <int W>
+struct Deal {
+  int64_t least;
+  int32_t more, ctas;
+  __device__ __forceinline__ Deal(int64_t total, int most) {
+    if (most == kCtas && total >= (int64_t)kCtas * W * kLeast) {
+      ctas = kCtas;
+      least = total / (kCtas * W);       // by a constant
+    } else {
+      // (a cluster's item has less than 2^28 units)
+      ctas = max(1, min(most, (int32_t)total / (W * kLeast)));
+      least = (uint32_t)total / (uint32_t)(ctas * W);
+    }
+    more = (int32_t)(total - least * (ctas * W));
+  }
+  __device__ __forceinline__ int64_t begin(int worker) const {
+    return worker * least + min(worker, more);
+  }
+  // The block that holds a unit (the whole warp asks).
+  __device__ __forceinline__ int cta_of(int64_t unit) const {
+    int upto = 0;
+    for (int i = 0; i < ctas; i += 32) {
+      const int c = i + (int)lane_id();
+      upto += __popc(__ballot_sync(0xFFFFFFFFu,
+                                   c < ctas && begin(c * W) <= unit));
+    }
+    return upto - 1;
+  }
+};
 
 // What a warp knows of a page in its ring.
 struct __align__(16) UnitMeta {
@@ -224,129 +328,102 @@ struct __align__(16) UnitMeta {
 constexpr uint32_t kFirst = 1u << 31;   // first unit of its item
 constexpr uint32_t kLast = 1u << 30;    // last unit of its item
 constexpr uint32_t kSkip = 1u << 29;    // no page (bad id, empty request)
-constexpr uint32_t kSubMask = kSkip - 1;
+constexpr uint32_t kWhole = 1u << 28;   // all 16 tokens are attended
+constexpr uint32_t kSubMask = kWhole - 1;
 
-// A part of an item left by a warp: entry 0 of a warp holds the part of an
-// item that ended in its run but began before it, entry 1 of one that goes
-// on behind it.
-struct __align__(8) PartRec {
-  int64_t begin;    // first unit of the item, where kFirst is set
-  int32_t r;
+// A part of an item left by a warp: entry 0 of a warp is of an item that
+// ended in its run but began before it (in the slot beside the ring), entry
+// 1 of one that goes on behind it (in the ring, when every page is read).
+struct __align__(16) PartRec {
+  int64_t begin;    // first unit of the item
+  int32_t r;        // < 0: there is no such part
   uint32_t sub;     // kFirst: begun here; kLast: ended here
-  int32_t present;  // 0, 1: in the warp's ring, 2: in its workspace slot
-  int32_t pad;
 };
 
-template <int HD>
+template <int HD, int NT>
 struct Smem {
-  static constexpr int W = warps_of(HD), S = stages_of(HD);
-  static constexpr int kBars = kRingBytes;
-  static constexpr int kMeta = kBars + W * S * 8;
-  static constexpr int kPrefix = kMeta + W * S * 16;
-  static constexpr int kRecs = kPrefix + W * 32 * 8;
-  static constexpr int kMisc = kRecs + W * 2 * (int)sizeof(PartRec);
-  static constexpr int kBytes = kMisc + 128 + 1024;  // + alignment slack
+  static constexpr int W = warps_of(HD, NT), S = stages_of(HD, NT);
+  static constexpr int kSlot = 4 * slot_floats(HD, NT);
+  static_assert(2 * W <= 32, "a warp's lanes hold the block's part records");
+  static_assert(S * stage_bytes(HD) >= kSlot, "a part fits a warp's ring");
+  static constexpr int kParts = W * S * stage_bytes(HD);
+  static constexpr int kBlockPart = kParts + W * kSlot;
+  static constexpr int kRecs = kBlockPart + kSlot;
+  static constexpr int kMeta = kRecs + W * 2 * (int)sizeof(PartRec);
+  static constexpr int kBars = kMeta + W * S * (int)sizeof(UnitMeta);
+  static constexpr int kPrefix = kBars + W * S * 8;
+  static constexpr int kMisc = kPrefix + W * 32 * 8;
+  static constexpr int kBytes = kMisc + 320 + 1024;  // + alignment slack
+  static_assert(kBytes <= 232448, "shared memory of a block");
 };
 
-// Heads of a column pair of a fragment: lane's columns 2 (lane & 3), + 1.
-// Writes the rows of a tile pair's transposed accumulators: dims
-// mt * 16 + {0, 8}, eight heads, scaled by inv (per column).
-template <class T, int HD>
-__device__ __forceinline__ void store_out_frag(const AttendParams& p, int r,
-                                               int head0, int rows, int nt,
-                                               int mt, const float (&c)[4],
-                                               float inv0, float inv1) {
-  const int lane = (int)lane_id(), gid = lane >> 2, tig = lane & 3;
-  // the transpose puts head gid, channels 2 tig and 2 tig + 1 in a lane
-  const uint32_t lo = transpose8(Elem<T>::pack(c[0] * inv0, c[1] * inv1));
-  const uint32_t hi = transpose8(Elem<T>::pack(c[2] * inv0, c[3] * inv1));
-  if (nt * 8 + gid < rows) {
-    T* o = static_cast<T*>(p.out) + (int64_t)r * p.out_ld +
-           (int64_t)(head0 + nt * 8 + gid) * HD + mt * 16 + tig * 2;
-    *reinterpret_cast<uint32_t*>(o) = lo;
-    *reinterpret_cast<uint32_t*>(o + 8) = hi;
-  }
-}
-
-__device__ __forceinline__ float inverse(float l) {
-  return l == 0.f ? 0.f : 1.f / l;
-}
-__device__ __forceinline__ float lse_of(float m, float l, float shift) {
-  return l == 0.f ? -INFINITY : (m + (log2f(l) - shift)) * kLn2;
-}
 // What exponents are taken relative to: m, or 0 where no score is finite
 // (so that 2^(-inf - base) is 0 and not NaN).
 __device__ __forceinline__ float base_of(float m) {
   return m == -INFINITY ? 0.f : m;
 }
-
 __device__ __forceinline__ void head_range(const AttendParams& p,
                                            uint32_t sub, int* head0,
                                            int* rows) {
-  const int j = (int)sub / p.tiles, t = (int)sub - j * p.tiles;
+  const int j = p.tiles == 1 ? (int)sub : (int)sub / p.tiles;
+  const int t = (int)sub - j * p.tiles;
   *head0 = j * p.group + t * p.tile_heads;
   *rows = min(p.tile_heads, p.group - t * p.tile_heads);
 }
 
-// Sum of `n` parts (part(i): its slot) at one fragment position: o, and the
-// joined m and l of its two columns.
-template <int HD, int NT, class F>
-__device__ __forceinline__ void join_parts(int n, int tile, F part,
-                                           float (&o)[4], float (&m)[2],
-                                           float (&l)[2]) {
-  const int lane = (int)lane_id();
-  const int col = (tile % NT) * 8 + (lane & 3) * 2;
-  m[0] = m[1] = -INFINITY;
-  for (int i = 0; i < n; ++i) {
-    const float2 mi = *reinterpret_cast<const float2*>(
-        part(i) + NT * 8 * HD + col);
-    m[0] = fmaxf(m[0], mi.x);
-    m[1] = fmaxf(m[1], mi.y);
+// Where an item's result goes.
+template <class T>
+struct Target {
+  T* out;           // its first head
+  float* lse;       // or null
+  int rows;         // heads
+  __device__ __forceinline__ Target(T* out_, float* lse_, int rows_)
+      : out(out_), lse(lse_), rows(rows_) {}
+  __device__ __forceinline__ Target(const AttendParams& p, int r,
+                                    uint32_t sub, int hd) {
+    int head0;
+    head_range(p, sub, &head0, &rows);
+    out = static_cast<T*>(p.out) + (int64_t)r * p.out_ld +
+          (int64_t)head0 * hd;
+    lse = p.lse ? p.lse + (int64_t)r * p.heads + head0 : nullptr;
   }
-  const float b0 = base_of(m[0]), b1 = base_of(m[1]);
-  l[0] = l[1] = 0.f;
-  o[0] = o[1] = o[2] = o[3] = 0.f;
-  for (int i = 0; i < n; ++i) {
-    const float* s = part(i);
-    const float2 mi = *reinterpret_cast<const float2*>(s + NT * 8 * HD + col);
-    const float2 li =
-        *reinterpret_cast<const float2*>(s + NT * 8 * (HD + 1) + col);
-    const float4 x = *reinterpret_cast<const float4*>(s + (tile * 32 + lane) *
-                                                              4);
-    const float f0 = exp2_fast(mi.x - b0), f1 = exp2_fast(mi.y - b1);
-    l[0] += li.x * f0;
-    l[1] += li.y * f1;
-    o[0] += x.x * f0;
-    o[1] += x.y * f1;
-    o[2] += x.z * f0;
-    o[3] += x.w * f1;
-  }
-}
-
-// Final values of an item from joined fragments: out and lse.
-template <class T, int HD, int NT>
-__device__ __forceinline__ void finish_item(const AttendParams& p, int r,
-                                            uint32_t sub, int tile,
-                                            const float (&o)[4],
-                                            const float (&m)[2],
-                                            const float (&l)[2]) {
-  const int lane = (int)lane_id(), gid = lane >> 2, tig = lane & 3;
-  const int mt = tile / NT, nt = tile % NT;
-  int head0, rows;
-  head_range(p, sub, &head0, &rows);
-  store_out_frag<T, HD>(p, r, head0, rows, nt, mt, o, inverse(l[0]),
-                        inverse(l[1]));
-  if (p.lse && mt == 0 && gid == 0) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int h = nt * 8 + tig * 2 + i;
-      if (h < rows)
-        p.lse[(int64_t)r * p.heads + head0 + h] = lse_of(m[i], l[i], Elem<T>::kShift);
+  // Lane: columns (heads) 2 (lane & 3) and + 1 of head tile nt.  The
+  // accumulators o of channel tile mt (rows lane / 4 and + 8) times inv.
+  template <int HD>
+  __device__ __forceinline__ void store(int nt, int mt, const float (&o)[4],
+                                        const float (&inv)[2]) const {
+    const int lane = (int)lane_id(), gid = lane >> 2, tig = lane & 3;
+    // the transpose puts head gid, channels 2 tig and 2 tig + 1 in a lane
+    const uint32_t lo =
+        transpose8(Elem<T>::pack(o[0] * inv[0], o[1] * inv[1]));
+    const uint32_t hi =
+        transpose8(Elem<T>::pack(o[2] * inv[0], o[3] * inv[1]));
+    if (nt * 8 + gid < rows) {
+      T* to = out + (nt * 8 + gid) * HD + mt * 16 + tig * 2;
+      *reinterpret_cast<uint32_t*>(to) = lo;
+      *reinterpret_cast<uint32_t*>(to + 8) = hi;
     }
   }
+  __device__ __forceinline__ void store_lse(int nt, const float (&m)[2],
+                                            const float (&l)[2]) const {
+    const int lane = (int)lane_id(), h = nt * 8 + lane * 2;
+    if (!lse || lane >= 4) return;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (h + i < rows)
+        lse[h + i] = l[i] == 0.f
+                         ? -INFINITY
+                         : (m[i] + (log2f(l[i]) - Elem<T>::kShift)) * kLn2;
+  }
+};
+// 1 / l; 0 for the empty sum.  (l >= 1 otherwise: some token's weight was 1
+// when the reference was its score, and a part's factor of 2^-126 or less
+// leaves nothing of it beside the largest part.)
+__device__ __forceinline__ float inverse(float l) {
+  return l == 0.f ? 0.f : rcp_fast(l);
 }
 
-// A joined part as a slot.
+// A part as a slot.
 template <int HD, int NT>
 __device__ __forceinline__ void store_part(float* slot, int tile,
                                            const float (&o)[4],
@@ -364,12 +441,82 @@ __device__ __forceinline__ void store_part(float* slot, int tile,
   }
 }
 
+// Join n parts in shared memory, part i at at(i) (of this block or `across`
+// the cluster's), at fragment tiles tile, tile + step, ...: into the result,
+// or where `to` is given into a slot.  kBatch parts are loaded at once; more
+// would only lengthen code that runs once a call and has to be fetched.  The
+// sums are spelled out so that the same two parts give the same bits here and
+// where a warp joins them in its registers.
+template <class T, int HD, int NT, int kBatch, bool across, class F>
+__device__ __forceinline__ void join_parts(int n, F at,
+                                           const Target<T>& target, float* to,
+                                           int tile, int step) {
+  const int lane = (int)lane_id();
+#pragma unroll 1
+  for (; tile < HD / 16 * NT; tile += step) {
+    const int nt = tile % NT;
+    const uint32_t stat = (NT * 8 * HD + nt * 8 + (lane & 3) * 2) * 4;
+    const uint32_t frag = (tile * 32 + lane) * 16;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    float o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+    for (int i0 = 0; i0 < n; i0 += kBatch) {
+      float2 mi[kBatch], li[kBatch];
+      float4 oi[kBatch];
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        const uint32_t slot = at(min(i0 + b, n - 1));
+        mi[b] = lds2<across>(slot + stat);
+        li[b] = lds2<across>(slot + stat + NT * 32);
+        oi[b] = lds4<across>(slot + frag);
+      }
+      float mn[2] = {m[0], m[1]};
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {    // (the last one may come twice)
+        mn[0] = fmaxf(mn[0], mi[b].x);
+        mn[1] = fmaxf(mn[1], mi[b].y);
+      }
+      const float base[2] = {base_of(mn[0]), base_of(mn[1])};
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const float f = exp2_fast(m[c] - base[c]);
+        m[c] = mn[c];
+        l[c] = __fmul_rn(l[c], f);
+        o[c] = __fmul_rn(o[c], f);
+        o[c + 2] = __fmul_rn(o[c + 2], f);
+      }
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        const bool in = i0 + b < n;
+        const float f0 = in ? exp2_fast(mi[b].x - base[0]) : 0.f;
+        const float f1 = in ? exp2_fast(mi[b].y - base[1]) : 0.f;
+        if (in) {
+          l[0] = __fmaf_rn(li[b].x, f0, l[0]);
+          l[1] = __fmaf_rn(li[b].y, f1, l[1]);
+          o[0] = __fmaf_rn(oi[b].x, f0, o[0]);
+          o[1] = __fmaf_rn(oi[b].y, f1, o[1]);
+          o[2] = __fmaf_rn(oi[b].z, f0, o[2]);
+          o[3] = __fmaf_rn(oi[b].w, f1, o[3]);
+        }
+      }
+    }
+    if (to) {
+      store_part<HD, NT>(to, tile, o, m, l);
+    } else {
+      const float inv[2] = {inverse(l[0]), inverse(l[1])};
+      target.template store<HD>(nt, tile / NT, o, inv);
+      if (tile < NT) target.store_lse(nt, m, l);
+    }
+  }
+}
+
 // ------------------------------------------------------------------ kernel
-// NT: tiles of eight query heads that a warp keeps.
-template <class T, int HD, int NT>
-__global__ void __launch_bounds__(warps_of(HD) * 32, 1)
+// NT: tiles of eight query heads that a warp keeps.  kCluster: a cluster of
+// blocks takes one item, else all items are dealt out to kCtas blocks.
+template <class T, int HD, int NT, bool kCluster>
+__global__ void __launch_bounds__(warps_of(HD, NT) * 32, 1)
     attend_kernel(const __grid_constant__ AttendParams p) {
-  using L = Smem<HD>;
+  using L = Smem<HD, NT>;
   constexpr int W = L::W, S = L::S, kThreads = W * 32;
   constexpr int MT = HD / 16;               // channel tiles of 16
   constexpr int kPage = HD * 32;            // bytes of one page of K or V
@@ -381,70 +528,94 @@ __global__ void __launch_bounds__(warps_of(HD) * 32, 1)
   UnitMeta* metas = reinterpret_cast<UnitMeta*>(smem + L::kMeta) + warp * S;
   int64_t* prefix = reinterpret_cast<int64_t*>(smem + L::kPrefix);
   PartRec* recs = reinterpret_cast<PartRec*>(smem + L::kRecs);
+  float* ring_slot = reinterpret_cast<float*>(smem + warp * S *
+                                                         stage_bytes(HD));
+  float* own_slot = reinterpret_cast<float*>(smem + L::kParts +
+                                             warp * L::kSlot);
   int64_t* warp_sums = reinterpret_cast<int64_t*>(smem + L::kMisc);
   volatile int* abort_flag =
-      reinterpret_cast<volatile int*>(smem + L::kMisc + 64);
+      reinterpret_cast<volatile int*>(smem + L::kMisc + 128);
+  volatile int* heads_ready =      // [W] entry 0 of the warp is complete
+      reinterpret_cast<volatile int*>(smem + L::kMisc + 192);
   const int items = p.kv_heads * p.tiles;   // per request
 
+  // the next launch's blocks may take their places: they wait for this grid
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (lane < S) mbar_init(bars + lane, 1);
   if (lane == 0) {
-    recs[warp * 2].present = recs[warp * 2 + 1].present = 0;
+    recs[warp * 2].r = recs[warp * 2 + 1].r = -1;
+    heads_ready[warp] = 0;
     prefetch_tmap(&p.tm_k);
     prefetch_tmap(&p.tm_v);
   }
   if (tid == 0) *abort_flag = 0;
   fence_mbar_init();
-
-  // Units of the requests before each thread's run of requests.
-  const int per = (p.R + kThreads - 1) / kThreads;
-  int64_t sum = 0;
-  for (int i = 0; i < per; ++i) {
-    const int r = tid * per + i;
-    if (r >= p.R) break;
-    sum += span_of(p, r).units;
-    if (p.flags && blockIdx.x == 0 &&
-        __ldg(p.lens + r) > (int64_t)p.max_blocks * kBlock)
-      atomicOr(p.flags, KVTC_FLAG_SPACE);
-  }
-  int64_t upto = sum;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int64_t o = __shfl_up_sync(0xFFFFFFFFu, upto, d);
-    if (lane >= d) upto += o;
-  }
-  if (lane == 31) warp_sums[warp] = upto;
-  __syncthreads();
-  int64_t total = 0;
-#pragma unroll
-  for (int w = 0; w < W; ++w) {
-    if (w < warp) upto += warp_sums[w];
-    total += warp_sums[w];
-  }
-  prefix[tid] = (upto - sum) * items;
-  total *= items;
-  __syncthreads();
+  // everything this call reads may come from the launch before it
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 
   // This warp's run of units, and the request that holds its first one.
-  // Fewer units than warps leave blocks or warps out, so that every worker
-  // has a unit and the parts of an item lie in consecutive blocks.
-  const int64_t ctas = min(total, (int64_t)kCtas);
-  const int64_t active = min(total / ctas, (int64_t)W);
-  const int64_t workers = ctas * active;
-  const int64_t worker = blockIdx.x * active + warp;
-  const bool works = blockIdx.x < ctas && warp < active;
-  const int64_t u0 = works ? worker * total / workers : 0;
-  const int64_t u1 = works ? (worker + 1) * total / workers : 0;
-  const int n = (int)(u1 - u0);
-  int cur_r = 0;
-  int64_t cur_s = 0;        // first unit of request cur_r
-  if (n) {
-    int lo = 0, hi = (p.R - 1) / per;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (prefix[mid] <= u0) lo = mid; else hi = mid - 1;
+  int64_t total;
+  int most = kCtas, rank = blockIdx.x, cur_r = 0;
+  uint32_t fixed_sub = 0;
+  if (kCluster) {
+    most = (int)cluster_size();
+    rank = (int)cluster_ctarank();
+    const int id = (int)blockIdx.x / most;
+    cur_r = id / items;
+    fixed_sub = (uint32_t)(id - cur_r * items);
+    total = span_of(p, cur_r).units;
+    if (tid == 0 && p.flags &&
+        __ldg(p.lens + cur_r) > (int64_t)p.max_blocks * kBlock)
+      atomicOr(p.flags, KVTC_FLAG_SPACE);
+    __syncthreads();
+  } else {
+    // Units of the requests before each thread's run of requests.
+    const int per = (p.R + kThreads - 1) / kThreads;
+    int64_t sum = 0;
+  #pragma unroll 1
+    for (int i = 0; i < per; ++i) {
+      const int r = tid * per + i;
+      if (r >= p.R) break;
+      sum += span_of(p, r).units;
+      if (p.flags && blockIdx.x == 0 &&
+          __ldg(p.lens + r) > (int64_t)p.max_blocks * kBlock)
+        atomicOr(p.flags, KVTC_FLAG_SPACE);
     }
-    cur_r = lo * per;
-    cur_s = prefix[lo];
+    int64_t upto = sum;
+  #pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t o = __shfl_up_sync(0xFFFFFFFFu, upto, d);
+      if (lane >= d) upto += o;
+    }
+    if (lane == 31) warp_sums[warp] = upto;
+    __syncthreads();
+    total = 0;
+  #pragma unroll
+    for (int w = 0; w < W; ++w) {
+      if (w < warp) upto += warp_sums[w];
+      total += warp_sums[w];
+    }
+    prefix[tid] = (upto - sum) * items;
+    total *= items;
+    __syncthreads();
+  }
+  const Deal<W> deal(total, most);
+  const int worker = rank * W + warp;
+  const bool works = rank < deal.ctas;
+  const int64_t u0 = works ? deal.begin(worker) : 0;
+  const int64_t u1 = works ? deal.begin(worker + 1) : 0;
+  const int n = (int)(u1 - u0);
+  int64_t cur_s = 0;        // first unit of request cur_r
+  if (!kCluster && n) {
+    const int per = (p.R + kThreads - 1) / kThreads;
+    int before = 0;         // runs of requests that begin at or before u0
+#pragma unroll
+    for (int i = 0; i < W; ++i)
+      before += __popc(__ballot_sync(
+          0xFFFFFFFFu, (i * 32 + lane) * per < p.R &&
+                           prefix[i * 32 + lane] <= u0));
+    cur_r = (before - 1) * per;
+    cur_s = prefix[before - 1];
   }
 
   const uint32_t ring = smem_u32(smem) + warp * S * stage_bytes(HD);
@@ -457,14 +628,15 @@ __global__ void __launch_bounds__(warps_of(HD) * 32, 1)
     int64_t s = cur_s;
     if (u < u1) {
       Span sp = span_of(p, r);
-      while (u >= s + (int64_t)sp.units * items) {
-        s += (int64_t)sp.units * items;
-        sp = span_of(p, ++r);
+      int v = (int)u;
+      uint32_t sub = fixed_sub;
+      if (!kCluster) {
+        while (u >= s + (int64_t)sp.units * items) {
+          s += (int64_t)sp.units * items;
+          sp = span_of(p, ++r);
+        }
+        sub = small_quotient(u - s, sp.units, &v);
       }
-      const int64_t o = u - s;
-      const uint32_t sub = (o >> 32) ? (uint32_t)(o / sp.units)
-                                     : (uint32_t)o / (uint32_t)sp.units;
-      const int v = (int)(o - (int64_t)sub * sp.units);
       b_r = r;
       b_page = v < sp.front ? v : v + sp.gap;
       b_len = sp.len;
@@ -479,15 +651,19 @@ __global__ void __launch_bounds__(warps_of(HD) * 32, 1)
         }
       }
       if (b_id < 0) b_sub |= kSkip;
+      const int t0 = b_page * kBlock;
+      if (sp.len - t0 >= kBlock &&
+          (!sp.hole || (int64_t)t0 + kBlock <= p.sink ||
+           t0 >= sp.len - p.window))
+        b_sub |= kWhole;
     }
     const int last = min(31, n - 1 - i);
     cur_r = __shfl_sync(0xFFFFFFFFu, r, last);
     cur_s = __shfl_sync(0xFFFFFFFFu, s, last);
   };
-  auto issue = [&](int i) {
+  auto issue = [&](int i, int st) {
     if ((i & 31) == 0) fill(i);
     if (lane == (i & 31)) {
-      const int st = i % S;
       UnitMeta m;
       m.r = b_r;
       m.sub = b_sub;
@@ -497,7 +673,8 @@ __global__ void __launch_bounds__(warps_of(HD) * 32, 1)
       if (b_sub & kSkip) {
         mbar_arrive(bars + st);
       } else {
-        const int slab = (int)((b_sub & kSubMask) / p.tiles) * (HD / 64);
+        int slab = (int)(b_sub & kSubMask) * (HD / 64);
+        if (p.tiles != 1) slab = (int)(b_sub & kSubMask) / p.tiles * (HD / 64);
         const uint32_t dst = ring + st * stage_bytes(HD);
         mbar_arrive_expect_tx(bars + st, 2 * kPage);
         tma_load_page(dst, &p.tm_k, slab, b_id, bars + st);
@@ -506,7 +683,6 @@ __global__ void __launch_bounds__(warps_of(HD) * 32, 1)
     }
     __syncwarp();
   };
-  for (int i = 0; i < min(n, S); ++i) issue(i);
 
   // ldmatrix addresses inside a page: the row of this lane and its 128-byte
   // swizzle.  K: matrices (token half, chunk); V, transposed: (chunk, half).
@@ -518,24 +694,31 @@ __global__ void __launch_bounds__(warps_of(HD) * 32, 1)
 
   uint32_t qf[MT][NT][2];
   float acc[MT][NT][4];
-  float m_run[NT][2], l_run[NT][2];
+  float m_run[NT][2], limit[NT][2], l_run[NT][2];
   bool begun = false;          // the current item began in this run
   int64_t item_begin = 0;
   int pending = 0;             // kept across the loop for the drain below
 
-  for (int c = 0; c < n; ++c) {
-    const int st = c % S;
-    if (!__all_sync(0xFFFFFFFFu,
-                    mbar_wait(bars + st, (c / S) & 1, abort_flag))) {
-      *abort_flag = 1;
-      break;
+  // Turn c uses unit c and then asks for unit c + S, which takes its place in
+  // the ring; the first S turns only ask.
+  int st = S - 1;
+  uint32_t phase = 0;
+  UnitMeta meta = {0, 0u, 0, 0};
+  for (int c = n ? -S : 0; c < n; ++c) {
+    if (++st == S) {
+      st = 0;
+      phase ^= 1;
     }
-    pending = c + 1;
-    const UnitMeta meta = metas[st];
+    if (c >= 0) {
+    meta = metas[st];
     const uint32_t sub = meta.sub & kSubMask;
     if (c == 0 || (meta.sub & kFirst)) {
       begun = meta.sub & kFirst;
       item_begin = u0 + c;
+      if (!begun) {
+        const Span sp = span_of(p, meta.r);
+        item_begin -= meta.page < sp.front ? meta.page : meta.page - sp.gap;
+      }
       int head0, rows;
       head_range(p, sub, &head0, &rows);
       const T* q = static_cast<const T*>(p.q) + (int64_t)meta.r * p.q_ld +
@@ -555,13 +738,23 @@ __global__ void __launch_bounds__(warps_of(HD) * 32, 1)
 #pragma unroll
           for (int i = 0; i < 4; ++i) acc[mt][nt][i] = 0.f;
         m_run[nt][0] = m_run[nt][1] = -INFINITY;
+        limit[nt][0] = limit[nt][1] = -INFINITY;
         l_run[nt][0] = l_run[nt][1] = 0.f;
       }
     }
+    // (the query's loads are under way while the page is waited for)
+    if (!__all_sync(0xFFFFFFFFu,
+                    mbar_wait(bars + st, phase, abort_flag))) {
+      *abort_flag = 1;
+      break;
+    }
+    pending = c + 1;
 
     if (!(meta.sub & kSkip)) {
       const uint32_t kp = ring + st * stage_bytes(HD), vp = kp + kPage;
-      float sc[NT][4];
+      // S^T, in two chains where there is one head tile
+      constexpr int kChains = NT == 1 ? 2 : 1;
+      float sc[NT][4], sd[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
         sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
@@ -572,60 +765,75 @@ __global__ void __launch_bounds__(warps_of(HD) * 32, 1)
         ldsm4(a, kp + (ks >> 2) * 2048 + k_base + ((chunk ^ swz) << 4));
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
-          Elem<T>::mma(sc[nt], a, qf[ks][nt][0], qf[ks][nt][1]);
+          Elem<T>::mma(kChains == 2 && (ks & 1) ? sd : sc[nt], a,
+                       qf[ks][nt][0], qf[ks][nt][1]);
       }
-      // tokens gid and gid + 8 of the page; columns are heads
+      const bool whole = meta.sub & kWhole;
       const int t0 = meta.page * kBlock;
       const int recent = p.window ? meta.len - p.window : 0;
-      const bool whole =
-          t0 + kBlock <= meta.len &&
-          (t0 >= recent || (int64_t)t0 + kBlock <= p.sink);
       auto seen = [&](int t) {
         return t < meta.len && (t < p.sink || t >= recent);
       };
-      const bool in0 = whole || seen(t0 + gid);
-      const bool in1 = whole || seen(t0 + gid + 8);
-      uint32_t ph[NT][2], pl[NT][2];
-      bool grew = false;
-      float alpha[NT][2];
+      // tokens gid and gid + 8 of the page; columns are heads
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float s[4];
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          sc[nt][i] = (kChains == 2 ? sc[nt][i] + sd[i] : sc[nt][i]) *
+                      p.scale_log2;
+          if (!whole && !seen(t0 + gid + (i >> 1) * 8))
+            sc[nt][i] = -INFINITY;
+        }
+      // The reference that exponents are taken from moves only when a score
+      // lies kSlack above it: the maximum over the lanes (six shuffles in
+      // chains of three) and the rescaling are seldom needed.
+      bool above = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          s[i] = (i < 2 ? in0 : in1) ? sc[nt][i] * p.scale_log2 : -INFINITY;
+          above |= sc[nt][i] > limit[nt][i & 1];
+      if (__any_sync(0xFFFFFFFFu, above)) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          float mx = fmaxf(s[i], s[i + 2]);
-          mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 4));
-          mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 8));
-          mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 16));
-          const float mn = fmaxf(m_run[nt][i], mx), base = base_of(mn);
-          alpha[nt][i] = exp2_fast(m_run[nt][i] - base);
-          grew |= mn != m_run[nt][i];
-          m_run[nt][i] = mn;
-          s[i] = exp2_fast(s[i] - (base - Elem<T>::kShift));
-          s[i + 2] = exp2_fast(s[i + 2] - (base - Elem<T>::kShift));
-          l_run[nt][i] = l_run[nt][i] * alpha[nt][i] + (s[i] + s[i + 2]);
-        }
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float mx = fmaxf(sc[nt][i], sc[nt][i + 2]);
+            mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 4));
+            mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 8));
+            mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 16));
+            const float mn = fmaxf(m_run[nt][i], mx);
+            const float alpha = exp2_fast(m_run[nt][i] - base_of(mn));
+            m_run[nt][i] = mn;
+            limit[nt][i] = mn + kSlack;
+            l_run[nt][i] *= alpha;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              acc[mt][nt][i] *= alpha;
+              acc[mt][nt][i + 2] *= alpha;
+            }
+          }
+      }
+      uint32_t ph[NT][2], pl[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          w[i] = exp2_fast(sc[nt][i] -
+                           (base_of(m_run[nt][i & 1]) - Elem<T>::kShift));
+        l_run[nt][0] += w[0] + w[2];
+        l_run[nt][1] += w[1] + w[3];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const uint32_t hi = Elem<T>::pack_down(
-              s[2 * h] * Elem<T>::kBelow, s[2 * h + 1] * Elem<T>::kBelow);
+              w[2 * h] * Elem<T>::kBelow, w[2 * h + 1] * Elem<T>::kBelow);
           const float2 f = Elem<T>::unpack(hi);
           const uint32_t lo =
-              Elem<T>::pack(s[2 * h] - f.x, s[2 * h + 1] - f.y);
+              Elem<T>::pack(w[2 * h] - f.x, w[2 * h + 1] - f.y);
           ph[nt][h] = transpose8(hi);
           pl[nt][h] = transpose8(lo);
         }
-      }
-      if (__any_sync(0xFFFFFFFFu, grew)) {
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[mt][nt][i] *= alpha[nt][i & 1];
       }
       auto pv = [&](auto masked) {
         // rows of V that are not attended may hold NaN: as zeros, 0 * 0
@@ -656,9 +864,12 @@ __global__ void __launch_bounds__(warps_of(HD) * 32, 1)
       };
       if (whole) pv(std::false_type{}); else pv(std::true_type{});
     }
+    }
     __syncwarp();
-    if (c + S < n) issue(c + S);
+    if (c + S < n) issue(c + S, st);
+    if (c < 0) continue;
 
+    const uint32_t sub = meta.sub & kSubMask;
     const bool ended = meta.sub & kLast;
     if (!ended && c + 1 < n) continue;
     // the sums over a head's tokens are still spread over the lanes
@@ -669,22 +880,57 @@ __global__ void __launch_bounds__(warps_of(HD) * 32, 1)
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1)
           l_run[nt][i] += __shfl_xor_sync(0xFFFFFFFFu, l_run[nt][i], d);
-    if (begun && ended) {
+    bool done = begun && ended;
+    if (begun && !ended && warp + 1 < W &&
+        __all_sync(0xFFFFFFFFu, heads_ready[warp + 1])) {
+      // The item ends in the next warp's run, which has left that part (it
+      // came first there): join it here, where the accumulators are.
+      __threadfence_block();
+      const float* slot = own_slot + L::kSlot / 4;
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+      for (int nt = 0; nt < NT; ++nt) {
+        const float* stat = slot + NT * 8 * HD + nt * 8 + tig * 2;
+        float f[2];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-          finish_item<T, HD, NT>(p, meta.r, sub, mt * NT + nt, acc[mt][nt],
-                                 m_run[nt], l_run[nt]);
+        for (int i = 0; i < 2; ++i) {
+          const float mn = fmaxf(m_run[nt][i], stat[i]), base = base_of(mn);
+          const float a = exp2_fast(m_run[nt][i] - base);
+          f[i] = exp2_fast(stat[i] - base);
+          m_run[nt][i] = mn;
+          l_run[nt][i] =
+              __fmaf_rn(stat[NT * 8 + i], f[i], __fmul_rn(l_run[nt][i], a));
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            acc[mt][nt][i] = __fmul_rn(acc[mt][nt][i], a);
+            acc[mt][nt][i + 2] = __fmul_rn(acc[mt][nt][i + 2], a);
+          }
+        }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          const float4 x = *reinterpret_cast<const float4*>(
+              slot + ((mt * NT + nt) * 32 + lane) * 4);
+          acc[mt][nt][0] = __fmaf_rn(x.x, f[0], acc[mt][nt][0]);
+          acc[mt][nt][1] = __fmaf_rn(x.y, f[1], acc[mt][nt][1]);
+          acc[mt][nt][2] = __fmaf_rn(x.z, f[0], acc[mt][nt][2]);
+          acc[mt][nt][3] = __fmaf_rn(x.w, f[1], acc[mt][nt][3]);
+        }
+      }
+      if (lane == 0) recs[(warp + 1) * 2].r = -1;
+      done = true;
+    }
+    if (done) {
+      const Target<T> target(p, meta.r, sub, HD);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const float inv[2] = {inverse(l_run[nt][0]), inverse(l_run[nt][1])};
+        target.store_lse(nt, m_run[nt], l_run[nt]);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+          target.template store<HD>(nt, mt, acc[mt][nt], inv);
+      }
       continue;
     }
-    // a part: in the ring when the run ends with it (every page has been
-    // read), else in the workspace
-    const bool at_end = c + 1 == n;
-    float* slot =
-        at_end ? reinterpret_cast<float*>(smem + warp * S * stage_bytes(HD))
-               : p.warp_slots + ((int64_t)blockIdx.x * W + warp) *
-                                    slot_floats(HD, NT);
+    float* slot = ended ? own_slot : ring_slot;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -692,11 +938,16 @@ __global__ void __launch_bounds__(warps_of(HD) * 32, 1)
         store_part<HD, NT>(slot, mt * NT + nt, acc[mt][nt], m_run[nt],
                            l_run[nt]);
     if (lane == 0) {
-      PartRec& rec = recs[warp * 2 + (ended ? 0 : 1)];
+      PartRec rec;
       rec.begin = item_begin;
       rec.r = meta.r;
       rec.sub = sub | (begun ? kFirst : 0u) | (ended ? kLast : 0u);
-      rec.present = at_end ? 1 : 2;
+      recs[warp * 2 + (ended ? 0 : 1)] = rec;
+    }
+    if (ended) {
+      __threadfence_block();
+      __syncwarp();
+      if (lane == 0) heads_ready[warp] = 1;
     }
   }
   if (pending < n) {
@@ -707,92 +958,246 @@ __global__ void __launch_bounds__(warps_of(HD) * 32, 1)
   }
   __syncthreads();
 
-  // Join the block's parts: entries in order, those of one item together.
-  auto entry = [&](int e) -> const float* {
-    const int w = e >> 1;
-    return recs[e].present == 1
-               ? reinterpret_cast<const float*>(smem + w * S *
-                                                           stage_bytes(HD))
-               : p.warp_slots + ((int64_t)blockIdx.x * W + w) *
-                                    slot_floats(HD, NT);
-  };
-  JoinDesc desc;
-  desc.r = -1;
-  desc.sub = desc.last_cta = desc.pad = 0;
-  int e = 0;
-  while (e < 2 * W) {
-    if (!recs[e].present) {
-      ++e;
-      continue;
-    }
-    const PartRec first = recs[e];
-    const uint32_t sub = first.sub & kSubMask;
-    int list[W + 1], k = 0;
-    uint32_t bits = first.sub & kFirst;
-    for (; e < 2 * W; ++e) {
-      if (!recs[e].present) continue;
-      if (recs[e].r != first.r || (recs[e].sub & kSubMask) != sub) break;
-      bits |= recs[e].sub & kLast;
-      list[k++] = e;
-    }
-    for (int tile = warp; tile < MT * NT; tile += W) {
-      float o[4], m[2], l[2];
-      join_parts<HD, NT>(k, tile, [&](int i) { return entry(list[i]); }, o, m,
-                         l);
-      if (bits == (kFirst | kLast))
-        finish_item<T, HD, NT>(p, first.r, sub, tile, o, m, l);
-      else
-        store_part<HD, NT>(p.cta_slots + ((int64_t)blockIdx.x * 2 +
-                                          (bits & kFirst ? 1 : 0)) *
-                                             slot_floats(HD, NT),
-                           tile, o, m, l);
-    }
-    if (bits == kFirst) {
-      // it ends in the block that holds its last unit
-      desc.r = first.r;
-      desc.sub = (int32_t)sub;
-      const int64_t end = first.begin + span_of(p, first.r).units;
-      desc.last_cta =
-          (int)min((end * workers - 1) / total / active, ctas - 1);
-    }
+  // Join the block's parts: runs of records of one item, in order.  Lane e
+  // of every warp holds record e.  A run goes to one warp, or where there
+  // are few (long items) to several, which share its channel tiles.
+  PartRec rec = {0, -1, 0u};
+  if (lane < 2 * W) rec = recs[lane];
+  const uint32_t item = rec.sub & kSubMask;
+  const uint32_t there = __ballot_sync(0xFFFFFFFFu, rec.r >= 0);
+  const uint32_t before = there & ((1u << lane) - 1);
+  const int prev = before ? 31 - __clz(before) : lane;
+  const int prev_r = __shfl_sync(0xFFFFFFFFu, rec.r, prev);
+  const uint32_t prev_item = __shfl_sync(0xFFFFFFFFu, item, prev);
+  const uint32_t heads = __ballot_sync(
+      0xFFFFFFFFu, rec.r >= 0 && (!before || prev_r != rec.r ||
+                                  prev_item != item));
+  const int runs = __popc(heads);
+  const int share = runs && runs < W ? W / runs : 1;   // warps per run
+  const uint32_t smem_at = smem_u32(smem);
+  uint32_t left = heads;
+#pragma unroll 1
+  for (int i = 0, w = 0; i < runs; ++i, w = w + share < W ? w + share : 0) {
+    const int e0 = __ffs(left) - 1;
+    left &= left - 1;
+    if (warp < w || warp >= w + share) continue;
+    const uint32_t in_run =
+        there & ~((1u << e0) - 1) & (left ? (left & (0u - left)) - 1 : ~0u);
+    const int e1 = 31 - __clz(in_run);
+    const bool begun_here = __shfl_sync(0xFFFFFFFFu, rec.sub, e0) & kFirst;
+    const bool ended_here = __shfl_sync(0xFFFFFFFFu, rec.sub, e1) & kLast;
+    // its parts: entry 1 of consecutive warps, and last what it is
+    auto slot_of = [&](int e) {
+      return smem_at + ((e & 1) ? (e >> 1) * S * stage_bytes(HD)
+                                : L::kParts + (e >> 1) * L::kSlot);
+    };
+    float* to = nullptr;
+    if (!(begun_here && ended_here))
+      to = kCluster ? reinterpret_cast<float*>(smem + L::kBlockPart)
+                    : p.cta_slots + ((int64_t)blockIdx.x * 2 +
+                                     (begun_here ? 1 : 0)) *
+                                        slot_floats(HD, NT);
+    const Target<T> target(p, __shfl_sync(0xFFFFFFFFu, rec.r, e0),
+                           __shfl_sync(0xFFFFFFFFu, item, e0), HD);
+    const uint32_t first = slot_of(e0), last = slot_of(e1);
+    const uint32_t base = slot_of(e0 | 1);
+    const int k = __popc(in_run);
+    join_parts<T, HD, NT, 4, false>(
+        k,
+        [=](int i) {
+          return i == 0 ? first
+                 : i == k - 1 ? last : base + i * (S * stage_bytes(HD));
+        },
+        target, to, warp - w, share);
   }
-  if (tid == 0) p.desc[blockIdx.x] = desc;
+
+  if (kCluster) {
+    if (deal.ctas == 1) return;
+    cluster_sync();
+    // one part in each working block, in their order
+    const uint32_t mine = smem_at + L::kBlockPart;
+    join_parts<T, HD, NT, 8, true>(
+        deal.ctas, [=](int i) { return mapa_shared(mine, (uint32_t)i); },
+        Target<T>(p, cur_r, fixed_sub, HD), nullptr, rank + warp * most,
+        most * W);
+    cluster_sync();       // (the others have read this block's part)
+    return;
+  }
+  // An item that goes on in the next blocks is the last run's.
+  if (warp == W - 1) {
+    const int e0 = heads ? 31 - __clz(heads) : 0;
+    const int e1 = there ? 31 - __clz(there) : 0;
+    const uint32_t first_sub = __shfl_sync(0xFFFFFFFFu, rec.sub, e0);
+    const uint32_t last_sub = __shfl_sync(0xFFFFFFFFu, rec.sub, e1);
+    const int64_t begin = __shfl_sync(0xFFFFFFFFu, rec.begin, e0);
+    const int r = __shfl_sync(0xFFFFFFFFu, rec.r, e0);
+    JoinDesc d = {-1, 0, 0, 0};
+    if (there && (first_sub & kFirst) && !(last_sub & kLast)) {
+      d.r = r;
+      d.sub = (int32_t)(first_sub & kSubMask);
+      d.last_cta = deal.cta_of(begin + span_of(p, r).units - 1);
+    }
+    if (lane == 0)
+      *reinterpret_cast<int4*>(p.desc + blockIdx.x) =
+          make_int4(d.r, d.sub, d.last_cta, 0);
+  }
 }
 
 // Items that lie over several blocks: block c joins the one that began in
 // block c of the attention, its own part and those of the blocks after it.
+// Groups of warps take every kGroups-th part, kBatch of them with all loads
+// in flight (before it is known how many there are), and are joined through
+// shared memory.
+__host__ __device__ constexpr int join_groups(int tiles) {
+  return tiles > 16 ? 1 : tiles > 8 ? 2 : 4;
+}
 template <class T, int HD, int NT>
-__global__ void __launch_bounds__(HD / 16 * NT * 32)
+__global__ void __launch_bounds__(HD / 16 * NT * 32 *
+                                  join_groups(HD / 16 * NT))
     attend_join_kernel(const __grid_constant__ AttendParams p) {
+  constexpr int kTiles = HD / 16 * NT, kGroups = join_groups(kTiles);
+  constexpr int kBatch = 5;
+  __shared__ float4 part_o[kGroups][kTiles * 32];
+  __shared__ float4 part_ml[kGroups][kTiles * 32];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tile = warp % kTiles, group = warp / kTiles;
+  const int nt = tile % NT, col = nt * 8 + (lane & 3) * 2;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const JoinDesc d = p.desc[blockIdx.x];
-  if (d.r < 0) return;
-  const int c = blockIdx.x, tile = threadIdx.x >> 5;
-  float o[4], m[2], l[2];
-  join_parts<HD, NT>(
-      d.last_cta - c + 1, tile,
-      [&](int i) {
-        return p.cta_slots + ((int64_t)(c + i) * 2 + (i == 0 ? 1 : 0)) *
-                                 slot_floats(HD, NT);
-      },
-      o, m, l);
-  finish_item<T, HD, NT>(p, d.r, (uint32_t)d.sub, tile, o, m, l);
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  float o[4] = {0.f, 0.f, 0.f, 0.f};
+  int4 d = make_int4(-1, 0, 0, 0);
+  int n = kCtas;
+  for (int i0 = group; i0 < n; i0 += kGroups * kBatch) {
+    float2 mi[kBatch], li[kBatch];
+    float4 oi[kBatch];
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const int i = i0 + b * kGroups;
+      const float* s = p.cta_slots +
+                       ((int64_t)min(c + i, kCtas - 1) * 2 + (i ? 0 : 1)) *
+                           slot_floats(HD, NT);
+      mi[b] = __ldcg(reinterpret_cast<const float2*>(s + NT * 8 * HD + col));
+      li[b] = __ldcg(
+          reinterpret_cast<const float2*>(s + NT * 8 * (HD + 1) + col));
+      oi[b] = __ldcg(reinterpret_cast<const float4*>(s) + tile * 32 + lane);
+    }
+    if (i0 == group) {
+      d = __ldcg(reinterpret_cast<const int4*>(p.desc + c));
+      if (d.x < 0) return;
+      n = d.z - c + 1;
+    }
+    float mn[2] = {m[0], m[1]};
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b)
+      if (i0 + b * kGroups < n) {
+        mn[0] = fmaxf(mn[0], mi[b].x);
+        mn[1] = fmaxf(mn[1], mi[b].y);
+      }
+    const float b0 = base_of(mn[0]), b1 = base_of(mn[1]);
+    const float a0 = exp2_fast(m[0] - b0), a1 = exp2_fast(m[1] - b1);
+    m[0] = mn[0];
+    m[1] = mn[1];
+    l[0] *= a0;
+    l[1] *= a1;
+    o[0] *= a0;
+    o[1] *= a1;
+    o[2] *= a0;
+    o[3] *= a1;
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b)
+      if (i0 + b * kGroups < n) {
+        const float f0 = exp2_fast(mi[b].x - b0);
+        const float f1 = exp2_fast(mi[b].y - b1);
+        l[0] += li[b].x * f0;
+        l[1] += li[b].y * f1;
+        o[0] += oi[b].x * f0;
+        o[1] += oi[b].y * f1;
+        o[2] += oi[b].z * f0;
+        o[3] += oi[b].w * f1;
+      }
+  }
+  if (kGroups > 1) {
+    part_o[group][tile * 32 + lane] = make_float4(o[0], o[1], o[2], o[3]);
+    part_ml[group][tile * 32 + lane] = make_float4(m[0], m[1], l[0], l[1]);
+    __syncthreads();
+    if (group) return;
+#pragma unroll
+    for (int g = 1; g < kGroups; ++g) {
+      const float4 y = part_ml[g][tile * 32 + lane];
+      m[0] = fmaxf(m[0], y.x);
+      m[1] = fmaxf(m[1], y.y);
+    }
+    l[0] = l[1] = o[0] = o[1] = o[2] = o[3] = 0.f;
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) {
+      const float4 y = part_ml[g][tile * 32 + lane];
+      const float4 x = part_o[g][tile * 32 + lane];
+      const float f0 = exp2_fast(y.x - base_of(m[0]));
+      const float f1 = exp2_fast(y.y - base_of(m[1]));
+      l[0] += y.z * f0;
+      l[1] += y.w * f1;
+      o[0] += x.x * f0;
+      o[1] += x.y * f1;
+      o[2] += x.z * f0;
+      o[3] += x.w * f1;
+    }
+  }
+  const Target<T> target(p, d.x, (uint32_t)d.y, HD);
+  const float inv[2] = {inverse(l[0]), inverse(l[1])};
+  target.template store<HD>(nt, tile / NT, o, inv);
+  if (tile < NT) target.store_lse(nt, m, l);
 }
 
 template <class T, int HD, int NT>
-cudaError_t launch_as(const AttendParams& p, cudaStream_t st) {
-  cudaError_t e = cudaFuncSetAttribute(
-      attend_kernel<T, HD, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-      Smem<HD>::kBytes);
-  if (e != cudaSuccess) return e;
-  e = launch_kernel(attend_kernel<T, HD, NT>, kCtas, warps_of(HD) * 32,
-                    Smem<HD>::kBytes, st, false, p);
+cudaError_t launch_as(const AttendParams& p, int cluster, int device,
+                      cudaStream_t st) {
+  constexpr int kThreads = warps_of(HD, NT) * 32;
+  constexpr int kBytes = Smem<HD, NT>::kBytes;
+  static std::atomic<uint64_t> ready[2];     // devices, as bits
+  cudaError_t e;
+  if (cluster) {
+    const auto kernel = attend_kernel<T, HD, NT, true>;
+    e = allow_smem(kernel, kBytes, device, ready[0], true);
+    if (e == cudaSuccess)
+      e = launch_kernel(kernel,
+                        (unsigned)(p.R * p.kv_heads * p.tiles * cluster),
+                        kThreads, kBytes, st, true, cluster, p);
+    if (e == cudaSuccess) count_launch();
+    return e;
+  }
+  const auto kernel = attend_kernel<T, HD, NT, false>;
+  e = allow_smem(kernel, kBytes, device, ready[1]);
+  if (e == cudaSuccess)
+    e = launch_kernel(kernel, kCtas, kThreads, kBytes, st, true, 0, p);
   if (e != cudaSuccess) return e;
   count_launch();
-  e = launch_kernel(attend_join_kernel<T, HD, NT>, kCtas, HD / 16 * NT * 32,
-                    0, st, true, p);
+  constexpr int kTiles = HD / 16 * NT;
+  e = launch_kernel(attend_join_kernel<T, HD, NT>, kCtas,
+                    kTiles * 32 * join_groups(kTiles), 0, st, true, 0, p);
   if (e == cudaSuccess) count_launch();
   return e;
+}
+
+// Blocks per item, or 0 for equal runs over all items.  The GPU holds 7
+// clusters of 16 such blocks at once, 15 of 8, 36 of 4, 76 of 2 (what
+// cudaOccupancyMaxActiveClusters says of it).  A cluster of more blocks than
+// the longest item can feed is of no use.  What clusters save is the join
+// across blocks, about 6 us; what they lose is that items * cluster blocks,
+// at about 90 GB/s a block, may read slower than all SMs at 7000 GB/s, which
+// is taken at the longest length that the table allows, for the others half
+// of that.
+int cluster_of(int64_t items, int64_t max_blocks, int head_dim, int nt) {
+  if (items > kCtas) return 0;
+  int cluster = items <= 7 ? 16 : items <= 15 ? 8 : items <= 36 ? 4
+                : items <= 76 ? 2 : 1;
+  const int64_t feeds = (int64_t)warps_of(head_dim, nt) * kLeast;
+  while (cluster > 1 && max_blocks <= feeds * (cluster / 2)) cluster /= 2;
+  const double bytes = (double)max_blocks * stage_bytes(head_dim);
+  const double others = items == 1 ? 1.0 : 0.5 + 0.5 / (double)items;
+  return bytes / (90.0 * cluster) - others * bytes * items / 7000.0 <= 6000.0
+             ? cluster
+             : 0;
 }
 
 // Tiles of eight query heads per warp: as many as the group needs, up to 32
@@ -804,17 +1209,17 @@ int head_tiles(int head_dim, int group) {
 }
 
 template <class T>
-cudaError_t launch(const AttendParams& p, int head_dim, int nt,
-                   cudaStream_t st) {
+cudaError_t launch(const AttendParams& p, int head_dim, int nt, int cluster,
+                   int device, cudaStream_t st) {
   if (head_dim == 64)
-    return nt == 1   ? launch_as<T, 64, 1>(p, st)
-           : nt == 2 ? launch_as<T, 64, 2>(p, st)
-                     : launch_as<T, 64, 4>(p, st);
+    return nt == 1   ? launch_as<T, 64, 1>(p, cluster, device, st)
+           : nt == 2 ? launch_as<T, 64, 2>(p, cluster, device, st)
+                     : launch_as<T, 64, 4>(p, cluster, device, st);
   if (head_dim == 128)
-    return nt == 1   ? launch_as<T, 128, 1>(p, st)
-           : nt == 2 ? launch_as<T, 128, 2>(p, st)
-                     : launch_as<T, 128, 4>(p, st);
-  return nt == 1 ? launch_as<T, 256, 1>(p, st) : launch_as<T, 256, 2>(p, st);
+    return nt == 1   ? launch_as<T, 128, 1>(p, cluster, device, st)
+           : nt == 2 ? launch_as<T, 128, 2>(p, cluster, device, st)
+                     : launch_as<T, 128, 4>(p, cluster, device, st);
+  return nt == 1 ? launch_as<T, 256, 1>(p, cluster, device, st) : launch_as<T, 256, 2>(p, cluster, device, st);
 }
 
 // A pool [num_blocks][16][D] as {64 channels, 16 tokens, D / 64, num_blocks}:
@@ -833,7 +1238,8 @@ bool encode_pages(CUtensorMap* m, const void* base, uint64_t D,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-constexpr int64_t kDescBytes = (kCtas * sizeof(JoinDesc) + 255) / 256 * 256;
+constexpr int64_t kDescBytes =
+    (kCtas * sizeof(JoinDesc) + 255) / 256 * 256;
 
 inline bool misaligned4(const void* p) {
   return (reinterpret_cast<uintptr_t>(p) & 3u) != 0;
@@ -862,9 +1268,9 @@ int64_t kvtc_paged_attend_workspace_bytes(int cuda_device, int R, int heads,
                                           int kv_heads, int head_dim) {
   const int st = check_shape(cuda_device, R, heads, kv_heads, head_dim);
   if (st != KVTC_OK) return st;
-  const int64_t slot =
-      4 * slot_floats(head_dim, head_tiles(head_dim, heads / kv_heads));
-  return kDescBytes + kCtas * (2 + warps_of(head_dim)) * slot;
+  const int nt = head_tiles(head_dim, heads / kv_heads);
+  const int64_t slot = 4 * slot_floats(head_dim, nt);
+  return kDescBytes + kCtas * 2 * slot;
 }
 
 int kvtc_paged_attend(int cuda_device, int R, int heads, int kv_heads,
@@ -913,7 +1319,6 @@ int kvtc_paged_attend(int cuda_device, int R, int heads, int kv_heads,
   p.desc = static_cast<JoinDesc*>(workspace);
   p.cta_slots = reinterpret_cast<float*>(static_cast<char*>(workspace) +
                                          kDescBytes);
-  p.warp_slots = p.cta_slots + kCtas * 2 * slot_floats(head_dim, nt);
   p.q_ld = q_ld;
   p.out_ld = out_ld;
   p.num_blocks = num_blocks;
@@ -927,10 +1332,14 @@ int kvtc_paged_attend(int cuda_device, int R, int heads, int kv_heads,
   p.group = group;
   p.tiles = (group + 8 * nt - 1) / (8 * nt);
   p.tile_heads = (group + p.tiles - 1) / p.tiles;
+  const int cluster = cluster_of((int64_t)R * kv_heads * p.tiles, max_blocks,
+                                 head_dim, nt);
   cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
   const cudaError_t e = dtype == KVTC_DTYPE_BF16
-                            ? launch<__nv_bfloat16>(p, head_dim, nt, st)
-                            : launch<__half>(p, head_dim, nt, st);
+                            ? launch<__nv_bfloat16>(p, head_dim, nt, cluster,
+                                                    cuda_device, st)
+                            : launch<__half>(p, head_dim, nt, cluster,
+                                             cuda_device, st);
   return e == cudaSuccess ? KVTC_OK : KVTC_ECUDA;
 }
 

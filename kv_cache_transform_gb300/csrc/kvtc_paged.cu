@@ -261,7 +261,7 @@ int kvtc_paged_assign(int cuda_device, int R, const int32_t* held,
   p.flags = flags;
   p.R = R;
   p.max_blocks = max_blocks;
-  if (launch_kernel(assign_scan_kernel, 1, kScanThreads, 0, st, false, p) !=
+  if (launch_kernel(assign_scan_kernel, 1, kScanThreads, 0, st, false, 0, p) !=
       cudaSuccess)
     return KVTC_ECUDA;
   count_launch();
@@ -270,7 +270,7 @@ int kvtc_paged_assign(int cuda_device, int R, const int32_t* held,
   if (want) {
     if (launch_kernel(assign_fill_kernel,
                       (unsigned)std::min<int64_t>(want, 8 * 152), 256, 0, st,
-                      false, p) != cudaSuccess)
+                      false, 0, p) != cudaSuccess)
       return KVTC_ECUDA;
     count_launch();
   }
@@ -314,7 +314,7 @@ int kvtc_paged_append(int cuda_device, int nstreams, const void* const* src,
                       (unsigned)std::min<int64_t>((total + 255) / 256,
                                                   8 * 152),
                       256, 0, static_cast<cudaStream_t>(cuda_stream), false,
-                      p) != cudaSuccess)
+                      0, p) != cudaSuccess)
       return KVTC_ECUDA;
     count_launch();
   }
