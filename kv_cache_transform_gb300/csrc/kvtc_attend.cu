@@ -61,22 +61,26 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kSlack = 6.f;        // log2; see the reference in the loop
 
-// Warps per block and pages in a warp's ring, for nt tiles of eight query
-// heads per warp: what fits 227 KB with the parts kept beside the ring, and
-// the registers.
-__host__ __device__ constexpr int warps_of(int hd, int nt) {
-  return hd == 64    ? (nt == 4 ? 8 : 12)
-         : hd == 128 ? (nt == 1 ? 10 : nt == 2 ? 8 : 5)
-                     : (nt == 1 ? 5 : 4);
-}
-__host__ __device__ constexpr int stages_of(int hd, int nt) {
-  return hd == 64 ? (nt == 4 ? 4 : 3) : hd == 128 && nt == 4 ? 3 : 2;
-}
-__host__ __device__ constexpr int stage_bytes(int hd) { return hd * 64; }
 // Floats of a partial result of nt x 8 query heads: o in fragment order
 // ([channel tile][head tile][lane][4]), then m and l per head.
 __host__ __device__ constexpr int slot_floats(int hd, int nt) {
   return nt * 8 * (hd + 2);
+}
+// Warps per block, for nt tiles of eight query heads per warp: as many as
+// registers and shared memory hold (a cluster's blocks need less of it), with
+// one page each in flight (two of head_dim 64, whose pages are small).  More
+// warps with one page beat fewer with two: 12 x 1 against 10 x 2 at head_dim
+// 128, 64 requests up to 4K: 50.5 and 53.1 us.
+__host__ __device__ constexpr int warps_of(int hd, int nt, bool cluster) {
+  return hd == 64    ? (nt <= 2 ? 12 : 8)
+         : hd == 128 ? (nt == 1 ? (cluster ? 14 : 12)
+                                : cluster || nt == 2 ? 8 : 5)
+                     : (cluster ? 8 : nt == 1 ? 7 : 5);
+}
+__host__ __device__ constexpr int stages_of(int hd) { return hd == 64 ? 2 : 1; }
+__host__ __device__ constexpr int page_bytes(int hd) { return hd * 2 * kBlock; }
+__host__ __device__ constexpr int query_bytes(int hd, int nt) {
+  return nt * 16 * hd;
 }
 
 // Where the join finds the parts of an item that began in a block and did
@@ -116,6 +120,15 @@ __device__ __forceinline__ void tma_load_page(uint32_t smem_dst,
       "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_"
       "tx::bytes [%0], [%1, {%2, %2, %3, %4}], [%5];" ::"r"(smem_dst),
       "l"(tmap), "r"(0), "r"(slab), "r"(block), "r"(smem_u32(bar))
+      : "memory");
+}
+// Bulk copy global -> shared (both 16-byte aligned, bytes % 16 == 0).
+__device__ __forceinline__ void bulk_load(uint32_t smem_dst, const void* src,
+                                          uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes "
+      "[%0], [%1], %2, [%3];" ::"r"(smem_dst),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
       : "memory");
 }
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
@@ -335,23 +348,32 @@ constexpr uint32_t kSubMask = kWhole - 1;
 // ended in its run but began before it (in the slot beside the ring), entry
 // 1 of one that goes on behind it (in the ring, when every page is read).
 struct __align__(16) PartRec {
-  int64_t begin;    // first unit of the item
+  int64_t begin;    // first unit of the item, where kFirst is set
   int32_t r;        // < 0: there is no such part
   uint32_t sub;     // kFirst: begun here; kLast: ended here
 };
 
-template <int HD, int NT>
+template <int HD, int NT, bool kCluster>
 struct Smem {
-  static constexpr int W = warps_of(HD, NT), S = stages_of(HD, NT);
+  static constexpr int W = warps_of(HD, NT, kCluster);
+  static constexpr int S = stages_of(HD);
   static constexpr int kSlot = 4 * slot_floats(HD, NT);
-  static_assert(2 * W <= 32, "a warp's lanes hold the block's part records");
-  static_assert(S * stage_bytes(HD) >= kSlot, "a part fits a warp's ring");
-  static constexpr int kParts = W * S * stage_bytes(HD);
-  static constexpr int kBlockPart = kParts + W * kSlot;
+  static constexpr int kStage = 2 * page_bytes(HD);   // a page of K, one of V
+  // A warp's ring of pages; when the last has been read, a part lies there.
+  static constexpr int kRing =
+      S * kStage >= kSlot ? S * kStage : (kSlot + 1023) / 1024 * 1024;
+  // Queries of the pages in the ring that begin an item (in a cluster each
+  // warp loads its one item's itself).
+  static constexpr int kQueries = kCluster ? 0 : S;
+  static constexpr int kQuery = W * kRing;
+  // Parts of items that end inside a run (in a cluster there are none).
+  static constexpr int kParts = kQuery + W * kQueries * query_bytes(HD, NT);
+  static constexpr int kBlockPart = kParts + (kCluster ? 0 : W * kSlot);
   static constexpr int kRecs = kBlockPart + kSlot;
+  static_assert(2 * W <= 32, "a warp's lanes hold the block's part records");
   static constexpr int kMeta = kRecs + W * 2 * (int)sizeof(PartRec);
   static constexpr int kBars = kMeta + W * S * (int)sizeof(UnitMeta);
-  static constexpr int kPrefix = kBars + W * S * 8;
+  static constexpr int kPrefix = kBars + W * S * 16;
   static constexpr int kMisc = kPrefix + W * 32 * 8;
   static constexpr int kBytes = kMisc + 320 + 1024;  // + alignment slack
   static_assert(kBytes <= 232448, "shared memory of a block");
@@ -362,14 +384,16 @@ struct Smem {
 __device__ __forceinline__ float base_of(float m) {
   return m == -INFINITY ? 0.f : m;
 }
-__device__ __forceinline__ void head_range(const AttendParams& p,
-                                           uint32_t sub, int* head0,
-                                           int* rows) {
-  const int j = p.tiles == 1 ? (int)sub : (int)sub / p.tiles;
-  const int t = (int)sub - j * p.tiles;
-  *head0 = j * p.group + t * p.tile_heads;
-  *rows = min(p.tile_heads, p.group - t * p.tile_heads);
-}
+// The query heads of an item.
+struct Heads {
+  int first, rows;
+  __device__ __forceinline__ Heads(const AttendParams& p, uint32_t sub) {
+    const int j = p.tiles == 1 ? (int)sub : (int)sub / p.tiles;
+    const int t = (int)sub - j * p.tiles;
+    first = j * p.group + t * p.tile_heads;
+    rows = min(p.tile_heads, p.group - t * p.tile_heads);
+  }
+};
 
 // Where an item's result goes.
 template <class T>
@@ -381,11 +405,11 @@ struct Target {
       : out(out_), lse(lse_), rows(rows_) {}
   __device__ __forceinline__ Target(const AttendParams& p, int r,
                                     uint32_t sub, int hd) {
-    int head0;
-    head_range(p, sub, &head0, &rows);
+    const Heads h(p, sub);
+    rows = h.rows;
     out = static_cast<T*>(p.out) + (int64_t)r * p.out_ld +
-          (int64_t)head0 * hd;
-    lse = p.lse ? p.lse + (int64_t)r * p.heads + head0 : nullptr;
+          (int64_t)h.first * hd;
+    lse = p.lse ? p.lse + (int64_t)r * p.heads + h.first : nullptr;
   }
   // Lane: columns (heads) 2 (lane & 3) and + 1 of head tile nt.  The
   // accumulators o of channel tile mt (rows lane / 4 and + 8) times inv.
@@ -514,24 +538,28 @@ __device__ __forceinline__ void join_parts(int n, F at,
 // NT: tiles of eight query heads that a warp keeps.  kCluster: a cluster of
 // blocks takes one item, else all items are dealt out to kCtas blocks.
 template <class T, int HD, int NT, bool kCluster>
-__global__ void __launch_bounds__(warps_of(HD, NT) * 32, 1)
+__global__ void __launch_bounds__(warps_of(HD, NT, kCluster) * 32, 1)
     attend_kernel(const __grid_constant__ AttendParams p) {
-  using L = Smem<HD, NT>;
+  using L = Smem<HD, NT, kCluster>;
   constexpr int W = L::W, S = L::S, kThreads = W * 32;
   constexpr int MT = HD / 16;               // channel tiles of 16
-  constexpr int kPage = HD * 32;            // bytes of one page of K or V
+  constexpr int kPage = page_bytes(HD);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int gid = lane >> 2, tig = lane & 3;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBars) + warp * S;
+  // a barrier for K and the queries of each page in the ring, one for V
+  uint64_t* k_bars = reinterpret_cast<uint64_t*>(smem + L::kBars) +
+                     warp * 2 * S;
+  uint64_t* v_bars = k_bars + S;
   UnitMeta* metas = reinterpret_cast<UnitMeta*>(smem + L::kMeta) + warp * S;
   int64_t* prefix = reinterpret_cast<int64_t*>(smem + L::kPrefix);
   PartRec* recs = reinterpret_cast<PartRec*>(smem + L::kRecs);
-  float* ring_slot = reinterpret_cast<float*>(smem + warp * S *
-                                                         stage_bytes(HD));
-  float* own_slot = reinterpret_cast<float*>(smem + L::kParts +
-                                             warp * L::kSlot);
+  // where a warp leaves its part of an item: one that goes on behind its run
+  // (1), or one that ended in it (0)
+  auto slot_at = [&](int w, int goes_on) {
+    return goes_on || kCluster ? w * L::kRing : L::kParts + w * L::kSlot;
+  };
   int64_t* warp_sums = reinterpret_cast<int64_t*>(smem + L::kMisc);
   volatile int* abort_flag =
       reinterpret_cast<volatile int*>(smem + L::kMisc + 128);
@@ -541,7 +569,7 @@ __global__ void __launch_bounds__(warps_of(HD, NT) * 32, 1)
 
   // the next launch's blocks may take their places: they wait for this grid
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (lane < S) mbar_init(bars + lane, 1);
+  if (lane < 2 * S) mbar_init(k_bars + lane, 1);
   if (lane == 0) {
     recs[warp * 2].r = recs[warp * 2 + 1].r = -1;
     heads_ready[warp] = 0;
@@ -572,7 +600,7 @@ __global__ void __launch_bounds__(warps_of(HD, NT) * 32, 1)
     // Units of the requests before each thread's run of requests.
     const int per = (p.R + kThreads - 1) / kThreads;
     int64_t sum = 0;
-  #pragma unroll 1
+#pragma unroll 1
     for (int i = 0; i < per; ++i) {
       const int r = tid * per + i;
       if (r >= p.R) break;
@@ -582,7 +610,7 @@ __global__ void __launch_bounds__(warps_of(HD, NT) * 32, 1)
         atomicOr(p.flags, KVTC_FLAG_SPACE);
     }
     int64_t upto = sum;
-  #pragma unroll
+#pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const int64_t o = __shfl_up_sync(0xFFFFFFFFu, upto, d);
       if (lane >= d) upto += o;
@@ -590,7 +618,7 @@ __global__ void __launch_bounds__(warps_of(HD, NT) * 32, 1)
     if (lane == 31) warp_sums[warp] = upto;
     __syncthreads();
     total = 0;
-  #pragma unroll
+#pragma unroll
     for (int w = 0; w < W; ++w) {
       if (w < warp) upto += warp_sums[w];
       total += warp_sums[w];
@@ -618,9 +646,11 @@ __global__ void __launch_bounds__(warps_of(HD, NT) * 32, 1)
     cur_s = prefix[before - 1];
   }
 
-  const uint32_t ring = smem_u32(smem) + warp * S * stage_bytes(HD);
+  const uint32_t ring = smem_u32(smem) + warp * L::kRing;
+  const uint32_t queries = smem_u32(smem) + L::kQuery +
+                           warp * L::kQueries * query_bytes(HD, NT);
   // Lane j's unit of the batch of 32 being issued.
-  int b_r = 0, b_page = 0, b_len = 0, b_id = -1;
+  int b_r = 0, b_page = 0, b_len = 0, b_id = -1, b_slab = 0;
   uint32_t b_sub = 0;
   auto fill = [&](int i) {
     const int64_t u = u0 + i + lane;
@@ -661,7 +691,7 @@ __global__ void __launch_bounds__(warps_of(HD, NT) * 32, 1)
     cur_r = __shfl_sync(0xFFFFFFFFu, r, last);
     cur_s = __shfl_sync(0xFFFFFFFFu, s, last);
   };
-  auto issue = [&](int i, int st) {
+  auto issue_k = [&](int i, int st) {
     if ((i & 31) == 0) fill(i);
     if (lane == (i & 31)) {
       UnitMeta m;
@@ -670,18 +700,39 @@ __global__ void __launch_bounds__(warps_of(HD, NT) * 32, 1)
       m.page = b_page;
       m.len = b_len;
       metas[st] = m;
-      if (b_sub & kSkip) {
-        mbar_arrive(bars + st);
+      const uint32_t sub = b_sub & kSubMask;
+      const bool page = !(b_sub & kSkip);
+      const uint32_t dst = ring + st * L::kStage;
+      const int j = p.tiles == 1 ? (int)sub : (int)sub / p.tiles;
+      b_slab = j * (HD / 64);
+      if (!kCluster && (i == 0 || (b_sub & kFirst))) {
+        // the rows of an item's query heads are consecutive
+        const Heads h(p, sub);
+        const uint32_t bytes = (uint32_t)h.rows * HD * 2;
+        mbar_arrive_expect_tx(k_bars + st, bytes + (page ? kPage : 0));
+        bulk_load(queries + st * query_bytes(HD, NT),
+                  static_cast<const T*>(p.q) + (int64_t)b_r * p.q_ld +
+                      (int64_t)h.first * HD,
+                  bytes, k_bars + st);
+      } else if (page) {
+        mbar_arrive_expect_tx(k_bars + st, kPage);
       } else {
-        int slab = (int)(b_sub & kSubMask) * (HD / 64);
-        if (p.tiles != 1) slab = (int)(b_sub & kSubMask) / p.tiles * (HD / 64);
-        const uint32_t dst = ring + st * stage_bytes(HD);
-        mbar_arrive_expect_tx(bars + st, 2 * kPage);
-        tma_load_page(dst, &p.tm_k, slab, b_id, bars + st);
-        tma_load_page(dst + kPage, &p.tm_v, slab, b_id, bars + st);
+        mbar_arrive(k_bars + st);
       }
+      if (page) tma_load_page(dst, &p.tm_k, b_slab, b_id, k_bars + st);
     }
     __syncwarp();
+  };
+  auto issue_v = [&](int i, int st) {
+    if (lane == (i & 31)) {
+      if (b_sub & kSkip) {
+        mbar_arrive(v_bars + st);
+      } else {
+        mbar_arrive_expect_tx(v_bars + st, kPage);
+        tma_load_page(ring + st * L::kStage + kPage, &p.tm_v, b_slab, b_id,
+                      v_bars + st);
+      }
+    }
   };
 
   // ldmatrix addresses inside a page: the row of this lane and its 128-byte
@@ -697,41 +748,66 @@ __global__ void __launch_bounds__(warps_of(HD, NT) * 32, 1)
   float m_run[NT][2], limit[NT][2], l_run[NT][2];
   bool begun = false;          // the current item began in this run
   int64_t item_begin = 0;
-  int pending = 0;             // kept across the loop for the drain below
+  int k_used = 0, v_used = 0;  // pages waited for
 
-  // Turn c uses unit c and then asks for unit c + S, which takes its place in
-  // the ring; the first S turns only ask.
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    const bool ok =
+        __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort_flag));
+    if (!ok) *abort_flag = 1;
+    return ok;
+  };
+
+  // Turn c uses unit c and asks for unit c + S in its place, for K as soon as
+  // the scores are formed and for V at the end; the first S turns only ask.
   int st = S - 1;
   uint32_t phase = 0;
   UnitMeta meta = {0, 0u, 0, 0};
+  float sc[NT][4];
   for (int c = n ? -S : 0; c < n; ++c) {
     if (++st == S) {
       st = 0;
       phase ^= 1;
     }
+    const uint32_t kp = ring + st * L::kStage, vp = kp + kPage;
     if (c >= 0) {
-    meta = metas[st];
-    const uint32_t sub = meta.sub & kSubMask;
-    if (c == 0 || (meta.sub & kFirst)) {
+      meta = metas[st];
+      if (kCluster && c == 0) {
+        // (these loads are under way while the page is waited for)
+        const Heads h(p, fixed_sub);
+        const T* q = static_cast<const T*>(p.q) + (int64_t)cur_r * p.q_ld +
+                     (int64_t)h.first * HD;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const bool in = nt * 8 + gid < h.rows;
+          const uint32_t* row = reinterpret_cast<const uint32_t*>(
+              q + (int64_t)(nt * 8 + gid) * HD + tig * 2);
+#pragma unroll
+          for (int ks = 0; ks < MT; ++ks) {
+            qf[ks][nt][0] = in ? __ldg(row + ks * 8) : 0u;
+            qf[ks][nt][1] = in ? __ldg(row + ks * 8 + 4) : 0u;
+          }
+        }
+      }
+      if (!wait(k_bars + st, phase)) break;
+      k_used = c + 1;
+    }
+    if (c >= 0 && (c == 0 || (meta.sub & kFirst))) {
       begun = meta.sub & kFirst;
       item_begin = u0 + c;
-      if (!begun) {
-        const Span sp = span_of(p, meta.r);
-        item_begin -= meta.page < sp.front ? meta.page : meta.page - sp.gap;
-      }
-      int head0, rows;
-      head_range(p, sub, &head0, &rows);
-      const T* q = static_cast<const T*>(p.q) + (int64_t)meta.r * p.q_ld +
-                   (int64_t)head0 * HD;
+      const int rows = Heads(p, meta.sub & kSubMask).rows;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const bool in = nt * 8 + gid < rows;
-        const uint32_t* row = reinterpret_cast<const uint32_t*>(
-            q + (int64_t)(nt * 8 + gid) * HD + tig * 2);
 #pragma unroll
-        for (int ks = 0; ks < MT; ++ks) {
-          qf[ks][nt][0] = in ? __ldg(row + ks * 8) : 0u;
-          qf[ks][nt][1] = in ? __ldg(row + ks * 8 + 4) : 0u;
+        for (int ks = 0; !kCluster && ks < MT; ks += 2) {
+          uint32_t b[4];
+          ldsm4(b, queries + st * query_bytes(HD, NT) +
+                       (nt * 8 + (lane & 7)) * (HD * 2) + ks * 32 +
+                       (lane >> 3) * 16);
+          qf[ks][nt][0] = in ? b[0] : 0u;
+          qf[ks][nt][1] = in ? b[1] : 0u;
+          qf[ks + 1][nt][0] = in ? b[2] : 0u;
+          qf[ks + 1][nt][1] = in ? b[3] : 0u;
         }
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
@@ -742,19 +818,11 @@ __global__ void __launch_bounds__(warps_of(HD, NT) * 32, 1)
         l_run[nt][0] = l_run[nt][1] = 0.f;
       }
     }
-    // (the query's loads are under way while the page is waited for)
-    if (!__all_sync(0xFFFFFFFFu,
-                    mbar_wait(bars + st, phase, abort_flag))) {
-      *abort_flag = 1;
-      break;
-    }
-    pending = c + 1;
-
-    if (!(meta.sub & kSkip)) {
-      const uint32_t kp = ring + st * stage_bytes(HD), vp = kp + kPage;
+    const bool use = c >= 0 && !(meta.sub & kSkip);
+    if (use) {
       // S^T, in two chains where there is one head tile
       constexpr int kChains = NT == 1 ? 2 : 1;
-      float sc[NT][4], sd[4] = {0.f, 0.f, 0.f, 0.f};
+      float sd[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
         sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
@@ -768,6 +836,16 @@ __global__ void __launch_bounds__(warps_of(HD, NT) * 32, 1)
           Elem<T>::mma(kChains == 2 && (ks & 1) ? sd : sc[nt], a,
                        qf[ks][nt][0], qf[ks][nt][1]);
       }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          sc[nt][i] = (kChains == 2 ? sc[nt][i] + sd[i] : sc[nt][i]) *
+                      p.scale_log2;
+    }
+    __syncwarp();
+    if (c + S < n) issue_k(c + S, st);
+    if (use) {
       const bool whole = meta.sub & kWhole;
       const int t0 = meta.page * kBlock;
       const int recent = p.window ? meta.len - p.window : 0;
@@ -778,12 +856,9 @@ __global__ void __launch_bounds__(warps_of(HD, NT) * 32, 1)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          sc[nt][i] = (kChains == 2 ? sc[nt][i] + sd[i] : sc[nt][i]) *
-                      p.scale_log2;
+        for (int i = 0; i < 4; ++i)
           if (!whole && !seen(t0 + gid + (i >> 1) * 8))
             sc[nt][i] = -INFINITY;
-        }
       // The reference that exponents are taken from moves only when a score
       // lies kSlack above it: the maximum over the lanes (six shuffles in
       // chains of three) and the rescaling are seldom needed.
@@ -862,12 +937,13 @@ __global__ void __launch_bounds__(warps_of(HD, NT) * 32, 1)
           }
         }
       };
+      if (!wait(v_bars + st, phase)) break;
       if (whole) pv(std::false_type{}); else pv(std::true_type{});
     }
-    }
     __syncwarp();
-    if (c + S < n) issue(c + S, st);
+    if (c + S < n) issue_v(c + S, st);
     if (c < 0) continue;
+    v_used = c + 1;
 
     const uint32_t sub = meta.sub & kSubMask;
     const bool ended = meta.sub & kLast;
@@ -886,7 +962,8 @@ __global__ void __launch_bounds__(warps_of(HD, NT) * 32, 1)
       // The item ends in the next warp's run, which has left that part (it
       // came first there): join it here, where the accumulators are.
       __threadfence_block();
-      const float* slot = own_slot + L::kSlot / 4;
+      const float* slot =
+          reinterpret_cast<const float*>(smem + slot_at(warp + 1, 0));
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const float* stat = slot + NT * 8 * HD + nt * 8 + tig * 2;
@@ -930,7 +1007,8 @@ __global__ void __launch_bounds__(warps_of(HD, NT) * 32, 1)
       }
       continue;
     }
-    float* slot = ended ? own_slot : ring_slot;
+    float* slot =
+        reinterpret_cast<float*>(smem + slot_at(warp, ended ? 0 : 1));
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -950,11 +1028,13 @@ __global__ void __launch_bounds__(warps_of(HD, NT) * 32, 1)
       if (lane == 0) heads_ready[warp] = 1;
     }
   }
-  if (pending < n) {
+  if (v_used < n) {
     // a wait ran out: report it, and let the loads in flight land
     if (lane == 0 && p.flags) atomicOr(p.flags, KVTC_FLAG_TIMEOUT);
-    for (int c = pending; c < min(n, pending + S); ++c)
-      mbar_drain(bars + c % S, (c / S) & 1);
+    for (int c = v_used; c < min(n, v_used + S); ++c)
+      mbar_drain(v_bars + c % S, (c / S) & 1);
+    for (int c = k_used; c < min(n, k_used + S); ++c)
+      mbar_drain(k_bars + c % S, (c / S) & 1);
   }
   __syncthreads();
 
@@ -987,10 +1067,7 @@ __global__ void __launch_bounds__(warps_of(HD, NT) * 32, 1)
     const bool begun_here = __shfl_sync(0xFFFFFFFFu, rec.sub, e0) & kFirst;
     const bool ended_here = __shfl_sync(0xFFFFFFFFu, rec.sub, e1) & kLast;
     // its parts: entry 1 of consecutive warps, and last what it is
-    auto slot_of = [&](int e) {
-      return smem_at + ((e & 1) ? (e >> 1) * S * stage_bytes(HD)
-                                : L::kParts + (e >> 1) * L::kSlot);
-    };
+    auto slot_of = [&](int e) { return smem_at + slot_at(e >> 1, e & 1); };
     float* to = nullptr;
     if (!(begun_here && ended_here))
       to = kCluster ? reinterpret_cast<float*>(smem + L::kBlockPart)
@@ -1006,7 +1083,7 @@ __global__ void __launch_bounds__(warps_of(HD, NT) * 32, 1)
         k,
         [=](int i) {
           return i == 0 ? first
-                 : i == k - 1 ? last : base + i * (S * stage_bytes(HD));
+                 : i == k - 1 ? last : base + i * L::kRing;
         },
         target, to, warp - w, share);
   }
@@ -1152,24 +1229,24 @@ __global__ void __launch_bounds__(HD / 16 * NT * 32 *
 template <class T, int HD, int NT>
 cudaError_t launch_as(const AttendParams& p, int cluster, int device,
                       cudaStream_t st) {
-  constexpr int kThreads = warps_of(HD, NT) * 32;
-  constexpr int kBytes = Smem<HD, NT>::kBytes;
   static std::atomic<uint64_t> ready[2];     // devices, as bits
   cudaError_t e;
   if (cluster) {
     const auto kernel = attend_kernel<T, HD, NT, true>;
-    e = allow_smem(kernel, kBytes, device, ready[0], true);
+    using L = Smem<HD, NT, true>;
+    e = allow_smem(kernel, L::kBytes, device, ready[0], true);
     if (e == cudaSuccess)
       e = launch_kernel(kernel,
                         (unsigned)(p.R * p.kv_heads * p.tiles * cluster),
-                        kThreads, kBytes, st, true, cluster, p);
+                        L::W * 32, L::kBytes, st, true, cluster, p);
     if (e == cudaSuccess) count_launch();
     return e;
   }
   const auto kernel = attend_kernel<T, HD, NT, false>;
-  e = allow_smem(kernel, kBytes, device, ready[1]);
+  using L = Smem<HD, NT, false>;
+  e = allow_smem(kernel, L::kBytes, device, ready[1]);
   if (e == cudaSuccess)
-    e = launch_kernel(kernel, kCtas, kThreads, kBytes, st, true, 0, p);
+    e = launch_kernel(kernel, kCtas, L::W * 32, L::kBytes, st, true, 0, p);
   if (e != cudaSuccess) return e;
   count_launch();
   constexpr int kTiles = HD / 16 * NT;
@@ -1187,15 +1264,16 @@ cudaError_t launch_as(const AttendParams& p, int cluster, int device,
 // at about 90 GB/s a block, may read slower than all SMs at 7000 GB/s, which
 // is taken at the longest length that the table allows, for the others half
 // of that.
-int cluster_of(int64_t items, int64_t max_blocks, int head_dim, int nt) {
+int cluster_of(int R, int64_t items, int64_t max_blocks, int head_dim,
+               int nt) {
   if (items > kCtas) return 0;
   int cluster = items <= 7 ? 16 : items <= 15 ? 8 : items <= 36 ? 4
                 : items <= 76 ? 2 : 1;
-  const int64_t feeds = (int64_t)warps_of(head_dim, nt) * kLeast;
+  const int64_t feeds = (int64_t)warps_of(head_dim, nt, true) * kLeast;
   while (cluster > 1 && max_blocks <= feeds * (cluster / 2)) cluster /= 2;
-  const double bytes = (double)max_blocks * stage_bytes(head_dim);
-  const double others = items == 1 ? 1.0 : 0.5 + 0.5 / (double)items;
-  return bytes / (90.0 * cluster) - others * bytes * items / 7000.0 <= 6000.0
+  const double bytes = 2.0 * (double)max_blocks * page_bytes(head_dim);
+  const double others = R == 1 ? 1.0 : 0.5 + 0.5 / R;
+  return bytes / (90.0 * cluster) - others * bytes * items / 7000.0 <= 3000.0
              ? cluster
              : 0;
 }
@@ -1332,8 +1410,8 @@ int kvtc_paged_attend(int cuda_device, int R, int heads, int kv_heads,
   p.group = group;
   p.tiles = (group + 8 * nt - 1) / (8 * nt);
   p.tile_heads = (group + p.tiles - 1) / p.tiles;
-  const int cluster = cluster_of((int64_t)R * kv_heads * p.tiles, max_blocks,
-                                 head_dim, nt);
+  const int cluster = cluster_of(R, (int64_t)R * kv_heads * p.tiles,
+                                 max_blocks, head_dim, nt);
   cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
   const cudaError_t e = dtype == KVTC_DTYPE_BF16
                             ? launch<__nv_bfloat16>(p, head_dim, nt, cluster,

@@ -246,6 +246,13 @@ def test_bad_block_ids_are_left_out_and_flagged(kv):
     a.call()
     a.check(flags=a.kv.KVTC_FLAG_BLOCK)
     assert (a.out[3, :a.width] == 0).all()
+    # the first block of longer requests, and all but the last
+    for cut in (slice(0, 1), slice(0, 6)):
+        table = clean.copy()
+        table[0, cut] = -1
+        c = Attend(kv, q, k, v, table, lens)
+        c.call()
+        c.check(flags=a.kv.KVTC_FLAG_BLOCK)
     # the flag is not set without one
     b = Attend(kv, q, k, v, clean, lens)
     b.call()
