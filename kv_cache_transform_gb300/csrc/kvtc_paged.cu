@@ -4,10 +4,12 @@
 // new blocks per request, cu is the exclusive sum of n, C the inclusive sum
 // of b, and request r takes free[head + C_r - b_r ...] if it fits.  Both are
 // integer sums, so the result is exact and does not depend on the launch.
-//   assign_scan_kernel  one block of 1024 threads, four consecutive requests
-//                       each: the two sums, who is served, head and held.
-//   assign_fill_kernel  the block-table columns and the slot map.
-// kvtc_paged_append: append_kernel copies 16-byte pieces of rows.
+//   few new tokens (decode steps): assign_small_kernel, one block, a thread
+//     per request: one launch, a chain of three loads.
+//   many: assign_scan_kernel, one block, forms the sums, and
+//     assign_fill_kernel, launched behind on the whole GPU, writes the table
+//     entries and the slots.
+// kvtc_paged_append: append_kernel, a warp per row.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -31,7 +33,7 @@ __host__ __device__ __forceinline__ int64_t blocks_of(int64_t tokens) {
 }
 
 // What the fill pass needs of a request, in the workspace.
-struct AssignRow {
+struct __align__(16) AssignRow {
   int64_t first;      // free-list index of its first new block
   int32_t held;       // tokens that had blocks
   int32_t blocks;     // new blocks; -1 where it is not served
@@ -55,119 +57,260 @@ struct AssignParams {
   int32_t max_blocks;
 };
 
-__device__ __forceinline__ int64_t warp_inclusive(int64_t v, int lane) {
+// A request's demand.
+struct Demand {
+  int32_t held, lens;
+  int64_t fresh;      // new tokens
+  int32_t need;       // new blocks, 0 where they cannot fit the table
+  bool fits;
+  __device__ __forceinline__ Demand(const AssignParams& p, int r) {
+    held = r < p.R ? max(p.held[r], 0) : 0;
+    lens = r < p.R ? max(p.lens[r], 0) : 0;
+    fresh = max((int64_t)lens - held, (int64_t)0);
+    fits = lens <= (int64_t)p.max_blocks * kBlock;
+    need = fresh && fits ? (int32_t)(blocks_of(lens) - blocks_of(held)) : 0;
+  }
+};
+
+// Inclusive sums over the block's threads of two values each; `total` of the
+// first.  sums: shared, two per warp.
+__device__ __forceinline__ void block_sums(int64_t& a, int64_t& b,
+                                           int64_t* sums, int64_t* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int warps = blockDim.x >> 5;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const int64_t o = __shfl_up_sync(0xFFFFFFFFu, v, d);
-    if (lane >= d) v += o;
+    const int64_t x = __shfl_up_sync(0xFFFFFFFFu, a, d);
+    const int64_t y = __shfl_up_sync(0xFFFFFFFFu, b, d);
+    if (lane >= d) {
+      a += x;
+      b += y;
+    }
   }
-  return v;
+  if (lane == 31) {
+    sums[2 * warp] = a;
+    sums[2 * warp + 1] = b;
+  }
+  __syncthreads();
+  // each warp adds up the warps before it
+  int64_t x = lane < warps ? sums[2 * lane] : 0;
+  int64_t y = lane < warps ? sums[2 * lane + 1] : 0;
+  int64_t all = x;
+  if (lane >= warp) x = y = 0;
+#pragma unroll
+  for (int d = 16; d; d >>= 1) {
+    x += __shfl_xor_sync(0xFFFFFFFFu, x, d);
+    y += __shfl_xor_sync(0xFFFFFFFFu, y, d);
+    all += __shfl_xor_sync(0xFFFFFFFFu, all, d);
+  }
+  a += x;
+  b += y;
+  *total = all;
 }
 
-__global__ void __launch_bounds__(kScanThreads)
-    assign_scan_kernel(const AssignParams p) {
-  __shared__ int64_t warp_new[32], warp_need[32];
+__device__ __forceinline__ int64_t free_left(const AssignParams& p,
+                                             int64_t head, bool* ok) {
+  *ok = head >= 0 && head <= p.n_free;
+  return *ok ? p.n_free - head : 0;
+}
+
+__device__ __forceinline__ int64_t slot_of(int64_t id, int64_t t) {
+  return id >= 0 ? id * kBlock + t % kBlock : -1;
+}
+
+// One block, a thread per request (R <= 1024).  Where a request has few new
+// tokens its thread writes their slots, else the warps share them.
+constexpr int kSmallReq = 1024;
+constexpr int64_t kSmallSlots = 8192;
+constexpr int kSmallOwn = 4;         // tokens that a thread writes itself
+__global__ void __launch_bounds__(kSmallReq)
+    assign_small_kernel(const __grid_constant__ AssignParams p) {
+  __shared__ int64_t sums[64];
   __shared__ unsigned long long given;   // blocks given out
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (tid == 0) given = 0;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int r = threadIdx.x, lane = r & 31;
+  if (r == 0) given = 0;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const Demand d(p, r);
   const int64_t head = *p.head;
-  const bool head_ok = head >= 0 && head <= p.n_free;
-  const int64_t avail = head_ok ? p.n_free - head : 0;
-  int64_t fresh[kScanPer], need[kScanPer];
-  int32_t held[kScanPer], lens[kScanPer];
-  int64_t sum_new = 0, sum_need = 0;
+  bool head_ok;
+  const int64_t left = free_left(p, head, &head_ok);
+  // the block that the first new token continues, asked for ahead
+  const int32_t had = (int32_t)blocks_of(d.held);
+  int32_t* row = p.table + (int64_t)r * p.max_blocks;
+  int32_t open = -1;
+  if (d.fresh && d.fits && d.held % kBlock) open = row[had - 1];
+  int64_t upto = d.fresh, used = d.need, total;
+  block_sums(upto, used, sums, &total);
+  const bool served = d.fits && (d.need == 0 || used <= left);
+  const int64_t first = head + used - d.need;
+  const int64_t at = upto - d.fresh;
+  bool short_of = r == 0 && (!head_ok || total > p.slot_capacity);
+  if (r < p.R) {
+    p.cu[r] = at;
+    p.held_out[r] = served ? max(d.held, d.lens) : d.held;
+    if (served && d.need) atomicMax(&given, (unsigned long long)used);
+    short_of |= !served && d.fresh;
+  }
+  if (r == 0) p.cu[p.R] = total;
+  if (short_of && p.flags) atomicOr(p.flags, KVTC_FLAG_SPACE);
+  // A request's new table entries, and the slots of its tokens as far as the
+  // map goes: entries or tokens k, k + step, ...
+  auto write = [&](int32_t held, int32_t open, int64_t fresh, int32_t blocks,
+                   int64_t first, int64_t at, int32_t* row, int k, int step) {
+    const int64_t had = blocks_of(held);
+    for (int i = k; i < blocks; i += step)
+      row[had + i] = p.free_blocks[first + i];
+    fresh = min(fresh, p.slot_capacity - at);
+    for (int64_t i = k; i < fresh; i += step) {
+      const int64_t t = held + i, b = t / kBlock;
+      int64_t slot = -1;
+      if (blocks >= 0)
+        slot = slot_of(b < had ? open : p.free_blocks[first + (b - had)], t);
+      p.slots[at + i] = slot;
+    }
+  };
+  const int32_t blocks = served ? d.need : -1;
+  const bool own = d.fresh <= kSmallOwn;
+  if (own) write(d.held, open, d.fresh, blocks, first, at, row, 0, 1);
+  // the others, of one lane after the other
+  for (uint32_t m = __ballot_sync(0xFFFFFFFFu, !own); m; m &= m - 1) {
+    const int l = __ffs(m) - 1;
+    write(__shfl_sync(0xFFFFFFFFu, d.held, l),
+          __shfl_sync(0xFFFFFFFFu, open, l),
+          __shfl_sync(0xFFFFFFFFu, d.fresh, l),
+          __shfl_sync(0xFFFFFFFFu, blocks, l),
+          __shfl_sync(0xFFFFFFFFu, first, l),
+          __shfl_sync(0xFFFFFFFFu, at, l),
+          p.table + (int64_t)((r & ~31) + l) * p.max_blocks, lane, 32);
+  }
+  for (int64_t j = total + r; j < p.slot_capacity; j += blockDim.x)
+    p.slots[j] = -1;
+  __syncthreads();
+  if (r == 0) *p.head_out = head + (int64_t)given;
+}
+
+// One block, kScanPer consecutive requests per thread.
+__global__ void __launch_bounds__(kScanThreads)
+    assign_scan_kernel(const __grid_constant__ AssignParams p) {
+  __shared__ int64_t sums[64];
+  __shared__ unsigned long long given;   // blocks given out
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int tid = threadIdx.x;
+  if (tid == 0) given = 0;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int64_t head = *p.head;
+  bool head_ok;
+  const int64_t left = free_left(p, head, &head_ok);
+  int64_t fresh = 0, need = 0, total;
 #pragma unroll
   for (int i = 0; i < kScanPer; ++i) {
-    const int r = tid * kScanPer + i;
-    held[i] = r < p.R ? max(p.held[r], 0) : 0;
-    lens[i] = r < p.R ? max(p.lens[r], 0) : 0;
-    fresh[i] = max((int64_t)lens[i] - held[i], (int64_t)0);
-    const bool fits = lens[i] <= (int64_t)p.max_blocks * kBlock;
-    need[i] = fresh[i] && fits ? blocks_of(lens[i]) - blocks_of(held[i]) : 0;
-    sum_new += fresh[i];
-    sum_need += need[i];
+    const Demand d(p, tid * kScanPer + i);
+    fresh += d.fresh;
+    need += d.need;
   }
-  int64_t in_new = warp_inclusive(sum_new, lane);
-  int64_t in_need = warp_inclusive(sum_need, lane);
-  if (lane == 31) {
-    warp_new[warp] = in_new;
-    warp_need[warp] = in_need;
-  }
-  __syncthreads();
-  if (warp == 0) {
-    warp_new[lane] = warp_inclusive(warp_new[lane], lane);
-    warp_need[lane] = warp_inclusive(warp_need[lane], lane);
-  }
-  __syncthreads();
-  if (warp) {
-    in_new += warp_new[warp - 1];
-    in_need += warp_need[warp - 1];
-  }
-  int64_t at_new = in_new - sum_new, at_need = in_need - sum_need;
-  bool short_of = tid == 0 && !head_ok;
+  int64_t upto = fresh, used = need;
+  block_sums(upto, used, sums, &total);
+  upto -= fresh;
+  used -= need;
+  bool short_of = tid == 0 && (!head_ok || total > p.slot_capacity);
 #pragma unroll
   for (int i = 0; i < kScanPer; ++i) {
     const int r = tid * kScanPer + i;
     if (r >= p.R) break;
-    p.cu[r] = at_new;
-    at_new += fresh[i];
-    at_need += need[i];
-    const bool served = lens[i] <= (int64_t)p.max_blocks * kBlock &&
-                        (need[i] == 0 || at_need <= avail);
+    const Demand d(p, r);
+    p.cu[r] = upto;
+    upto += d.fresh;
+    used += d.need;
+    const bool served = d.fits && (d.need == 0 || used <= left);
     AssignRow row;
-    row.first = head + at_need - need[i];
-    row.held = held[i];
-    row.blocks = served ? (int32_t)need[i] : -1;
+    row.first = head + used - d.need;
+    row.held = d.held;
+    row.blocks = served ? d.need : -1;
     p.rows[r] = row;
-    p.held_out[r] = served ? max(held[i], lens[i]) : held[i];
-    if (served && need[i]) atomicMax(&given, (unsigned long long)at_need);
-    short_of |= !served && fresh[i];
-    if (r == p.R - 1) {
-      p.cu[p.R] = at_new;
-      short_of |= at_new > p.slot_capacity;
-    }
+    // (a request's held is read for the last time above)
+    p.held_out[r] = served ? max(d.held, d.lens) : d.held;
+    if (served && d.need) atomicMax(&given, (unsigned long long)used);
+    short_of |= !served && d.fresh;
   }
   if (short_of && p.flags) atomicOr(p.flags, KVTC_FLAG_SPACE);
   __syncthreads();
   if (tid == 0) {
+    p.cu[p.R] = total;
     *p.head_out = head + (int64_t)given;
-    if (p.R == 0) p.cu[0] = 0;
   }
 }
 
-__global__ void __launch_bounds__(256)
-    assign_fill_kernel(const AssignParams p) {
-  const int64_t tid = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  const int64_t threads = (int64_t)gridDim.x * blockDim.x;
+// Last request r in [lo, hi] with cu[r] <= j (cu[lo] <= j); the whole warp
+// looks, 32 places at a time.
+__device__ __forceinline__ int request_at(const int64_t* cu, int lo, int hi,
+                                          int64_t j) {
   const int lane = threadIdx.x & 31;
-  for (int64_t r = tid >> 5; r < p.R; r += threads >> 5) {
+  while (lo < hi) {
+    const int step = (hi - lo + 31) / 32;
+    const int at = lo + 1 + lane * step;
+    const bool in = at <= hi && cu[at] <= j;
+    const int n = __popc(__ballot_sync(0xFFFFFFFFu, in));
+    if (n == 0) return lo;
+    lo += 1 + (n - 1) * step;
+    hi = min(hi, lo + step - 1);
+  }
+  return lo;
+}
+
+// Slots and new table entries.  A warp takes runs of 256 tokens, finds their
+// first and last request once, and each lane walks from there: tokens mostly
+// lie many to a request.
+constexpr int kFillRun = 256;
+__global__ void __launch_bounds__(256)
+    assign_fill_kernel(const __grid_constant__ AssignParams p) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int lane = threadIdx.x & 31;
+  const int64_t warp = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+  const int64_t warps = ((int64_t)gridDim.x * blockDim.x) >> 5;
+  for (int64_t r = warp; r < p.R; r += warps) {
     const AssignRow row = p.rows[r];
     int32_t* to = p.table + r * p.max_blocks + blocks_of(row.held);
     for (int i = lane; i < row.blocks; i += 32)
       to[i] = p.free_blocks[row.first + i];
   }
-  const int64_t total = p.R ? p.cu[p.R] : 0;
-  for (int64_t j = tid; j < p.slot_capacity; j += threads) {
-    int64_t slot = -1;
-    if (j < total) {
-      // the last request whose first new token is at or before j; of
-      // several (requests with no new token) the one that holds j
-      int lo = 0, hi = p.R - 1;
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (p.cu[mid] <= j) lo = mid; else hi = mid - 1;
+  const int64_t total = p.cu[p.R];
+  for (int64_t j0 = warp * kFillRun; j0 < p.slot_capacity;
+       j0 += warps * kFillRun) {
+    int r = 0;
+    if (j0 < total) r = request_at(p.cu, 0, p.R - 1, j0);
+    AssignRow row = {0, 0, -1};
+    int64_t from = 0, to = 0;      // tokens of request r; none looked up yet
+#pragma unroll
+    for (int k = 0; k < kFillRun / 32; ++k) {
+      const int64_t j = j0 + k * 32 + lane;
+      int64_t slot = -1;
+      if (j < total && j < p.slot_capacity) {
+        if (j >= to) {
+          if (p.cu[r + 1] <= j && p.cu[++r + 1] <= j) {
+            int hi = p.R - 1;
+            while (r < hi) {
+              const int mid = (r + hi + 1) >> 1;
+              if (p.cu[mid] <= j) r = mid; else hi = mid - 1;
+            }
+          }
+          row = p.rows[r];
+          from = p.cu[r];
+          to = p.cu[r + 1];
+        }
+        if (row.blocks >= 0) {
+          // (a new block's id from the list: its table entry may not be
+          // written yet)
+          const int64_t t = row.held + (j - from), b = t / kBlock;
+          const int64_t had = blocks_of(row.held);
+          slot = slot_of(b < had ? p.table[(int64_t)r * p.max_blocks + b]
+                                 : p.free_blocks[row.first + (b - had)],
+                         t);
+        }
       }
-      const AssignRow row = p.rows[lo];
-      if (row.blocks >= 0) {
-        const int64_t t = row.held + (j - p.cu[lo]);
-        const int64_t had = blocks_of(row.held), b = t / kBlock;
-        const int64_t id = b < had
-            ? p.table[(int64_t)lo * p.max_blocks + b]
-            : p.free_blocks[row.first + (b - had)];
-        if (id >= 0) slot = id * kBlock + t % kBlock;
-      }
+      if (j < p.slot_capacity) p.slots[j] = slot;
     }
-    p.slots[j] = slot;
   }
 }
 
@@ -184,23 +327,36 @@ struct AppendParams {
   int32_t nstreams;
 };
 
+// A warp per (stream, row): the row's slot once, its pieces 32 at a time with
+// four loads in flight a lane.  Bound by HBM: 8192 rows of K and V of 2 KB,
+// 67 MB moved.
 __global__ void __launch_bounds__(256)
     append_kernel(const __grid_constant__ AppendParams p) {
-  const int64_t total = p.N * p.nstreams * p.pieces;
-  const int64_t step = (int64_t)gridDim.x * blockDim.x;
-  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total;
-       i += step) {
-    const int64_t row = i / p.pieces;
-    const int c = (int)(i - row * p.pieces);
-    const int j = (int)(row / p.N);
-    const int64_t n = row - j * p.N;
-    const int64_t slot = p.slots[n];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int lane = threadIdx.x & 31;
+  const uint32_t warp = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  const uint32_t warps = gridDim.x * (blockDim.x >> 5);
+  const uint4* src = p.src[blockIdx.y];
+  uint4* cache = p.cache[blockIdx.y];
+  for (int64_t n = warp; n < p.N; n += warps) {
+    const int64_t slot = __ldg(p.slots + n);
+    const uint4* from = src + n * p.ld;
     if (slot < 0) continue;
     if (slot >= p.pool_rows) {
-      if (p.flags) atomicOr(p.flags, KVTC_FLAG_BLOCK);
+      if (lane == 0 && p.flags) atomicOr(p.flags, KVTC_FLAG_BLOCK);
       continue;
     }
-    p.cache[j][slot * p.pieces + c] = p.src[j][n * p.ld + c];
+    uint4* to = cache + slot * p.pieces;
+    for (int c0 = lane; c0 < p.pieces; c0 += 128) {
+      uint4 v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (c0 + i * 32 < p.pieces) v[i] = __ldg(from + c0 + i * 32);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (c0 + i * 32 < p.pieces) to[c0 + i * 32] = v[i];
+    }
   }
 }
 
@@ -237,7 +393,7 @@ int kvtc_paged_assign(int cuda_device, int R, const int32_t* held,
   if (workspace_bytes < kvtc_paged_assign_workspace_bytes(R))
     return KVTC_ESIZE;
   if (misaligned(head, 8) || misaligned(cu, 8) || misaligned(head_out, 8) ||
-      misaligned(slots, 8) || misaligned(workspace, 8) ||
+      misaligned(slots, 8) || !aligned16(workspace) ||
       misaligned(held, 4) || misaligned(lens, 4) ||
       misaligned(free_blocks, 4) || misaligned(block_table, 4) ||
       misaligned(held_out, 4) || misaligned(flags, 4))
@@ -261,19 +417,25 @@ int kvtc_paged_assign(int cuda_device, int R, const int32_t* held,
   p.flags = flags;
   p.R = R;
   p.max_blocks = max_blocks;
-  if (launch_kernel(assign_scan_kernel, 1, kScanThreads, 0, st, false, 0, p) !=
+  if (R <= kSmallReq && slot_capacity <= kSmallSlots) {
+    if (launch_kernel(assign_small_kernel, 1, std::max(32, (R + 31) / 32 * 32),
+                      0, st, true, 0, p) != cudaSuccess)
+      return KVTC_ECUDA;
+    count_launch();
+    return KVTC_OK;
+  }
+  if (launch_kernel(assign_scan_kernel, 1, kScanThreads, 0, st, true, 0, p) !=
       cudaSuccess)
     return KVTC_ECUDA;
   count_launch();
-  const int64_t want = std::max((slot_capacity + 255) / 256,
-                                ((int64_t)R * 32 + 255) / 256);
-  if (want) {
-    if (launch_kernel(assign_fill_kernel,
-                      (unsigned)std::min<int64_t>(want, 8 * 152), 256, 0, st,
-                      false, 0, p) != cudaSuccess)
-      return KVTC_ECUDA;
-    count_launch();
-  }
+  // (capacity is what the host knows of the tokens)
+  const int64_t runs = std::max<int64_t>(
+      (slot_capacity + kFillRun - 1) / kFillRun, 152 * 8);
+  if (launch_kernel(assign_fill_kernel,
+                    (unsigned)std::min<int64_t>((runs + 7) / 8, 8 * 152), 256,
+                    0, st, true, 0, p) != cudaSuccess)
+    return KVTC_ECUDA;
+  count_launch();
   return KVTC_OK;
 }
 
@@ -309,12 +471,11 @@ int kvtc_paged_append(int cuda_device, int nstreams, const void* const* src,
       p.src[j] = static_cast<const uint4*>(src[j0 + j]);
       p.cache[j] = static_cast<uint4*>(cache[j0 + j]);
     }
-    const int64_t total = N * p.nstreams * p.pieces;
-    if (launch_kernel(append_kernel,
-                      (unsigned)std::min<int64_t>((total + 255) / 256,
-                                                  8 * 152),
-                      256, 0, static_cast<cudaStream_t>(cuda_stream), false,
-                      0, p) != cudaSuccess)
+    const dim3 grid((unsigned)std::min<int64_t>((N + 7) / 8, 16 * 152),
+                    p.nstreams);
+    if (launch_kernel(append_kernel, grid, 256, 0,
+                      static_cast<cudaStream_t>(cuda_stream), true, 0, p) !=
+        cudaSuccess)
       return KVTC_ECUDA;
     count_launch();
   }

@@ -147,6 +147,50 @@ def test_assign_out_of_the_ordinary(kv, case):
     run_assign(kv, held, lens, free, head, table, cap)
 
 
+@pytest.mark.parametrize("R,cap", [(5, 40), (5, 9000), (1500, 7)])
+def test_assign_lengths_far_beyond_the_map(kv, R, cap):
+    """Lengths that no table row holds (here near 2^31) cost nothing, and
+    blocks are given to tokens that the slot map has no room for."""
+    lens = np.full(R, 30)
+    lens[1] = 2 ** 31 - 1
+    lens[3] = 2 ** 31 - 17
+    held = np.zeros(R, np.int64)
+    held[3] = 5
+    c = Assign(kv, held, lens, np.arange(2 * R), 0, np.full((R, 3), -1), cap)
+    c.call()
+    table = np.full((R, 3), -1)
+    ok = np.ones(R, bool)
+    ok[[1, 3]] = False
+    table[ok, :2] = np.arange(2 * (R - 2)).reshape(-1, 2)
+    np.testing.assert_array_equal(c.table.cpu().numpy(), table)
+    np.testing.assert_array_equal(
+        c.held_out.cpu().numpy(), np.where(ok, 30, held))
+    cu = np.concatenate([[0], np.cumsum(lens - held)])
+    np.testing.assert_array_equal(c.cu.cpu().numpy()[:R + 1], cu)
+    slots = np.full(cap, -1, np.int64)
+    n = min(cap, 30)
+    slots[:n] = np.arange(n)          # request 0: blocks 0 and 1
+    np.testing.assert_array_equal(c.slots.cpu().numpy()[:cap], slots)
+    assert int(c.flags.cpu()[0]) == kv.KVTC_FLAG_SPACE
+
+
+@pytest.mark.parametrize("R,hi", [(1024, 3), (1025, 3), (4096, 60), (600, 1),
+                                  (64, 128), (64, 129)])
+def test_assign_with_many_empty_requests(kv, R, hi):
+    """On both sides of the single launch's limits (1024 requests, 8192
+    slots), with long runs of requests that want nothing."""
+    rng = np.random.default_rng(R + hi)
+    lens = rng.integers(1, hi + 1, R)
+    lens[rng.integers(0, R, R // 2)] = 0
+    lens[R // 3:R // 3 + R // 4] = 0
+    if R == 64:
+        lens[:] = hi
+    held = np.zeros(R, np.int64)
+    free, head, table = start_state(rng, held, blocks_of(hi) + 1,
+                                    int(sum(blocks_of(n) for n in lens)) + 5)
+    run_assign(kv, held, lens, free, head, table, int(lens.sum()))
+
+
 @pytest.mark.parametrize("head", [-1, 6, 1 << 40])
 def test_assign_with_the_head_outside_the_list(kv, head):
     run_assign(kv, [0, 4], [5, 6], [3, 4, 5, 6, 7], head, [[1, 2], [3, 4]],

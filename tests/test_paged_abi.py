@@ -59,7 +59,7 @@ def attend(kv, **over):
     (dict(free=A + 2), "EALIGN"), (dict(head=A + 4), "EALIGN"),
     (dict(table=A + 2), "EALIGN"), (dict(slots=A + 4), "EALIGN"),
     (dict(cu=A + 4), "EALIGN"), (dict(held_out=A + 2), "EALIGN"),
-    (dict(head_out=A + 4), "EALIGN"), (dict(workspace=A + 4), "EALIGN"),
+    (dict(head_out=A + 4), "EALIGN"), (dict(workspace=A + 8), "EALIGN"),
     (dict(flags=A + 2), "EALIGN")])
 def test_assign_refusals(kv, over, code):
     assert assign(kv, **over) == getattr(kv, "KVTC_" + code)
