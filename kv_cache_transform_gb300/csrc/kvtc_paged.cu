@@ -26,7 +26,6 @@ namespace {
 constexpr int kBlock = 16;           // tokens per pool block
 constexpr int kMaxReq = 4096;        // requests per call
 constexpr int kScanThreads = 1024;
-constexpr int kScanPer = kMaxReq / kScanThreads;
 
 __host__ __device__ __forceinline__ int64_t blocks_of(int64_t tokens) {
   return (tokens + kBlock - 1) / kBlock;
@@ -190,9 +189,9 @@ __global__ void __launch_bounds__(kSmallReq)
   if (r == 0) *p.head_out = head + (int64_t)given;
 }
 
-// One block, kScanPer consecutive requests per thread.
+// One block, `per` consecutive requests per thread.
 __global__ void __launch_bounds__(kScanThreads)
-    assign_scan_kernel(const __grid_constant__ AssignParams p) {
+    assign_scan_kernel(const __grid_constant__ AssignParams p, int per) {
   __shared__ int64_t sums[64];
   __shared__ unsigned long long given;   // blocks given out
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -203,9 +202,8 @@ __global__ void __launch_bounds__(kScanThreads)
   bool head_ok;
   const int64_t left = free_left(p, head, &head_ok);
   int64_t fresh = 0, need = 0, total;
-#pragma unroll
-  for (int i = 0; i < kScanPer; ++i) {
-    const Demand d(p, tid * kScanPer + i);
+  for (int i = 0; i < per; ++i) {
+    const Demand d(p, tid * per + i);
     fresh += d.fresh;
     need += d.need;
   }
@@ -214,9 +212,8 @@ __global__ void __launch_bounds__(kScanThreads)
   upto -= fresh;
   used -= need;
   bool short_of = tid == 0 && (!head_ok || total > p.slot_capacity);
-#pragma unroll
-  for (int i = 0; i < kScanPer; ++i) {
-    const int r = tid * kScanPer + i;
+  for (int i = 0; i < per; ++i) {
+    const int r = tid * per + i;
     if (r >= p.R) break;
     const Demand d(p, r);
     p.cu[r] = upto;
@@ -258,9 +255,11 @@ __device__ __forceinline__ int request_at(const int64_t* cu, int lo, int hi,
   return lo;
 }
 
-// Slots and new table entries.  A warp takes runs of 256 tokens, finds their
-// first and last request once, and each lane walks from there: tokens mostly
-// lie many to a request.
+// Slots and new table entries.  A warp takes runs of 256 tokens and finds
+// their first request once; each lane goes on from there (tokens mostly lie
+// many to a request).  The lane that has a new block's first token writes its
+// table entry; blocks whose first token lies behind the slot map come after.
+// 2.1 million slots, 17 MB: bound by what a token takes in instructions.
 constexpr int kFillRun = 256;
 __global__ void __launch_bounds__(256)
     assign_fill_kernel(const __grid_constant__ AssignParams p) {
@@ -269,24 +268,22 @@ __global__ void __launch_bounds__(256)
   const int lane = threadIdx.x & 31;
   const int64_t warp = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
   const int64_t warps = ((int64_t)gridDim.x * blockDim.x) >> 5;
-  for (int64_t r = warp; r < p.R; r += warps) {
-    const AssignRow row = p.rows[r];
-    int32_t* to = p.table + r * p.max_blocks + blocks_of(row.held);
-    for (int i = lane; i < row.blocks; i += 32)
-      to[i] = p.free_blocks[row.first + i];
-  }
   const int64_t total = p.cu[p.R];
   for (int64_t j0 = warp * kFillRun; j0 < p.slot_capacity;
        j0 += warps * kFillRun) {
-    int r = 0;
-    if (j0 < total) r = request_at(p.cu, 0, p.R - 1, j0);
-    AssignRow row = {0, 0, -1};
-    int64_t from = 0, to = 0;      // tokens of request r; none looked up yet
+    int r = j0 < total ? request_at(p.cu, 0, p.R - 1, j0) : 0;
+    const int64_t end = min(total, p.slot_capacity);
+    // of request r: tokens from, ..., to - 1 of the map (none looked up yet)
+    int64_t from = 0, to = 0;
+    const int32_t* fresh = nullptr;  // ids of its blocks, by block index
+    int32_t* table = nullptr;
+    int32_t held = 0, had = 0;
+    bool served = false;
 #pragma unroll
     for (int k = 0; k < kFillRun / 32; ++k) {
       const int64_t j = j0 + k * 32 + lane;
       int64_t slot = -1;
-      if (j < total && j < p.slot_capacity) {
+      if (j < end) {
         if (j >= to) {
           if (p.cu[r + 1] <= j && p.cu[++r + 1] <= j) {
             int hi = p.R - 1;
@@ -295,22 +292,35 @@ __global__ void __launch_bounds__(256)
               if (p.cu[mid] <= j) r = mid; else hi = mid - 1;
             }
           }
-          row = p.rows[r];
+          const AssignRow row = p.rows[r];
           from = p.cu[r];
           to = p.cu[r + 1];
+          held = row.held;
+          had = (int32_t)blocks_of(held);
+          served = row.blocks >= 0;
+          fresh = p.free_blocks + row.first - had;
+          table = p.table + (int64_t)r * p.max_blocks;
         }
-        if (row.blocks >= 0) {
-          // (a new block's id from the list: its table entry may not be
-          // written yet)
-          const int64_t t = row.held + (j - from), b = t / kBlock;
-          const int64_t had = blocks_of(row.held);
-          slot = slot_of(b < had ? p.table[(int64_t)r * p.max_blocks + b]
-                                 : p.free_blocks[row.first + (b - had)],
-                         t);
+        if (served) {
+          const int32_t t = held + (int32_t)(j - from), b = t / kBlock;
+          const int32_t id = b < had ? table[b] : fresh[b];
+          slot = slot_of(id, t);
+          if (b >= had && t % kBlock == 0) table[b] = id;
         }
       }
       if (j < p.slot_capacity) p.slots[j] = slot;
     }
+  }
+  if (total <= p.slot_capacity) return;
+  for (int64_t r = warp; r < p.R; r += warps) {
+    const AssignRow row = p.rows[r];
+    // the first block whose first token has no place in the map
+    const int64_t mapped = max(p.slot_capacity - p.cu[r], (int64_t)0);
+    const int64_t had = blocks_of(row.held);
+    const int64_t i0 = max(blocks_of(row.held + mapped) - had, (int64_t)0);
+    int32_t* to = p.table + r * p.max_blocks + had;
+    for (int64_t i = i0 + lane; i < row.blocks; i += 32)
+      to[i] = p.free_blocks[row.first + i];
   }
 }
 
@@ -424,8 +434,10 @@ int kvtc_paged_assign(int cuda_device, int R, const int32_t* held,
     count_launch();
     return KVTC_OK;
   }
-  if (launch_kernel(assign_scan_kernel, 1, kScanThreads, 0, st, true, 0, p) !=
-      cudaSuccess)
+  const int per = std::max(1, (R + kScanThreads - 1) / kScanThreads);
+  const int threads = std::max(1, (R + per - 1) / per);
+  if (launch_kernel(assign_scan_kernel, 1, (threads + 31) / 32 * 32, 0, st,
+                    true, 0, p, per) != cudaSuccess)
     return KVTC_ECUDA;
   count_launch();
   // (capacity is what the host knows of the tokens)
