@@ -274,7 +274,7 @@ __device__ __forceinline__ Span span_of(const AttendParams& p, int r) {
   s.gap = 0;
   s.hole = p.window && (int64_t)p.sink + p.window < s.len;
   if (s.hole) {
-    s.front = (p.sink + kBlock - 1) / kBlock;     // sink < len: no overflow
+    s.front = (int32_t)(((int64_t)p.sink + kBlock - 1) / kBlock);
     s.gap = max((s.len - p.window) / kBlock - s.front, 0);
   }
   s.units = max(all - s.gap, 1);

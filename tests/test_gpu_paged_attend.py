@@ -278,6 +278,80 @@ def test_requests_that_share_blocks(kv):
     a.check()
 
 
+@pytest.mark.parametrize("R,heads,kv_heads,hd,longest", [
+    (1, 8, 1, 64, 10), (1, 8, 1, 64, 500), (1, 8, 1, 64, 1500),
+    (1, 8, 1, 64, 9000), (1, 32, 1, 128, 3000), (1, 16, 1, 256, 700),
+    (1, 4, 1, 256, 2500), (5, 7, 1, 128, 3000), (1, 28, 7, 128, 4000),
+    (2, 8, 4, 64, 4000), (3, 12, 4, 128, 2000), (1, 15, 15, 64, 2000),
+    (9, 16, 4, 128, 900), (12, 6, 6, 64, 600), (38, 40, 1, 128, 300),
+    (19, 8, 8, 128, 200), (152, 2, 1, 64, 150), (1, 100, 1, 64, 3000)])
+def test_few_items(kv, R, heads, kv_heads, hd, longest):
+    """Few requests and KV heads, one of them long and the others short or
+    empty: clusters of 1 to 16 blocks to an item."""
+    rng = np.random.default_rng(R + longest)
+    lens = rng.integers(0, 40, R)
+    lens[R // 2] = longest
+    if R > 2:
+        lens[0] = 0
+    run(kv, longest, lens, heads, kv_heads, hd)
+    lens[:] = longest - rng.integers(0, min(9, longest), R)
+    run(kv, longest + 1, lens[:20], heads, kv_heads, hd, "fp16", sink=3,
+        window=longest // 2)
+
+
+def test_captured_behind_copies_and_other_streams(kv):
+    """In a captured graph: behind a memory copy, behind a fill, and behind
+    two streams that join."""
+    import torch
+    q, k, v, table, lens = paged_case(37, [300, 20, 90, 1], 8, 2, 128)
+    a = Attend(kv, q, k, v, table, lens)
+    # K pool larger than it needs to be, so that the copies take a while
+    q_in, k_in = a.q.clone(), a.k.clone()
+    lens_in = a.lens.clone()
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+    main.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=main):
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            a.k.copy_(k_in)
+        a.out.fill_(77.0)
+        a.q.copy_(q_in)
+        main.wait_stream(side)
+        a.lens.copy_(lens_in)
+        a.call()
+        a.lens.zero_()
+        a.q.zero_()
+    for _ in range(3):
+        a.k.fill_(float("nan"))
+        g.replay()
+        torch.cuda.synchronize()
+        a.check()
+        assert (a.lens == 0).all()
+
+
+def test_launches_are_counted(kv):
+    q, k, v, table, lens = paged_case(38, [40], 4, 2, 64)
+    a = Attend(kv, q, k, v, table, lens)
+    n = kv.kvtc_launch_count()
+    a.call()
+    assert kv.kvtc_launch_count() - n in (1, 2)
+
+
+def test_a_missing_device_is_an_error(kv):
+    q, k, v, table, lens = paged_case(39, [40], 4, 2, 64)
+    a = Attend(kv, q, k, v, table, lens)
+    with pytest.raises(kv.KvtcError) as e:
+        kv.kvtc_paged_attend(
+            1, 4, 2, 64, kv.KVTC_DTYPE_BF16, a.q, a.q.stride(0), a.k, a.v,
+            a.num_blocks, BLOCK, a.table, a.table.shape[1], a.lens, 0, 0, 1.0,
+            a.out, a.out.stride(0), None, a.ws, a.ws.numel(), device=63,
+            stream=0)
+    assert e.value.code == kv.KVTC_ECUDA
+    a.call()
+    a.check()
+
+
 def test_without_lse(kv):
     run(kv, 27, [33, 0, 900], 8, 2, 64, lse=False)
 
