@@ -3,7 +3,8 @@
 // For a query head, s_t = scale q.k_t over the attended tokens.  With a
 // running reference m near the maximum, l = sum 2^(s_t - m) and o = sum
 // 2^(s_t - m) v_t (s in units of log2) are multiplied by 2^(m_old - m_new)
-// when m grows, so K and V are read once; partial results of disjoint tokens join the same way:
+// when m grows, so K and V are read once; partial results of disjoint tokens
+// join the same way:
 //     m = max m_i,  l = sum l_i 2^(m_i - m),  o = sum o_i 2^(m_i - m),
 // and out = o / l, lse = (m + log2 l) ln 2.
 //
@@ -33,6 +34,14 @@
 // that rescale by them.  P enters the second product as two 16-bit terms
 // (p = hi + lo to 2^-15), so that only the output's own rounding is of 16
 // bits.
+//
+// What bounds it.  HBM: each attended row of K and V is read once, 4 heads
+// flops a row element, 44 TFLOP/s at eight query heads a KV head, a small
+// part of what mma.sync gives.  Between the first page and the last one SM
+// after the other reads at 7.8 TB/s in all (570 MB: 16 requests up to 16K,
+// 93 us in all, 6.1 TB/s); the rest is latency: 3.5 us until the first page
+// (lengths, block table, page, one after the other), and 6 us of joining
+// after the last.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -90,8 +99,9 @@ struct __align__(16) JoinDesc {
 };
 
 struct AttendParams {
-  CUtensorMap tm_k, tm_v;   // a pool as {64, 16, D / 64, num_blocks},
-                            // box {64, 16, head_dim / 64, 1}
+  // a pool as {64, 16, D / 64, num_blocks}: a page of a head, box {64, 16,
+  // head_dim / 64, 1}, and 64 channels of half a page, box {64, 8, 1, 1}
+  CUtensorMap tm_k, tm_v, tm_k8, tm_v8;
   const void* q;
   const int32_t* table;
   const int32_t* lens;
@@ -113,13 +123,14 @@ __device__ __forceinline__ uint32_t cluster_size() {
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(n));
   return n;
 }
-__device__ __forceinline__ void tma_load_page(uint32_t smem_dst,
-                                              const void* tmap, int32_t slab,
-                                              int32_t block, uint64_t* bar) {
+__device__ __forceinline__ void tma_load_box(uint32_t smem_dst,
+                                             const void* tmap, int32_t row,
+                                             int32_t slab, int32_t block,
+                                             uint64_t* bar) {
   asm volatile(
       "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_"
-      "tx::bytes [%0], [%1, {%2, %2, %3, %4}], [%5];" ::"r"(smem_dst),
-      "l"(tmap), "r"(0), "r"(slab), "r"(block), "r"(smem_u32(bar))
+      "tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_dst),
+      "l"(tmap), "r"(0), "r"(row), "r"(slab), "r"(block), "r"(smem_u32(bar))
       : "memory");
 }
 // Bulk copy global -> shared (both 16-byte aligned, bytes % 16 == 0).
@@ -342,7 +353,9 @@ constexpr uint32_t kFirst = 1u << 31;   // first unit of its item
 constexpr uint32_t kLast = 1u << 30;    // last unit of its item
 constexpr uint32_t kSkip = 1u << 29;    // no page (bad id, empty request)
 constexpr uint32_t kWhole = 1u << 28;   // all 16 tokens are attended
-constexpr uint32_t kSubMask = kWhole - 1;
+constexpr uint32_t kNoLow = 1u << 27;   // none of the first eight is
+constexpr uint32_t kNoHigh = 1u << 26;  // none of the last eight is
+constexpr uint32_t kSubMask = kNoHigh - 1;
 
 // A part of an item left by a warp: entry 0 of a warp is of an item that
 // ended in its run but began before it (in the slot beside the ring), entry
@@ -681,15 +694,37 @@ __global__ void __launch_bounds__(warps_of(HD, NT, kCluster) * 32, 1)
         }
       }
       if (b_id < 0) b_sub |= kSkip;
-      const int t0 = b_page * kBlock;
+      const int t0 = b_page * kBlock, recent = sp.hole ? sp.len - p.window : 0;
       if (sp.len - t0 >= kBlock &&
-          (!sp.hole || (int64_t)t0 + kBlock <= p.sink ||
-           t0 >= sp.len - p.window))
+          (t0 >= recent || (int64_t)t0 + kBlock <= p.sink))
         b_sub |= kWhole;
+      // (a cluster's items are few: it is not worth their code there)
+      if (!kCluster && t0 + 8 <= recent && t0 >= p.sink) b_sub |= kNoLow;
+      if (!kCluster &&
+          (t0 + 8 >= sp.len || (t0 + 16 <= recent && t0 + 8 >= p.sink)))
+        b_sub |= kNoHigh;
     }
     const int last = min(31, n - 1 - i);
     cur_r = __shfl_sync(0xFFFFFFFFu, r, last);
     cur_s = __shfl_sync(0xFFFFFFFFu, s, last);
+  };
+  // What is attended of a page: it whole, or half of it.
+  auto page_loads = [&]() {
+    return b_sub & kSkip ? 0
+           : !kCluster && (b_sub & (kNoLow | kNoHigh)) ? kPage / 2
+                                                       : kPage;
+  };
+  auto load_page = [&](uint32_t dst, const CUtensorMap& whole,
+                       const CUtensorMap& half, uint64_t* bar) {
+    if (kCluster || !(b_sub & (kNoLow | kNoHigh))) {
+      tma_load_box(dst, &whole, 0, b_slab, b_id, bar);
+    } else {
+      const int row = b_sub & kNoLow ? 8 : 0;
+#pragma unroll
+      for (int i = 0; i < HD / 64; ++i)
+        tma_load_box(dst + i * 2048 + row * 128, &half, row, b_slab + i, b_id,
+                     bar);
+    }
   };
   auto issue_k = [&](int i, int st) {
     if ((i & 31) == 0) fill(i);
@@ -701,7 +736,7 @@ __global__ void __launch_bounds__(warps_of(HD, NT, kCluster) * 32, 1)
       m.len = b_len;
       metas[st] = m;
       const uint32_t sub = b_sub & kSubMask;
-      const bool page = !(b_sub & kSkip);
+      const uint32_t page = page_loads();
       const uint32_t dst = ring + st * L::kStage;
       const int j = p.tiles == 1 ? (int)sub : (int)sub / p.tiles;
       b_slab = j * (HD / 64);
@@ -709,28 +744,29 @@ __global__ void __launch_bounds__(warps_of(HD, NT, kCluster) * 32, 1)
         // the rows of an item's query heads are consecutive
         const Heads h(p, sub);
         const uint32_t bytes = (uint32_t)h.rows * HD * 2;
-        mbar_arrive_expect_tx(k_bars + st, bytes + (page ? kPage : 0));
+        mbar_arrive_expect_tx(k_bars + st, bytes + page);
         bulk_load(queries + st * query_bytes(HD, NT),
                   static_cast<const T*>(p.q) + (int64_t)b_r * p.q_ld +
                       (int64_t)h.first * HD,
                   bytes, k_bars + st);
       } else if (page) {
-        mbar_arrive_expect_tx(k_bars + st, kPage);
+        mbar_arrive_expect_tx(k_bars + st, page);
       } else {
         mbar_arrive(k_bars + st);
       }
-      if (page) tma_load_page(dst, &p.tm_k, b_slab, b_id, k_bars + st);
+      if (page) load_page(dst, p.tm_k, p.tm_k8, k_bars + st);
     }
     __syncwarp();
   };
   auto issue_v = [&](int i, int st) {
     if (lane == (i & 31)) {
-      if (b_sub & kSkip) {
+      const uint32_t page = page_loads();
+      if (!page) {
         mbar_arrive(v_bars + st);
       } else {
-        mbar_arrive_expect_tx(v_bars + st, kPage);
-        tma_load_page(ring + st * L::kStage + kPage, &p.tm_v, b_slab, b_id,
-                      v_bars + st);
+        mbar_arrive_expect_tx(v_bars + st, page);
+        load_page(ring + st * L::kStage + kPage, p.tm_v, p.tm_v8,
+                  v_bars + st);
       }
     }
   };
@@ -956,8 +992,11 @@ __global__ void __launch_bounds__(warps_of(HD, NT, kCluster) * 32, 1)
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1)
           l_run[nt][i] += __shfl_xor_sync(0xFFFFFFFFu, l_run[nt][i], d);
-    bool done = begun && ended;
-    if (begun && !ended && warp + 1 < W &&
+    // (In a cluster, whose blocks run this once, every part is left to the
+    // block's join: less code to fetch took 8K tokens of one request from
+    // 12.2 to 11.9 us.)
+    bool done = !kCluster && begun && ended;
+    if (!kCluster && begun && !ended && warp + 1 < W &&
         __all_sync(0xFFFFFFFFu, heads_ready[warp + 1])) {
       // The item ends in the next warp's run, which has left that part (it
       // came first there): join it here, where the accumulators are.
@@ -1301,14 +1340,15 @@ cudaError_t launch(const AttendParams& p, int head_dim, int nt, int cluster,
 }
 
 // A pool [num_blocks][16][D] as {64 channels, 16 tokens, D / 64, num_blocks}:
-// a box is one block's rows of one head, as head_dim / 64 tiles [16][64].
+// a box is `rows` rows of one block, `slabs` times 64 channels of each, as
+// tiles [rows][64].
 bool encode_pages(CUtensorMap* m, const void* base, uint64_t D,
-                  uint64_t num_blocks, uint32_t head_dim) {
+                  uint64_t num_blocks, uint32_t rows, uint32_t slabs) {
   auto enc = tensor_map_encoder();
   if (!enc) return false;
   cuuint64_t dims[4] = {64, kBlock, D / 64, num_blocks};
   cuuint64_t strides[3] = {D * 2, 128, D * 2 * kBlock};
-  cuuint32_t box[4] = {64u, (cuuint32_t)kBlock, head_dim / 64, 1u};
+  cuuint32_t box[4] = {64u, rows, slabs, 1u};
   cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base),
              dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -1384,8 +1424,11 @@ int kvtc_paged_attend(int cuda_device, int R, int heads, int kv_heads,
   if (!guard.ok) return KVTC_ECUDA;
   AttendParams p;
   const uint64_t D = (uint64_t)kv_heads * head_dim;
-  if (!encode_pages(&p.tm_k, k_cache, D, num_blocks, head_dim) ||
-      !encode_pages(&p.tm_v, v_cache, D, num_blocks, head_dim))
+  const uint32_t slabs = (uint32_t)head_dim / 64;
+  if (!encode_pages(&p.tm_k, k_cache, D, num_blocks, kBlock, slabs) ||
+      !encode_pages(&p.tm_v, v_cache, D, num_blocks, kBlock, slabs) ||
+      !encode_pages(&p.tm_k8, k_cache, D, num_blocks, 8, 1) ||
+      !encode_pages(&p.tm_v8, v_cache, D, num_blocks, 8, 1))
     return KVTC_ECUDA;
   const int group = heads / kv_heads, nt = head_tiles(head_dim, group);
   p.q = q;
