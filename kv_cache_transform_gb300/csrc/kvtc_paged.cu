@@ -4,10 +4,10 @@
 // new blocks per request, cu is the exclusive sum of n, C the inclusive sum
 // of b, and request r takes free[head + C_r - b_r ...] if it fits.  Both are
 // integer sums, so the result is exact and does not depend on the launch.
-//   few new tokens (decode steps): assign_small_kernel, one block, a thread
-//     per request: one launch, a chain of three loads.
-//   many: assign_scan_kernel, one block, forms the sums, and
-//     assign_fill_kernel, launched behind on the whole GPU, writes the table
+//   few slots (decode steps): assign_small_kernel, one block, a thread per
+//     request: one launch and a chain of three loads, 1.8 us;
+//   more: assign_scan_kernel, one block, forms the sums, and
+//     assign_fill_kernel, behind it on the whole GPU, writes the table
 //     entries and the slots.
 // kvtc_paged_append: append_kernel, a warp per row.
 #include <cuda_runtime.h>
@@ -120,7 +120,7 @@ __device__ __forceinline__ int64_t slot_of(int64_t id, int64_t t) {
 // One block, a thread per request (R <= 1024).  Where a request has few new
 // tokens its thread writes their slots, else the warps share them.
 constexpr int kSmallReq = 1024;
-constexpr int64_t kSmallSlots = 8192;
+constexpr int64_t kSmallSlots = 2048;  // beyond, two launches are faster
 constexpr int kSmallOwn = 4;         // tokens that a thread writes itself
 __global__ void __launch_bounds__(kSmallReq)
     assign_small_kernel(const __grid_constant__ AssignParams p) {
@@ -259,7 +259,9 @@ __device__ __forceinline__ int request_at(const int64_t* cu, int lo, int hi,
 // their first request once; each lane goes on from there (tokens mostly lie
 // many to a request).  The lane that has a new block's first token writes its
 // table entry; blocks whose first token lies behind the slot map come after.
-// 2.1 million slots, 17 MB: bound by what a token takes in instructions.
+// 131 thousand slots (1 MB) take 7.4 us with the scan, 2.1 million (17 MB)
+// 10.4: two launches, and chains of loads in each.  (One cluster of 16 blocks
+// that each form the sums: 7.6 and 35 us.)
 constexpr int kFillRun = 256;
 __global__ void __launch_bounds__(256)
     assign_fill_kernel(const __grid_constant__ AssignParams p) {
@@ -271,8 +273,38 @@ __global__ void __launch_bounds__(256)
   const int64_t total = p.cu[p.R];
   for (int64_t j0 = warp * kFillRun; j0 < p.slot_capacity;
        j0 += warps * kFillRun) {
-    int r = j0 < total ? request_at(p.cu, 0, p.R - 1, j0) : 0;
+    // (looked up before `total` is here to say whether it is of use)
+    int r = p.R ? request_at(p.cu, 0, p.R - 1, j0) : 0;
+    const AssignRow row0 = p.R ? p.rows[r] : AssignRow{0, 0, -1};
+    const int64_t from0 = p.cu[r], to0 = p.R ? p.cu[r + 1] : 0;
     const int64_t end = min(total, p.slot_capacity);
+    if (j0 + kFillRun <= min(end, to0)) {
+      // the whole run is one request's (in a third of the instructions)
+      const AssignRow row = row0;
+      int64_t* to = p.slots + j0 + lane;
+      if (row.blocks < 0) {
+#pragma unroll
+        for (int k = 0; k < kFillRun / 32; ++k) to[k * 32] = -1;
+        continue;
+      }
+      const int32_t had = (int32_t)blocks_of(row.held);
+      const int32_t* fresh = p.free_blocks + row.first - had;
+      int32_t* table = p.table + (int64_t)r * p.max_blocks;
+      const int32_t t0 = row.held + (int32_t)(j0 - from0) + lane;
+      int32_t id[kFillRun / 32];
+#pragma unroll
+      for (int k = 0; k < kFillRun / 32; ++k) {
+        const int32_t b = (t0 + k * 32) / kBlock;
+        id[k] = b < had ? table[b] : fresh[b];
+      }
+#pragma unroll
+      for (int k = 0; k < kFillRun / 32; ++k) {
+        const int32_t t = t0 + k * 32, b = t / kBlock;
+        if (t % kBlock == 0 && b >= had) table[b] = id[k];
+        to[k * 32] = slot_of(id[k], t);
+      }
+      continue;
+    }
     // of request r: tokens from, ..., to - 1 of the map (none looked up yet)
     int64_t from = 0, to = 0;
     const int32_t* fresh = nullptr;  // ids of its blocks, by block index
@@ -338,8 +370,9 @@ struct AppendParams {
 };
 
 // A warp per (stream, row): the row's slot once, its pieces 32 at a time with
-// four loads in flight a lane.  Bound by HBM: 8192 rows of K and V of 2 KB,
-// 67 MB moved.
+// four loads in flight a lane.  Bound by HBM and, for decode steps, by two
+// loads one after the other: 8192 rows of K and V of 2 KB (67 MB moved)
+// 11.5 us, 5.8 TB/s; with two rows in flight a warp 12.2.
 __global__ void __launch_bounds__(256)
     append_kernel(const __grid_constant__ AppendParams p) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

@@ -175,9 +175,9 @@ def test_assign_lengths_far_beyond_the_map(kv, R, cap):
 
 
 @pytest.mark.parametrize("R,hi", [(1024, 3), (1025, 3), (4096, 60), (600, 1),
-                                  (64, 128), (64, 129)])
+                                  (64, 32), (64, 33), (64, 128), (64, 129)])
 def test_assign_with_many_empty_requests(kv, R, hi):
-    """On both sides of the single launch's limits (1024 requests, 8192
+    """On both sides of the single launch's limits (1024 requests, 2048
     slots), with long runs of requests that want nothing."""
     rng = np.random.default_rng(R + hi)
     lens = rng.integers(1, hi + 1, R)
