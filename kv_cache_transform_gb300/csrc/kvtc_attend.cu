@@ -77,16 +77,18 @@ __host__ __device__ constexpr int slot_floats(int hd, int nt) {
 }
 // Warps per block, for nt tiles of eight query heads per warp: as many as
 // registers and shared memory hold (a cluster's blocks need less of it), with
-// one page each in flight (two of head_dim 64, whose pages are small).  More
-// warps with one page beat fewer with two: 12 x 1 against 10 x 2 at head_dim
-// 128, 64 requests up to 4K: 50.5 and 53.1 us.
+// one page each in flight (two where 12 or fewer warps read the small pages
+// of head_dim 64).  More warps with one page beat fewer with two: 64 requests
+// up to 4K at head_dim 128, 12 x 1 against 10 x 2: 50.5 and 53.1 us; up to 8K
+// at head_dim 64, 16 x 1 against 12 x 2: 102 and 105 us.
 __host__ __device__ constexpr int warps_of(int hd, int nt, bool cluster) {
-  return hd == 64    ? (nt <= 2 ? 12 : 8)
-         : hd == 128 ? (nt == 1 ? (cluster ? 14 : 12)
-                                : cluster || nt == 2 ? 8 : 5)
+  return hd == 64    ? (nt == 1 ? 16 : nt == 2 ? 12 : 8)
+         : hd == 128 ? (nt == 1 ? (cluster ? 14 : 12) : 8)
                      : (cluster ? 8 : nt == 1 ? 7 : 5);
 }
-__host__ __device__ constexpr int stages_of(int hd) { return hd == 64 ? 2 : 1; }
+__host__ __device__ constexpr int stages_of(int hd, int nt) {
+  return hd == 64 && nt > 1 ? 2 : 1;
+}
 __host__ __device__ constexpr int page_bytes(int hd) { return hd * 2 * kBlock; }
 __host__ __device__ constexpr int query_bytes(int hd, int nt) {
   return nt * 16 * hd;
@@ -369,7 +371,7 @@ struct __align__(16) PartRec {
 template <int HD, int NT, bool kCluster>
 struct Smem {
   static constexpr int W = warps_of(HD, NT, kCluster);
-  static constexpr int S = stages_of(HD);
+  static constexpr int S = stages_of(HD, NT);
   static constexpr int kSlot = 4 * slot_floats(HD, NT);
   static constexpr int kStage = 2 * page_bytes(HD);   // a page of K, one of V
   // A warp's ring of pages; when the last has been read, a part lies there.
@@ -1317,12 +1319,14 @@ int cluster_of(int R, int64_t items, int64_t max_blocks, int head_dim,
              : 0;
 }
 
-// Tiles of eight query heads per warp: as many as the group needs, up to 32
-// heads (16 at head_dim 256, where the accumulators of 32 heads would not
-// fit the registers); larger groups are cut into equal tiles of heads, each
-// of which reads the pages again (from L2, mostly).
+// Tiles of eight query heads per warp: one or two, by the group, and four for
+// large groups of head_dim 64.  Larger groups are cut into equal tiles of
+// heads, each of which reads the pages again (from L2, mostly).  At 32 heads
+// a KV head (32 requests up to 8K), one pass with four tiles takes 154 us at
+// head_dim 64, two passes with two 183; at 128 it is 217 and 175: the
+// accumulators of 32 heads leave too few warps.
 int head_tiles(int head_dim, int group) {
-  return group <= 8 ? 1 : group <= 16 || head_dim == 256 ? 2 : 4;
+  return group <= 8 ? 1 : group <= 16 || head_dim > 64 ? 2 : 4;
 }
 
 template <class T>
@@ -1333,9 +1337,8 @@ cudaError_t launch(const AttendParams& p, int head_dim, int nt, int cluster,
            : nt == 2 ? launch_as<T, 64, 2>(p, cluster, device, st)
                      : launch_as<T, 64, 4>(p, cluster, device, st);
   if (head_dim == 128)
-    return nt == 1   ? launch_as<T, 128, 1>(p, cluster, device, st)
-           : nt == 2 ? launch_as<T, 128, 2>(p, cluster, device, st)
-                     : launch_as<T, 128, 4>(p, cluster, device, st);
+    return nt == 1 ? launch_as<T, 128, 1>(p, cluster, device, st)
+                   : launch_as<T, 128, 2>(p, cluster, device, st);
   return nt == 1 ? launch_as<T, 256, 1>(p, cluster, device, st) : launch_as<T, 256, 2>(p, cluster, device, st);
 }
 
