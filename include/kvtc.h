@@ -432,7 +432,7 @@ int64_t kvtc_paged_attend_workspace_bytes(int cuda_device, int R, int heads,
  * and the softmax statistics held, in fp32; out is rounded once.  The result
  * does not depend on timing, so equal calls on one device give equal bits.
  *   head_dim 64, 128 or 256; kv_heads * head_dim <= 8192; at most 128 query
- * heads a KV head; num_blocks < 2^31.  out must not overlap an input.
+ * heads a KV head; num_blocks < 2^31, max_blocks < 2^27 - 1.  out must not overlap an input.
  * workspace: device scratch of kvtc_paged_attend_workspace_bytes bytes, used
  * only while the call's work runs on cuda_stream: calls that may run at the
  * same time need one each.  q, pools, out and workspace 16-byte aligned,

@@ -64,6 +64,8 @@ namespace {
 constexpr int kBlock = 16;           // tokens per pool block (a page)
 constexpr int kMaxReq = 4096;        // requests per call
 constexpr int kMaxGroup = 128;       // query heads per KV head
+constexpr int kMaxTable = INT32_MAX / kBlock - 1;  // table columns: token
+                                     // indices and a page more in 32 bits
 constexpr int kCtas = 152;           // one block per SM
 constexpr int kLeast = 2;            // units per warp
 constexpr float kLog2e = 1.4426950408889634f;
@@ -280,7 +282,7 @@ struct Span {
 __device__ __forceinline__ Span span_of(const AttendParams& p, int r) {
   Span s;
   const int64_t room = (int64_t)p.max_blocks * kBlock;
-  const int32_t len = max(__ldg(p.lens + r), 0);
+  const int32_t len = max(p.lens[r], 0);
   s.len = (int32_t)min((int64_t)len, room);
   const int32_t all = (int32_t)(((int64_t)s.len + kBlock - 1) / kBlock);
   s.front = all;
@@ -593,7 +595,9 @@ __global__ void __launch_bounds__(warps_of(HD, NT, kCluster) * 32, 1)
   }
   if (tid == 0) *abort_flag = 0;
   fence_mbar_init();
-  // everything this call reads may come from the launch before it
+  // Everything this call reads may come from the launch before it, and is
+  // read by plain loads: this grid may have started under that one, so the
+  // read-only path could hold what it held before.
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
   // This warp's run of units, and the request that holds its first one.
@@ -608,7 +612,7 @@ __global__ void __launch_bounds__(warps_of(HD, NT, kCluster) * 32, 1)
     fixed_sub = (uint32_t)(id - cur_r * items);
     total = span_of(p, cur_r).units;
     if (tid == 0 && p.flags &&
-        __ldg(p.lens + cur_r) > (int64_t)p.max_blocks * kBlock)
+        p.lens[cur_r] > (int64_t)p.max_blocks * kBlock)
       atomicOr(p.flags, KVTC_FLAG_SPACE);
     __syncthreads();
   } else {
@@ -621,7 +625,7 @@ __global__ void __launch_bounds__(warps_of(HD, NT, kCluster) * 32, 1)
       if (r >= p.R) break;
       sum += span_of(p, r).units;
       if (p.flags && blockIdx.x == 0 &&
-          __ldg(p.lens + r) > (int64_t)p.max_blocks * kBlock)
+          p.lens[r] > (int64_t)p.max_blocks * kBlock)
         atomicOr(p.flags, KVTC_FLAG_SPACE);
     }
     int64_t upto = sum;
@@ -689,7 +693,7 @@ __global__ void __launch_bounds__(warps_of(HD, NT, kCluster) * 32, 1)
               (v == sp.units - 1 ? kLast : 0u);
       b_id = -1;
       if (sp.len) {
-        b_id = __ldg(p.table + (int64_t)r * p.max_blocks + b_page);
+        b_id = p.table[(int64_t)r * p.max_blocks + b_page];
         if (b_id < 0 || b_id >= p.num_blocks) {
           b_id = -1;
           if (p.flags) atomicOr(p.flags, KVTC_FLAG_BLOCK);
@@ -821,8 +825,8 @@ __global__ void __launch_bounds__(warps_of(HD, NT, kCluster) * 32, 1)
               q + (int64_t)(nt * 8 + gid) * HD + tig * 2);
 #pragma unroll
           for (int ks = 0; ks < MT; ++ks) {
-            qf[ks][nt][0] = in ? __ldg(row + ks * 8) : 0u;
-            qf[ks][nt][1] = in ? __ldg(row + ks * 8 + 4) : 0u;
+            qf[ks][nt][0] = in ? row[ks * 8] : 0u;
+            qf[ks][nt][1] = in ? row[ks * 8 + 4] : 0u;
           }
         }
       }
@@ -1410,7 +1414,7 @@ int kvtc_paged_attend(int cuda_device, int R, int heads, int kv_heads,
       max_blocks <= 0 || sink < 0 || window < 0 || !std::isfinite(scale) ||
       !workspace || (R && (!q || !block_table || !lens || !out)))
     return KVTC_EINVAL;
-  if (block_size != kBlock) return KVTC_ENOTSUP;
+  if (block_size != kBlock || max_blocks > kMaxTable) return KVTC_ENOTSUP;
   const int64_t width = (int64_t)heads * head_dim;
   const int64_t need = kvtc_paged_attend_workspace_bytes(
       cuda_device, R, heads, kv_heads, head_dim);

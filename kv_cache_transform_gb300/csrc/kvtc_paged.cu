@@ -383,7 +383,7 @@ __global__ void __launch_bounds__(256)
   const uint4* src = p.src[blockIdx.y];
   uint4* cache = p.cache[blockIdx.y];
   for (int64_t n = warp; n < p.N; n += warps) {
-    const int64_t slot = __ldg(p.slots + n);
+    const int64_t slot = p.slots[n];
     const uint4* from = src + n * p.ld;
     if (slot < 0) continue;
     if (slot >= p.pool_rows) {
@@ -395,7 +395,7 @@ __global__ void __launch_bounds__(256)
       uint4 v[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        if (c0 + i * 32 < p.pieces) v[i] = __ldg(from + c0 + i * 32);
+        if (c0 + i * 32 < p.pieces) v[i] = from[c0 + i * 32];
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         if (c0 + i * 32 < p.pieces) to[c0 + i * 32] = v[i];

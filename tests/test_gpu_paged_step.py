@@ -136,3 +136,68 @@ def test_restore_append_and_attend(graph):
     assert int(flags.cpu()[0]) == 0
     assert int(head.cpu()[0]) == sum(blocks_of(T + steps) for T in prefix)
     calib.free()
+
+
+FIRST_CALLS = """
+import numpy as np, torch
+import kv_cache_transform_gb300 as kv
+R, H, KV, hd, cols, nb = 3, 8, 2, 128, 4, 16
+D = KV * hd
+i32 = dict(dtype=torch.int32, device='cuda')
+i64 = dict(dtype=torch.int64, device='cuda')
+pools = [torch.zeros(nb, 16, D, dtype=torch.bfloat16, device='cuda')
+         for _ in range(2)]
+table, held = torch.full((R, cols), -1, **i32), torch.zeros(R, **i32)
+lens = torch.tensor([20, 1, 33], **i32)
+free, head = torch.arange(nb, **i32), torch.zeros(1, **i64)
+cap = {cap}
+slots, cu = torch.empty(cap, **i64), torch.empty(R + 1, **i64)
+flags = torch.zeros(1, **i32)
+ws = torch.empty(max(kv.kvtc_paged_assign_workspace_bytes(R),
+                     kv.kvtc_paged_attend_workspace_bytes(R, H, KV, hd)),
+                 dtype=torch.uint8, device='cuda')
+rows = torch.randn(cap, 2 * D, device='cuda').bfloat16()
+q = torch.randn(R, H * hd, device='cuda').bfloat16()
+out, lse = torch.empty_like(q), torch.empty(R, H, device='cuda')
+st = torch.cuda.Stream()
+st.wait_stream(torch.cuda.current_stream())
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g, stream=st):
+    kv.kvtc_paged_assign(R, held, lens, free, nb, head, table, cols, 16,
+                         slots, cap, cu, held, head, ws, ws.numel(), flags)
+    kv.kvtc_paged_append([rows[:, :D], rows[:, D:]], 2 * D, cap, slots, D, 16,
+                         pools, nb, flags)
+    kv.kvtc_paged_attend(R, H, KV, hd, kv.KVTC_DTYPE_BF16, q, H * hd,
+                         pools[0], pools[1], nb, 16, table, {cols}, held, 0,
+                         0, hd ** -0.5, out, H * hd, lse, ws, ws.numel(),
+                         flags)
+g.replay()
+torch.cuda.synchronize()
+assert int(flags[0]) == 0 and held.tolist() == [20, 1, 33]
+at = 0
+for r, n in enumerate((20, 1, 33)):
+    k = rows[at:at + n, :D].double().view(n, KV, hd)
+    v = rows[at:at + n, D:].double().view(n, KV, hd)
+    x = q[r].double().view(KV, 4, hd) @ k.permute(1, 2, 0) * hd ** -0.5
+    ref = (torch.softmax(x, -1) @ v.permute(1, 0, 2)).reshape(-1)
+    assert (out[r].double() - ref).abs().max() <= 2 ** -8 * ref.abs().max()
+    at += n
+print('captured first')
+"""
+
+
+@pytest.mark.parametrize("cap", [54, 5000])
+def test_first_calls_of_a_process_are_captured(cap):
+    """Nothing has to run before a capture: a process whose first calls are
+    inside one (both launch forms of assign)."""
+    import os
+    import subprocess
+    import sys
+    from kv_cache_transform_gb300 import _build
+    _build.build()
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run(
+        [sys.executable, "-c", FIRST_CALLS.format(cap=cap, cols="cols")],
+        cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured first" in r.stdout, \
+        r.stdout[-2000:] + r.stderr[-4000:]

@@ -95,6 +95,7 @@ def test_append_refusals(kv, over, code):
     (dict(scale=float("nan")), "EINVAL"),
     (dict(scale=float("inf")), "EINVAL"),
     (dict(block_size=32), "ENOTSUP"), (dict(head_dim=96), "ENOTSUP"),
+    (dict(max_blocks=(1 << 27) - 1), "ENOTSUP"),
     (dict(heads=80, kv_heads=80, q_ld=10240, out_ld=10240), "ENOTSUP"),
     (dict(heads=129, kv_heads=1, q_ld=16512, out_ld=16512), "ENOTSUP")])
 def test_attend_refusals(kv, over, code):
