@@ -483,33 +483,37 @@ __device__ __forceinline__ void store_part(float* slot, int tile,
 }
 
 // Join n parts in shared memory, part i at at(i) (of this block or `across`
-// the cluster's), at fragment tiles tile, tile + step, ...: into the result,
-// or where `to` is given into a slot.  kBatch parts are loaded at once; more
-// would only lengthen code that runs once a call and has to be fetched.  The
-// sums are spelled out so that the same two parts give the same bits here and
-// where a warp joins them in its registers.
-template <class T, int HD, int NT, int kBatch, bool across, class F>
+// the cluster's), kTiles channel tiles at a time (place, place + step, ...):
+// into the result, or where `to` is given into a slot.  kBatch parts are
+// loaded at once; more would only lengthen code that runs once a call and has
+// to be fetched.  The sums are spelled out so that the same two parts give
+// the same bits here and where a warp joins them in its registers.
+template <class T, int HD, int NT, int kTiles, int kBatch, bool across,
+          class F>
 __device__ __forceinline__ void join_parts(int n, F at,
                                            const Target<T>& target, float* to,
-                                           int tile, int step) {
+                                           int place, int step) {
+  constexpr int kPlaces = HD / 16 / kTiles;     // of a head tile
   const int lane = (int)lane_id();
 #pragma unroll 1
-  for (; tile < HD / 16 * NT; tile += step) {
-    const int nt = tile % NT;
+  for (; place < kPlaces * NT; place += step) {
+    const int nt = place / kPlaces, mt = place % kPlaces * kTiles;
     const uint32_t stat = (NT * 8 * HD + nt * 8 + (lane & 3) * 2) * 4;
-    const uint32_t frag = (tile * 32 + lane) * 16;
+    const uint32_t frag = ((mt * NT + nt) * 32 + lane) * 16;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-    float o[4] = {0.f, 0.f, 0.f, 0.f};
+    float o[kTiles][4] = {};
 #pragma unroll 1
     for (int i0 = 0; i0 < n; i0 += kBatch) {
       float2 mi[kBatch], li[kBatch];
-      float4 oi[kBatch];
+      float4 oi[kBatch][kTiles];
 #pragma unroll
       for (int b = 0; b < kBatch; ++b) {
         const uint32_t slot = at(min(i0 + b, n - 1));
         mi[b] = lds2<across>(slot + stat);
         li[b] = lds2<across>(slot + stat + NT * 32);
-        oi[b] = lds4<across>(slot + frag);
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t)
+          oi[b][t] = lds4<across>(slot + frag + t * NT * 512);
       }
       float mn[2] = {m[0], m[1]};
 #pragma unroll
@@ -523,30 +527,39 @@ __device__ __forceinline__ void join_parts(int n, F at,
         const float f = exp2_fast(m[c] - base[c]);
         m[c] = mn[c];
         l[c] = __fmul_rn(l[c], f);
-        o[c] = __fmul_rn(o[c], f);
-        o[c + 2] = __fmul_rn(o[c + 2], f);
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) {
+          o[t][c] = __fmul_rn(o[t][c], f);
+          o[t][c + 2] = __fmul_rn(o[t][c + 2], f);
+        }
       }
 #pragma unroll
       for (int b = 0; b < kBatch; ++b) {
-        const bool in = i0 + b < n;
-        const float f0 = in ? exp2_fast(mi[b].x - base[0]) : 0.f;
-        const float f1 = in ? exp2_fast(mi[b].y - base[1]) : 0.f;
-        if (in) {
+        if (i0 + b < n) {
+          const float f0 = exp2_fast(mi[b].x - base[0]);
+          const float f1 = exp2_fast(mi[b].y - base[1]);
           l[0] = __fmaf_rn(li[b].x, f0, l[0]);
           l[1] = __fmaf_rn(li[b].y, f1, l[1]);
-          o[0] = __fmaf_rn(oi[b].x, f0, o[0]);
-          o[1] = __fmaf_rn(oi[b].y, f1, o[1]);
-          o[2] = __fmaf_rn(oi[b].z, f0, o[2]);
-          o[3] = __fmaf_rn(oi[b].w, f1, o[3]);
+#pragma unroll
+          for (int t = 0; t < kTiles; ++t) {
+            o[t][0] = __fmaf_rn(oi[b][t].x, f0, o[t][0]);
+            o[t][1] = __fmaf_rn(oi[b][t].y, f1, o[t][1]);
+            o[t][2] = __fmaf_rn(oi[b][t].z, f0, o[t][2]);
+            o[t][3] = __fmaf_rn(oi[b][t].w, f1, o[t][3]);
+          }
         }
       }
     }
     if (to) {
-      store_part<HD, NT>(to, tile, o, m, l);
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t)
+        store_part<HD, NT>(to, (mt + t) * NT + nt, o[t], m, l);
     } else {
       const float inv[2] = {inverse(l[0]), inverse(l[1])};
-      target.template store<HD>(nt, tile / NT, o, inv);
-      if (tile < NT) target.store_lse(nt, m, l);
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t)
+        target.template store<HD>(nt, mt + t, o[t], inv);
+      if (mt == 0) target.store_lse(nt, m, l);
     }
   }
 }
@@ -1124,7 +1137,8 @@ __global__ void __launch_bounds__(warps_of(HD, NT, kCluster) * 32, 1)
     const uint32_t first = slot_of(e0), last = slot_of(e1);
     const uint32_t base = slot_of(e0 | 1);
     const int k = __popc(in_run);
-    join_parts<T, HD, NT, 4, false>(
+    // (a cluster's block has one run, and a warp for each of its tiles)
+    join_parts<T, HD, NT, kCluster ? 1 : 2, kCluster ? 4 : 3, false>(
         k,
         [=](int i) {
           return i == 0 ? first
@@ -1138,7 +1152,7 @@ __global__ void __launch_bounds__(warps_of(HD, NT, kCluster) * 32, 1)
     cluster_sync();
     // one part in each working block, in their order
     const uint32_t mine = smem_at + L::kBlockPart;
-    join_parts<T, HD, NT, 8, true>(
+    join_parts<T, HD, NT, 1, 8, true>(
         deal.ctas, [=](int i) { return mapa_shared(mine, (uint32_t)i); },
         Target<T>(p, cur_r, fixed_sub, HD), nullptr, rank + warp * most,
         most * W);
