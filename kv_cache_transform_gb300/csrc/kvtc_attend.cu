@@ -1179,72 +1179,52 @@ __global__ void __launch_bounds__(warps_of(HD, NT, kCluster) * 32, 1)
   }
 }
 
-// Items that lie over several blocks: block c joins the one that began in
-// block c of the attention, its own part and those of the blocks after it.
-// Groups of warps take every kGroups-th part, kBatch of them with all loads
-// in flight (before it is known how many there are), and are joined through
-// shared memory.
-__host__ __device__ constexpr int join_groups(int tiles) {
-  return tiles > 16 ? 1 : tiles > 8 ? 2 : 4;
-}
-template <class T, int HD, int NT>
-__global__ void __launch_bounds__(HD / 16 * NT * 32 *
-                                  join_groups(HD / 16 * NT))
-    attend_join_kernel(const __grid_constant__ AttendParams p) {
-  constexpr int kTiles = HD / 16 * NT, kGroups = join_groups(kTiles);
-  constexpr int kBatch = 5;
-  __shared__ float4 part_o[kGroups][kTiles * 32];
-  __shared__ float4 part_ml[kGroups][kTiles * 32];
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int tile = warp % kTiles, group = warp / kTiles;
-  const int nt = tile % NT, col = nt * 8 + (lane & 3) * 2;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+// A running join at one fragment position (two columns), of parts that other
+// blocks left in the workspace.
+template <int HD, int NT>
+struct FarJoin {
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
   float o[4] = {0.f, 0.f, 0.f, 0.f};
-  int4 d = make_int4(-1, 0, 0, 0);
-  int n = kCtas;
-  for (int i0 = group; i0 < n; i0 += kGroups * kBatch) {
-    float2 mi[kBatch], li[kBatch];
-    float4 oi[kBatch];
+  // Parts i0, i0 + kStep .. (N of them) of the item that began in block c, as
+  // far as there are n; all loads are in flight before n is asked for.
+  template <int N, int kStep, class F>
+  __device__ __forceinline__ void add(const float* slots, int c, int i0,
+                                      int tile, F n) {
+    const int lane = (int)lane_id();
+    const int col = tile % NT * 8 + (lane & 3) * 2;
+    float2 mi[N], li[N];
+    float4 oi[N];
 #pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      const int i = i0 + b * kGroups;
-      const float* s = p.cta_slots +
-                       ((int64_t)min(c + i, kCtas - 1) * 2 + (i ? 0 : 1)) *
-                           slot_floats(HD, NT);
+    for (int b = 0; b < N; ++b) {
+      const int i = i0 + b * kStep;
+      const float* s = slots + ((int64_t)min(c + i, kCtas - 1) * 2 +
+                                (i ? 0 : 1)) * slot_floats(HD, NT);
       mi[b] = __ldcg(reinterpret_cast<const float2*>(s + NT * 8 * HD + col));
       li[b] = __ldcg(
           reinterpret_cast<const float2*>(s + NT * 8 * (HD + 1) + col));
       oi[b] = __ldcg(reinterpret_cast<const float4*>(s) + tile * 32 + lane);
     }
-    if (i0 == group) {
-      d = __ldcg(reinterpret_cast<const int4*>(p.desc + c));
-      if (d.x < 0) return;
-      n = d.z - c + 1;
-    }
+    const int end = n();
     float mn[2] = {m[0], m[1]};
 #pragma unroll
-    for (int b = 0; b < kBatch; ++b)
-      if (i0 + b * kGroups < n) {
+    for (int b = 0; b < N; ++b)
+      if (i0 + b * kStep < end) {
         mn[0] = fmaxf(mn[0], mi[b].x);
         mn[1] = fmaxf(mn[1], mi[b].y);
       }
-    const float b0 = base_of(mn[0]), b1 = base_of(mn[1]);
-    const float a0 = exp2_fast(m[0] - b0), a1 = exp2_fast(m[1] - b1);
-    m[0] = mn[0];
-    m[1] = mn[1];
-    l[0] *= a0;
-    l[1] *= a1;
-    o[0] *= a0;
-    o[1] *= a1;
-    o[2] *= a0;
-    o[3] *= a1;
 #pragma unroll
-    for (int b = 0; b < kBatch; ++b)
-      if (i0 + b * kGroups < n) {
-        const float f0 = exp2_fast(mi[b].x - b0);
-        const float f1 = exp2_fast(mi[b].y - b1);
+    for (int k = 0; k < 2; ++k) {
+      const float f = exp2_fast(m[k] - base_of(mn[k]));
+      m[k] = mn[k];
+      l[k] *= f;
+      o[k] *= f;
+      o[k + 2] *= f;
+    }
+#pragma unroll
+    for (int b = 0; b < N; ++b)
+      if (i0 + b * kStep < end) {
+        const float f0 = exp2_fast(mi[b].x - base_of(m[0]));
+        const float f1 = exp2_fast(mi[b].y - base_of(m[1]));
         l[0] += li[b].x * f0;
         l[1] += li[b].y * f1;
         o[0] += oi[b].x * f0;
@@ -1253,36 +1233,77 @@ __global__ void __launch_bounds__(HD / 16 * NT * 32 *
         o[3] += oi[b].w * f1;
       }
   }
+  // Another such join, with {m, m, l, l}.
+  __device__ __forceinline__ void more(const float4& x, const float4& y) {
+    const float m0 = fmaxf(m[0], y.x), m1 = fmaxf(m[1], y.y);
+    const float f0 = exp2_fast(m[0] - base_of(m0));
+    const float f1 = exp2_fast(m[1] - base_of(m1));
+    const float g0 = exp2_fast(y.x - base_of(m0));
+    const float g1 = exp2_fast(y.y - base_of(m1));
+    m[0] = m0;
+    m[1] = m1;
+    l[0] = l[0] * f0 + y.z * g0;
+    l[1] = l[1] * f1 + y.w * g1;
+    o[0] = o[0] * f0 + x.x * g0;
+    o[1] = o[1] * f1 + x.y * g1;
+    o[2] = o[2] * f0 + x.z * g0;
+    o[3] = o[3] * f1 + x.w * g1;
+  }
+};
+
+// Items that lie over several blocks: block c joins the one that began in
+// block c of the attention, its own part and those of the blocks after it, a
+// warp per channel tile.  With many items there are two or three parts mostly,
+// and blocks of that size find room beside the attention's and wait for its
+// end in place.  Where an item lies over kFewParts blocks or more on average,
+// join_groups groups of warps take every so-many-th part and are joined
+// through shared memory.  One group and join_groups: 64 requests up to 4K
+// (256 items) 48.5 and 49.8 us; two of 32K (16 items) 39.6 and 39.0, one
+// (8 items) 30.5 and 29.2.
+constexpr int kFewParts = 8;
+__host__ __device__ constexpr int join_groups(int tiles) {
+  return tiles > 16 ? 1 : tiles > 8 ? 2 : 4;
+}
+template <class T, int HD, int NT, int kGroups>
+__global__ void __launch_bounds__(HD / 16 * NT * 32 * kGroups)
+    attend_join_kernel(const __grid_constant__ AttendParams p) {
+  constexpr int kTiles = HD / 16 * NT;
+  constexpr int kFirst = kGroups > 1 ? 5 : 3;
+  constexpr int kNext = kTiles * kGroups > 16 ? 5 : 8;   // by registers
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int c = blockIdx.x, warp = threadIdx.x >> 5;
+  const int tile = warp % kTiles, group = warp / kTiles;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  int4 d;
+  int n;
+  FarJoin<HD, NT> join;
+  join.template add<kFirst, kGroups>(p.cta_slots, c, group, tile, [&] {
+    d = __ldcg(reinterpret_cast<const int4*>(p.desc + c));
+    n = d.x < 0 ? 0 : d.z - c + 1;
+    return n;
+  });
+  if (n == 0) return;
+#pragma unroll 1
+  for (int i = group + kFirst * kGroups; i < n; i += kNext * kGroups)
+    join.template add<kNext, kGroups>(p.cta_slots, c, i, tile,
+                                      [&] { return n; });
   if (kGroups > 1) {
-    part_o[group][tile * 32 + lane] = make_float4(o[0], o[1], o[2], o[3]);
-    part_ml[group][tile * 32 + lane] = make_float4(m[0], m[1], l[0], l[1]);
+    __shared__ float4 part_o[kGroups][kTiles * 32];
+    __shared__ float4 part_ml[kGroups][kTiles * 32];
+    const int at = tile * 32 + (int)lane_id();
+    part_o[group][at] =
+        make_float4(join.o[0], join.o[1], join.o[2], join.o[3]);
+    part_ml[group][at] =
+        make_float4(join.m[0], join.m[1], join.l[0], join.l[1]);
     __syncthreads();
     if (group) return;
 #pragma unroll
-    for (int g = 1; g < kGroups; ++g) {
-      const float4 y = part_ml[g][tile * 32 + lane];
-      m[0] = fmaxf(m[0], y.x);
-      m[1] = fmaxf(m[1], y.y);
-    }
-    l[0] = l[1] = o[0] = o[1] = o[2] = o[3] = 0.f;
-#pragma unroll
-    for (int g = 0; g < kGroups; ++g) {
-      const float4 y = part_ml[g][tile * 32 + lane];
-      const float4 x = part_o[g][tile * 32 + lane];
-      const float f0 = exp2_fast(y.x - base_of(m[0]));
-      const float f1 = exp2_fast(y.y - base_of(m[1]));
-      l[0] += y.z * f0;
-      l[1] += y.w * f1;
-      o[0] += x.x * f0;
-      o[1] += x.y * f1;
-      o[2] += x.z * f0;
-      o[3] += x.w * f1;
-    }
+    for (int g = 1; g < kGroups; ++g) join.more(part_o[g][at], part_ml[g][at]);
   }
   const Target<T> target(p, d.x, (uint32_t)d.y, HD);
-  const float inv[2] = {inverse(l[0]), inverse(l[1])};
-  target.template store<HD>(nt, tile / NT, o, inv);
-  if (tile < NT) target.store_lse(nt, m, l);
+  const float inv[2] = {inverse(join.l[0]), inverse(join.l[1])};
+  target.template store<HD>(tile % NT, tile / NT, join.o, inv);
+  if (tile < NT) target.store_lse(tile % NT, join.m, join.l);
 }
 
 template <class T, int HD, int NT>
@@ -1308,9 +1329,12 @@ cudaError_t launch_as(const AttendParams& p, int cluster, int device,
     e = launch_kernel(kernel, kCtas, L::W * 32, L::kBytes, st, true, 0, p);
   if (e != cudaSuccess) return e;
   count_launch();
-  constexpr int kTiles = HD / 16 * NT;
-  e = launch_kernel(attend_join_kernel<T, HD, NT>, kCtas,
-                    kTiles * 32 * join_groups(kTiles), 0, st, true, 0, p);
+  constexpr int kTiles = HD / 16 * NT, kGroups = join_groups(kTiles);
+  const bool few = (int64_t)p.R * p.kv_heads * p.tiles * kFewParts <= kCtas;
+  e = launch_kernel(few ? attend_join_kernel<T, HD, NT, kGroups>
+                        : attend_join_kernel<T, HD, NT, 1>,
+                    kCtas, kTiles * 32 * (few ? kGroups : 1), 0, st, true, 0,
+                    p);
   if (e == cudaSuccess) count_launch();
   return e;
 }
@@ -1357,7 +1381,8 @@ cudaError_t launch(const AttendParams& p, int head_dim, int nt, int cluster,
   if (head_dim == 128)
     return nt == 1 ? launch_as<T, 128, 1>(p, cluster, device, st)
                    : launch_as<T, 128, 2>(p, cluster, device, st);
-  return nt == 1 ? launch_as<T, 256, 1>(p, cluster, device, st) : launch_as<T, 256, 2>(p, cluster, device, st);
+  return nt == 1 ? launch_as<T, 256, 1>(p, cluster, device, st)
+                 : launch_as<T, 256, 2>(p, cluster, device, st);
 }
 
 // A pool [num_blocks][16][D] as {64 channels, 16 tokens, D / 64, num_blocks}:
