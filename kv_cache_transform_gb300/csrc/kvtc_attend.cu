@@ -175,32 +175,35 @@ __device__ __forceinline__ float exp2_fast(float x) {
 }
 
 // Loads from this block's shared memory, or from that of the cluster's blocks
-// (which takes several times as long, for an own address too).  Not volatile:
-// what they read was written before the caller's last barrier.
+// (which takes several times as long, for an own address too).
 template <bool across>
 __device__ __forceinline__ float2 lds2(uint32_t addr) {
   float2 v;
   if (across)
-    asm("ld.shared::cluster.v2.f32 {%0,%1}, [%2];"
-        : "=f"(v.x), "=f"(v.y)
-        : "r"(addr));
+    asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];"
+                 : "=f"(v.x), "=f"(v.y)
+                 : "r"(addr)
+                 : "memory");
   else
-    asm("ld.shared.v2.f32 {%0,%1}, [%2];"
-        : "=f"(v.x), "=f"(v.y)
-        : "r"(addr));
+    asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];"
+                 : "=f"(v.x), "=f"(v.y)
+                 : "r"(addr)
+                 : "memory");
   return v;
 }
 template <bool across>
 __device__ __forceinline__ float4 lds4(uint32_t addr) {
   float4 v;
   if (across)
-    asm("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
-        : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-        : "r"(addr));
+    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
   else
-    asm("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
-        : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-        : "r"(addr));
+    asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
   return v;
 }
 __device__ __forceinline__ float rcp_fast(float x) {
@@ -418,8 +421,6 @@ struct Target {
   T* out;           // its first head
   float* lse;       // or null
   int rows;         // heads
-  __device__ __forceinline__ Target(T* out_, float* lse_, int rows_)
-      : out(out_), lse(lse_), rows(rows_) {}
   __device__ __forceinline__ Target(const AttendParams& p, int r,
                                     uint32_t sub, int hd) {
     const Heads h(p, sub);
