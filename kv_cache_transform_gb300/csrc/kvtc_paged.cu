@@ -5,10 +5,11 @@
 // of b, and request r takes free[head + C_r - b_r ...] if it fits.  Both are
 // integer sums, so the result is exact and does not depend on the launch.
 //   few slots (decode steps): assign_small_kernel, one block, a thread per
-//     request: one launch and a chain of three loads, 1.8 us;
-//   more: assign_scan_kernel, one block, forms the sums, and
-//     assign_fill_kernel, behind it on the whole GPU, writes the table
-//     entries and the slots.
+//     request: a chain of three loads, 1.8 us;
+//   more: assign_fill_kernel on the whole GPU writes the table entries and
+//     the slots; every block forms the sums itself, or assign_scan_kernel
+//     does so before it, in one block (more than 1024 requests, or a state
+//     that is kept in place).
 // kvtc_paged_append: append_kernel, a warp per row.
 #include <cuda_runtime.h>
 
@@ -119,9 +120,12 @@ __device__ __forceinline__ int64_t slot_of(int64_t id, int64_t t) {
 
 // One block, a thread per request (R <= 1024).  Where a request has few new
 // tokens its thread writes their slots, else the warps share them.
+// (64 requests of 16 new tokens 4.6 us, where the warps share all above four
+// tokens 13.2, by assign_fill_kernel 7.3; of 32, 13.4 and 5.8; 1024 of 8, 8.6
+// and 10.9, of 16, 14.7 and 10.9.)
 constexpr int kSmallReq = 1024;
-constexpr int64_t kSmallSlots = 2048;  // beyond, two launches are faster
-constexpr int kSmallOwn = 4;         // tokens that a thread writes itself
+constexpr int64_t kSmallSlots = 8192;  // and kSmallOwn a request
+constexpr int kSmallOwn = 16;          // tokens that a thread writes itself
 __global__ void __launch_bounds__(kSmallReq)
     assign_small_kernel(const __grid_constant__ AssignParams p) {
   __shared__ int64_t sums[64];
@@ -189,15 +193,13 @@ __global__ void __launch_bounds__(kSmallReq)
   if (r == 0) *p.head_out = head + (int64_t)given;
 }
 
-// One block, `per` consecutive requests per thread.
-__global__ void __launch_bounds__(kScanThreads)
-    assign_scan_kernel(const __grid_constant__ AssignParams p, int per) {
-  __shared__ int64_t sums[64];
-  __shared__ unsigned long long given;   // blocks given out
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+// One block forms the sums, `per` consecutive requests per thread, into cu
+// and rows; where `writes`, it also writes what the call returns of them.
+__device__ __forceinline__ void scan_requests(const AssignParams& p, int per,
+                                              bool writes, int64_t* sums,
+                                              unsigned long long* given,
+                                              int64_t* cu, AssignRow* rows) {
   const int tid = threadIdx.x;
-  if (tid == 0) given = 0;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int64_t head = *p.head;
   bool head_ok;
   const int64_t left = free_left(p, head, &head_ok);
@@ -216,7 +218,8 @@ __global__ void __launch_bounds__(kScanThreads)
     const int r = tid * per + i;
     if (r >= p.R) break;
     const Demand d(p, r);
-    p.cu[r] = upto;
+    cu[r] = upto;
+    if (writes) p.cu[r] = upto;
     upto += d.fresh;
     used += d.need;
     const bool served = d.fits && (d.need == 0 || used <= left);
@@ -224,18 +227,31 @@ __global__ void __launch_bounds__(kScanThreads)
     row.first = head + used - d.need;
     row.held = d.held;
     row.blocks = served ? d.need : -1;
-    p.rows[r] = row;
+    rows[r] = row;
+    if (!writes) continue;
     // (a request's held is read for the last time above)
     p.held_out[r] = served ? max(d.held, d.lens) : d.held;
-    if (served && d.need) atomicMax(&given, (unsigned long long)used);
+    if (served && d.need) atomicMax(given, (unsigned long long)used);
     short_of |= !served && d.fresh;
   }
-  if (short_of && p.flags) atomicOr(p.flags, KVTC_FLAG_SPACE);
-  __syncthreads();
-  if (tid == 0) {
-    p.cu[p.R] = total;
-    *p.head_out = head + (int64_t)given;
+  if (tid == 0) cu[p.R] = total;
+  if (writes) {
+    if (short_of && p.flags) atomicOr(p.flags, KVTC_FLAG_SPACE);
+    __syncthreads();
+    if (tid == 0) {
+      p.cu[p.R] = total;
+      *p.head_out = head + (int64_t)*given;
+    }
   }
+}
+__global__ void __launch_bounds__(kScanThreads)
+    assign_scan_kernel(const __grid_constant__ AssignParams p, int per) {
+  __shared__ int64_t sums[64];
+  __shared__ unsigned long long given;   // blocks given out
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (threadIdx.x == 0) given = 0;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  scan_requests(p, per, true, sums, &given, p.cu, p.rows);
 }
 
 // Last request r in [lo, hi] with cu[r] <= j (cu[lo] <= j); the whole warp
@@ -259,24 +275,41 @@ __device__ __forceinline__ int request_at(const int64_t* cu, int lo, int hi,
 // their first request once; each lane goes on from there (tokens mostly lie
 // many to a request).  The lane that has a new block's first token writes its
 // table entry; blocks whose first token lies behind the slot map come after.
-// 131 thousand slots (1 MB) take 7.4 us with the scan, 2.1 million (17 MB)
-// 10.4: two launches, and chains of loads in each.  (One cluster of 16 blocks
-// that each form the sums: 7.6 and 35 us.)
+// 131 thousand slots (1 MB) take 4.6 us, 2.1 million (17 MB) 8.0 (with twice
+// the blocks 9.2, with half of them 8.4).
+//
+// kOwnSums: every block forms the sums itself, in shared memory, instead of a
+// launch before that does (7.4 and 10.5 us); not for a state kept in place,
+// which one block would change while another still reads it.
 constexpr int kFillRun = 256;
-__global__ void __launch_bounds__(256)
+constexpr int kFillThreads = 256;
+template <bool kOwnSums>
+__global__ void __launch_bounds__(kFillThreads)
     assign_fill_kernel(const __grid_constant__ AssignParams p) {
+  __shared__ int64_t own_cu[kOwnSums ? kSmallReq + 1 : 1];
+  __shared__ AssignRow own_rows[kOwnSums ? kSmallReq : 1];
+  __shared__ int64_t sums[64];
+  __shared__ unsigned long long given;
+  const int64_t* cu = kOwnSums ? own_cu : p.cu;
+  const AssignRow* rows = kOwnSums ? own_rows : p.rows;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (kOwnSums && threadIdx.x == 0) given = 0;
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (kOwnSums) {
+    scan_requests(p, (p.R + kFillThreads - 1) / kFillThreads,
+                  blockIdx.x == 0, sums, &given, own_cu, own_rows);
+    __syncthreads();
+  }
   const int lane = threadIdx.x & 31;
   const int64_t warp = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
   const int64_t warps = ((int64_t)gridDim.x * blockDim.x) >> 5;
-  const int64_t total = p.cu[p.R];
+  const int64_t total = cu[p.R];
   for (int64_t j0 = warp * kFillRun; j0 < p.slot_capacity;
        j0 += warps * kFillRun) {
     // (looked up before `total` is here to say whether it is of use)
-    int r = p.R ? request_at(p.cu, 0, p.R - 1, j0) : 0;
-    const AssignRow row0 = p.R ? p.rows[r] : AssignRow{0, 0, -1};
-    const int64_t from0 = p.cu[r], to0 = p.R ? p.cu[r + 1] : 0;
+    int r = p.R ? request_at(cu, 0, p.R - 1, j0) : 0;
+    const AssignRow row0 = p.R ? rows[r] : AssignRow{0, 0, -1};
+    const int64_t from0 = cu[r], to0 = p.R ? cu[r + 1] : 0;
     const int64_t end = min(total, p.slot_capacity);
     if (j0 + kFillRun <= min(end, to0)) {
       // the whole run is one request's (in a third of the instructions)
@@ -317,16 +350,16 @@ __global__ void __launch_bounds__(256)
       int64_t slot = -1;
       if (j < end) {
         if (j >= to) {
-          if (p.cu[r + 1] <= j && p.cu[++r + 1] <= j) {
+          if (cu[r + 1] <= j && cu[++r + 1] <= j) {
             int hi = p.R - 1;
             while (r < hi) {
               const int mid = (r + hi + 1) >> 1;
-              if (p.cu[mid] <= j) r = mid; else hi = mid - 1;
+              if (cu[mid] <= j) r = mid; else hi = mid - 1;
             }
           }
-          const AssignRow row = p.rows[r];
-          from = p.cu[r];
-          to = p.cu[r + 1];
+          const AssignRow row = rows[r];
+          from = cu[r];
+          to = cu[r + 1];
           held = row.held;
           had = (int32_t)blocks_of(held);
           served = row.blocks >= 0;
@@ -345,9 +378,9 @@ __global__ void __launch_bounds__(256)
   }
   if (total <= p.slot_capacity) return;
   for (int64_t r = warp; r < p.R; r += warps) {
-    const AssignRow row = p.rows[r];
+    const AssignRow row = rows[r];
     // the first block whose first token has no place in the map
-    const int64_t mapped = max(p.slot_capacity - p.cu[r], (int64_t)0);
+    const int64_t mapped = max(p.slot_capacity - cu[r], (int64_t)0);
     const int64_t had = blocks_of(row.held);
     const int64_t i0 = max(blocks_of(row.held + mapped) - had, (int64_t)0);
     int32_t* to = p.table + r * p.max_blocks + had;
@@ -460,9 +493,21 @@ int kvtc_paged_assign(int cuda_device, int R, const int32_t* held,
   p.flags = flags;
   p.R = R;
   p.max_blocks = max_blocks;
-  if (R <= kSmallReq && slot_capacity <= kSmallSlots) {
+  if (R <= kSmallReq &&
+      slot_capacity <= std::min(kSmallSlots, (int64_t)kSmallOwn * R)) {
     if (launch_kernel(assign_small_kernel, 1, std::max(32, (R + 31) / 32 * 32),
                       0, st, true, 0, p) != cudaSuccess)
+      return KVTC_ECUDA;
+    count_launch();
+    return KVTC_OK;
+  }
+  // (capacity is what the host knows of the tokens)
+  const int64_t runs = std::max<int64_t>(
+      (slot_capacity + kFillRun - 1) / kFillRun, 152 * 8);
+  const unsigned grid = (unsigned)std::min<int64_t>((runs + 7) / 8, 4 * 152);
+  if (R <= kSmallReq && held_out != held && head_out != head) {
+    if (launch_kernel(assign_fill_kernel<true>, grid, kFillThreads, 0, st,
+                      true, 0, p) != cudaSuccess)
       return KVTC_ECUDA;
     count_launch();
     return KVTC_OK;
@@ -473,12 +518,8 @@ int kvtc_paged_assign(int cuda_device, int R, const int32_t* held,
                     true, 0, p, per) != cudaSuccess)
     return KVTC_ECUDA;
   count_launch();
-  // (capacity is what the host knows of the tokens)
-  const int64_t runs = std::max<int64_t>(
-      (slot_capacity + kFillRun - 1) / kFillRun, 152 * 8);
-  if (launch_kernel(assign_fill_kernel,
-                    (unsigned)std::min<int64_t>((runs + 7) / 8, 8 * 152), 256,
-                    0, st, true, 0, p) != cudaSuccess)
+  if (launch_kernel(assign_fill_kernel<false>, grid, kFillThreads, 0, st,
+                    true, 0, p) != cudaSuccess)
     return KVTC_ECUDA;
   count_launch();
   return KVTC_OK;

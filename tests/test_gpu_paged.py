@@ -177,8 +177,8 @@ def test_assign_lengths_far_beyond_the_map(kv, R, cap):
 @pytest.mark.parametrize("R,hi", [(1024, 3), (1025, 3), (4096, 60), (600, 1),
                                   (64, 32), (64, 33), (64, 128), (64, 129)])
 def test_assign_with_many_empty_requests(kv, R, hi):
-    """On both sides of the single launch's limits (1024 requests, 2048
-    slots), with long runs of requests that want nothing."""
+    """Long runs of requests that want nothing, and calls on both sides of
+    the 1024 requests of a single launch."""
     rng = np.random.default_rng(R + hi)
     lens = rng.integers(1, hi + 1, R)
     lens[rng.integers(0, R, R // 2)] = 0
@@ -189,6 +189,34 @@ def test_assign_with_many_empty_requests(kv, R, hi):
     free, head, table = start_state(rng, held, blocks_of(hi) + 1,
                                     int(sum(blocks_of(n) for n in lens)) + 5)
     run_assign(kv, held, lens, free, head, table, int(lens.sum()))
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("trouble", [None, "list", "map", "table", "ids"])
+@pytest.mark.parametrize("R,each", [(7, 15), (7, 17), (64, 16), (64, 18),
+                                    (512, 16), (512, 17), (1024, 8),
+                                    (1024, 9)])
+def test_assign_around_the_limits_of_its_forms(kv, R, each, trouble,
+                                               in_place):
+    """On both sides of 16 slots a request and of 8192, with the state in
+    place and not, where all is well and where something is short."""
+    rng = np.random.default_rng(R + each)
+    held = rng.integers(0, 20, R)
+    lens = held + each
+    if trouble == "table":
+        lens[R // 2] = 16 * 4 + 1
+        held[R // 3] = lens[R // 3] + 3
+    free, head, table = start_state(rng, held, 4, 3 * R + 9)
+    cap = int(np.maximum(lens - held, 0).sum())
+    if trouble == "list":
+        free = free[:head + R // 2]
+    elif trouble == "map":
+        cap = cap // 3
+    elif trouble == "ids":
+        table[R // 2] = -5
+        free = free.copy()
+        free[head + 1::7] = -1
+    run_assign(kv, held, lens, free, head, table, cap, in_place=in_place)
 
 
 @pytest.mark.parametrize("head", [-1, 6, 1 << 40])
