@@ -35,13 +35,14 @@
 // (p = hi + lo to 2^-15), so that only the output's own rounding is of 16
 // bits.
 //
-// What bounds it.  HBM: each attended row of K and V is read once, 4 heads
-// flops a row element, 44 TFLOP/s at eight query heads a KV head, a small
-// part of what mma.sync gives.  Between the first page and the last one SM
-// after the other reads at 7.8 TB/s in all (570 MB: 16 requests up to 16K,
-// 93 us in all, 6.1 TB/s); the rest is latency: 3.5 us until the first page
-// (lengths, block table, page, one after the other), and 6 us of joining
-// after the last.
+// What bounds it.  HBM: each attended row of K and V is read once, at 4 heads
+// flops a row element (50 TFLOP/s at eight query heads a KV head, a small
+// part of what mma.sync gives).  While all warps have pages to ask for, the
+// SMs read 7.8 TB/s together (570 MB, 16 requests up to 16K: 92 us in all,
+// 6.2 TB/s); the rest is latency: 3.6 us until the first page (lengths, block
+// table, page, one after the other), and after the last ones 4 us, more or
+// less, of warps that end apart, 2 us of the block's join, 2 to 3 us of the
+// launch behind.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -80,9 +81,10 @@ __host__ __device__ constexpr int slot_floats(int hd, int nt) {
 // Warps per block, for nt tiles of eight query heads per warp: as many as
 // registers and shared memory hold (a cluster's blocks need less of it), with
 // one page each in flight (two where 12 or fewer warps read the small pages
-// of head_dim 64).  More warps with one page beat fewer with two: 64 requests
-// up to 4K at head_dim 128, 12 x 1 against 10 x 2: 50.5 and 53.1 us; up to 8K
-// at head_dim 64, 16 x 1 against 12 x 2: 102 and 105 us.
+// of head_dim 64).  More warps with one page mostly beat fewer with two: 64
+// requests up to 4K at head_dim 128, 12 x 1 against 9 x 2: 48.5 and 49.7 us;
+// 64 of 2K to 4K at head_dim 64 (8 KV heads), 16 x 1 against 12 x 2: 73.0 and
+// 74.4 (32 of 4K to 8K, 4 KV heads: 40.0 and 38.3).
 __host__ __device__ constexpr int warps_of(int hd, int nt, bool cluster) {
   return hd == 64    ? (nt == 1 ? 16 : nt == 2 ? 12 : 8)
          : hd == 128 ? (nt == 1 ? (cluster ? 14 : 12) : 8)
@@ -1344,10 +1346,12 @@ cudaError_t launch_as(const AttendParams& p, int cluster, int device,
 // clusters of 16 such blocks at once, 15 of 8, 36 of 4, 76 of 2 (what
 // cudaOccupancyMaxActiveClusters says of it).  A cluster of more blocks than
 // the longest item can feed is of no use.  What clusters save is the join
-// across blocks, about 6 us; what they lose is that items * cluster blocks,
+// across blocks, about 3 us; what they lose is that items * cluster blocks,
 // at about 90 GB/s a block, may read slower than all SMs at 7000 GB/s, which
 // is taken at the longest length that the table allows, for the others half
-// of that.
+// of that.  Clusters and runs, 32 heads on 8 of 128: one request of 2K 9.6
+// and 11.6 us, 8K 12.2 and 14.5, 16K 19.1 and 20.3, 32K 29.9 and 29.1; two of
+// 8K 18.2 and 17.1; 16 of up to 1K 14.1 and 16.5.
 int cluster_of(int R, int64_t items, int64_t max_blocks, int head_dim,
                int nt) {
   if (items > kCtas) return 0;
@@ -1365,9 +1369,9 @@ int cluster_of(int R, int64_t items, int64_t max_blocks, int head_dim,
 // Tiles of eight query heads per warp: one or two, by the group, and four for
 // large groups of head_dim 64.  Larger groups are cut into equal tiles of
 // heads, each of which reads the pages again (from L2, mostly).  At 32 heads
-// a KV head (32 requests up to 8K), one pass with four tiles takes 154 us at
-// head_dim 64, two passes with two 183; at 128 it is 217 and 175: the
-// accumulators of 32 heads leave too few warps.
+// a KV head, one pass with four tiles takes 59.8 us at head_dim 64, two with
+// two 69.1 (32 requests of 4K to 8K, 4 KV heads); at 128 it was 217 and 175
+// (32 up to 8K, 8 KV heads): the accumulators of 32 heads leave too few warps.
 int head_tiles(int head_dim, int group) {
   return group <= 8 ? 1 : group <= 16 || head_dim > 64 ? 2 : 4;
 }
