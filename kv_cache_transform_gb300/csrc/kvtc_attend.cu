@@ -69,6 +69,7 @@ constexpr int kMaxTable = INT32_MAX / kBlock - 1;  // table columns: token
                                      // indices and a page more in 32 bits
 constexpr int kCtas = 152;           // one block per SM
 constexpr int kLeast = 2;            // units per warp
+constexpr int kFewReq = 128;         // requests that each warp sums itself
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kSlack = 6.f;        // log2; see the reference in the loop
@@ -284,21 +285,23 @@ struct Span {
   int32_t len, units, front, gap;
   bool hole;      // tokens between the sink and the window are left out
 };
-__device__ __forceinline__ Span span_of(const AttendParams& p, int r) {
-  Span s;
-  const int64_t room = (int64_t)p.max_blocks * kBlock;
-  const int32_t len = max(p.lens[r], 0);
-  s.len = (int32_t)min((int64_t)len, room);
-  const int32_t all = (int32_t)(((int64_t)s.len + kBlock - 1) / kBlock);
+__device__ __forceinline__ Span span_of_len(const AttendParams& p,
+                                            int32_t len) {
+  Span s;       // (kMaxTable keeps all of this inside 32 bits)
+  s.len = min(max(len, 0), p.max_blocks * kBlock);
+  const int32_t all = (s.len + kBlock - 1) / kBlock;
   s.front = all;
   s.gap = 0;
-  s.hole = p.window && (int64_t)p.sink + p.window < s.len;
+  s.hole = p.window && (uint32_t)p.sink + p.window < (uint32_t)s.len;
   if (s.hole) {
-    s.front = (int32_t)(((int64_t)p.sink + kBlock - 1) / kBlock);
+    s.front = (p.sink + kBlock - 1) / kBlock;
     s.gap = max((s.len - p.window) / kBlock - s.front, 0);
   }
   s.units = max(all - s.gap, 1);
   return s;
+}
+__device__ __forceinline__ Span span_of(const AttendParams& p, int r) {
+  return span_of_len(p, p.lens[r]);
 }
 
 // a / b and the remainder, for a quotient below 2^20 (a float quotient is
@@ -611,13 +614,16 @@ __global__ void __launch_bounds__(warps_of(HD, NT, kCluster) * 32, 1)
   }
   if (tid == 0) *abort_flag = 0;
   fence_mbar_init();
+  __syncthreads();
   // Everything this call reads may come from the launch before it, and is
   // read by plain loads: this grid may have started under that one, so the
   // read-only path could hold what it held before.
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
   // This warp's run of units, and the request that holds its first one.
-  int64_t total;
+  const bool few = p.R <= kFewReq;
+  const int per = few ? (p.R + 31) / 32 : (p.R + kThreads - 1) / kThreads;
+  int64_t total, ahead = 0;    // ahead: units before this lane's requests
   int most = kCtas, rank = blockIdx.x, cur_r = 0;
   uint32_t fixed_sub = 0;
   if (kCluster) {
@@ -628,12 +634,36 @@ __global__ void __launch_bounds__(warps_of(HD, NT, kCluster) * 32, 1)
     fixed_sub = (uint32_t)(id - cur_r * items);
     total = span_of(p, cur_r).units;
     if (tid == 0 && p.flags &&
-        p.lens[cur_r] > (int64_t)p.max_blocks * kBlock)
+        p.lens[cur_r] > p.max_blocks * kBlock)
       atomicOr(p.flags, KVTC_FLAG_SPACE);
-    __syncthreads();
+  } else if (few) {
+    // Every warp sums them itself, `per` requests a lane.
+    int32_t len[kFewReq / 32];
+#pragma unroll
+    for (int i = 0; i < kFewReq / 32; ++i) {
+      const int r = lane * per + i;
+      len[i] = i < per && r < p.R ? p.lens[r] : -1;
+    }
+    int64_t sum = 0;
+#pragma unroll 1
+    for (int i = 0; i < per; ++i) {
+      if (lane * per + i < p.R) sum += span_of_len(p, len[0]).units;
+      if (p.flags && blockIdx.x == 0 && warp == 0 &&
+          len[0] > p.max_blocks * kBlock)
+        atomicOr(p.flags, KVTC_FLAG_SPACE);
+#pragma unroll
+      for (int j = 1; j < kFewReq / 32; ++j) len[j - 1] = len[j];
+    }
+    total = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t o = __shfl_up_sync(0xFFFFFFFFu, total, d);
+      if (lane >= d) total += o;
+    }
+    ahead = (total - sum) * items;
+    total = __shfl_sync(0xFFFFFFFFu, total, 31) * items;
   } else {
     // Units of the requests before each thread's run of requests.
-    const int per = (p.R + kThreads - 1) / kThreads;
     int64_t sum = 0;
 #pragma unroll 1
     for (int i = 0; i < per; ++i) {
@@ -641,7 +671,7 @@ __global__ void __launch_bounds__(warps_of(HD, NT, kCluster) * 32, 1)
       if (r >= p.R) break;
       sum += span_of(p, r).units;
       if (p.flags && blockIdx.x == 0 &&
-          p.lens[r] > (int64_t)p.max_blocks * kBlock)
+          p.lens[r] > p.max_blocks * kBlock)
         atomicOr(p.flags, KVTC_FLAG_SPACE);
     }
     int64_t upto = sum;
@@ -669,8 +699,12 @@ __global__ void __launch_bounds__(warps_of(HD, NT, kCluster) * 32, 1)
   const int64_t u1 = works ? deal.begin(worker + 1) : 0;
   const int n = (int)(u1 - u0);
   int64_t cur_s = 0;        // first unit of request cur_r
-  if (!kCluster && n) {
-    const int per = (p.R + kThreads - 1) / kThreads;
+  if (!kCluster && few && n) {
+    const int l = 31 - __clz(__ballot_sync(
+                           0xFFFFFFFFu, lane * per < p.R && ahead <= u0));
+    cur_r = l * per;
+    cur_s = __shfl_sync(0xFFFFFFFFu, ahead, l);
+  } else if (!kCluster && n) {
     int before = 0;         // runs of requests that begin at or before u0
 #pragma unroll
     for (int i = 0; i < W; ++i)
@@ -710,7 +744,7 @@ __global__ void __launch_bounds__(warps_of(HD, NT, kCluster) * 32, 1)
       b_id = -1;
       if (sp.len) {
         b_id = p.table[(int64_t)r * p.max_blocks + b_page];
-        if (b_id < 0 || b_id >= p.num_blocks) {
+        if ((uint32_t)b_id >= (uint32_t)p.num_blocks) {
           b_id = -1;
           if (p.flags) atomicOr(p.flags, KVTC_FLAG_BLOCK);
         }
@@ -718,7 +752,7 @@ __global__ void __launch_bounds__(warps_of(HD, NT, kCluster) * 32, 1)
       if (b_id < 0) b_sub |= kSkip;
       const int t0 = b_page * kBlock, recent = sp.hole ? sp.len - p.window : 0;
       if (sp.len - t0 >= kBlock &&
-          (t0 >= recent || (int64_t)t0 + kBlock <= p.sink))
+          (t0 >= recent || t0 + kBlock <= p.sink))
         b_sub |= kWhole;
       // (a cluster's items are few: it is not worth their code there)
       if (!kCluster && t0 + 8 <= recent && t0 >= p.sink) b_sub |= kNoLow;
