@@ -38,8 +38,8 @@
 // What bounds it.  HBM: each attended row of K and V is read once, at 4 heads
 // flops a row element (50 TFLOP/s at eight query heads a KV head, a small
 // part of what mma.sync gives).  While all warps have pages to ask for, the
-// SMs read 7.8 TB/s together (570 MB, 16 requests up to 16K: 92 us in all,
-// 6.2 TB/s); the rest is latency: 3.6 us until the first page (lengths, block
+// SMs read 7.8 TB/s together (570 MB, 16 requests up to 16K: 91 us in all,
+// 6.3 TB/s); the rest is latency: 3.6 us until the first page (lengths, block
 // table, page, one after the other), and after the last ones 4 us, more or
 // less, of warps that end apart, 2 us of the block's join, 2 to 3 us of the
 // launch behind.
@@ -637,7 +637,9 @@ __global__ void __launch_bounds__(warps_of(HD, NT, kCluster) * 32, 1)
         p.lens[cur_r] > p.max_blocks * kBlock)
       atomicOr(p.flags, KVTC_FLAG_SPACE);
   } else if (few) {
-    // Every warp sums them itself, `per` requests a lane.
+    // Every warp sums them itself, `per` requests a lane: no barrier, and the
+    // loop is kept short, as the code has to be fetched (64 requests up to 4K
+    // 48.1 us, by the block below 48.5; but 256 windows 34.9 and 34.3).
     int32_t len[kFewReq / 32];
 #pragma unroll
     for (int i = 0; i < kFewReq / 32; ++i) {
