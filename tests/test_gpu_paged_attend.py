@@ -146,6 +146,18 @@ def test_many_short_requests(kv):
     run(kv, 4, rng.integers(0, 20, 4096), 4, 1, 64, "fp16")
 
 
+@pytest.mark.parametrize("R", [31, 32, 33, 64, 65, 127, 128, 129, 257])
+def test_numbers_of_requests(kv, R):
+    """On both sides of what a lane and a warp hold of the lengths, empty
+    requests, short and long ones mixed."""
+    rng = np.random.default_rng(R)
+    lens = rng.integers(0, 90, R)
+    lens[rng.integers(0, R, R // 4)] = 0
+    lens[R // 2] = 700
+    lens[-1] = 33
+    run(kv, R, lens, 12, 6, 64)
+
+
 def test_one_request_among_empty_ones(kv):
     lens = np.zeros(700, np.int64)
     lens[311] = 2500
@@ -171,6 +183,34 @@ def test_sink_and_window(kv, sink, window):
     a = Attend(kv, q, k, v, table, lens, sink=sink, window=window)
     a.call()
     a.check()
+
+
+@pytest.mark.parametrize("sink,window", [
+    (2 ** 31 - 1, 2 ** 31 - 1), (2 ** 31 - 1, 1), (0, 2 ** 31 - 1),
+    (2 ** 31 - 17, 16)])
+@pytest.mark.parametrize("R", [2, 40])
+def test_sink_and_window_beyond_every_length(kv, sink, window, R):
+    run(kv, 7, [1 + 13 * i for i in range(R)], 8, 4, 64, sink=sink,
+        window=window)
+
+
+def test_the_widest_table(kv):
+    """A request of 2^31 - 32 tokens: its first 3 and last 20 are those of a
+    short one with the same first and last blocks."""
+    import torch
+    q, k, v, table, lens = paged_case(8, [64, 64, 50], 16, 2, 64)
+    a = Attend(kv, q, k, v, table, lens, sink=3, window=20)
+    ref = a.reference()
+    cols = 2 ** 27 - 2
+    wide = torch.zeros((3, cols), dtype=torch.int32, device="cuda")
+    wide[:, 0] = a.table[:, 0]
+    wide[:, cols - 2:] = a.table[:, 2:4]
+    wide[2] = 0
+    wide[2, :4] = a.table[2, :4]
+    a.table = wide
+    a.lens.copy_(torch.tensor([16 * cols, 16 * cols, 50]))
+    a.call()
+    a.check(ref)
 
 
 def test_sink_without_window_is_ignored(kv):
