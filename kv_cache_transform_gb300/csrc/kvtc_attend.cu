@@ -68,7 +68,6 @@ constexpr int kMaxGroup = 128;       // query heads per KV head
 constexpr int kMaxTable = INT32_MAX / kBlock - 1;  // table columns: token
                                      // indices and a page more in 32 bits
 constexpr int kCtas = 152;           // one block per SM
-constexpr int kLeast = 2;            // units per warp
 constexpr int kFewReq = 128;         // requests that each warp sums itself
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -122,12 +121,18 @@ struct AttendParams {
   float scale_log2;
   int32_t R, heads, kv_heads, max_blocks, sink, window;
   int32_t group, tiles, tile_heads;  // heads per KV head; tiles of them
+  uint32_t tiles_inv;                // 2^16 / tiles, rounded up
 };
 
 // ------------------------------------------------------------ PTX wrappers
 __device__ __forceinline__ uint32_t cluster_size() {
   uint32_t n;
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(n));
+  return n;
+}
+__device__ __forceinline__ uint32_t cluster_id() {    // in x
+  uint32_t n;
+  asm volatile("mov.u32 %0, %%clusterid.x;" : "=r"(n));
   return n;
 }
 __device__ __forceinline__ void tma_load_box(uint32_t smem_dst,
@@ -322,19 +327,19 @@ __device__ __forceinline__ int small_quotient(int64_t a, int32_t b,
 }
 // `total` units in order over the warps of the first `ctas` of `most` blocks:
 // the first `more` warps take least + 1 units, the others `least`.  With few
-// units, blocks are left out until every warp has kLeast of them: what
-// reading on more SMs saves, the join of more blocks costs.
+// units, blocks are left out until every warp has one.  (With two a warp or
+// more, one request of 1K, 32 heads on 8 of 128, took 9.3 us, not 8.1.)
 template <int W>
 struct Deal {
   int64_t least;
   int32_t more, ctas;
   __device__ __forceinline__ Deal(int64_t total, int most) {
-    if (most == kCtas && total >= (int64_t)kCtas * W * kLeast) {
+    if (most == kCtas && total >= kCtas * W) {
       ctas = kCtas;
       least = total / (kCtas * W);       // by a constant
     } else {
       // (a cluster's item has less than 2^28 units)
-      ctas = max(1, min(most, (int32_t)total / (W * kLeast)));
+      ctas = max(1, min(most, (int32_t)total / W));
       least = (uint32_t)total / (uint32_t)(ctas * W);
     }
     more = (int32_t)(total - least * (ctas * W));
@@ -409,11 +414,18 @@ struct Smem {
 __device__ __forceinline__ float base_of(float m) {
   return m == -INFINITY ? 0.f : m;
 }
+// An item's KV head: sub / tiles, by a reciprocal of 16 bits.  (Items per
+// request are at most 128 KV heads x 8 tiles: its error of at most 7 in 2^16
+// stays below 1 / tiles.  A division would be 20 instructions to fetch.)
+__device__ __forceinline__ int kv_head_of(const AttendParams& p,
+                                          uint32_t sub) {
+  return (int)((sub * p.tiles_inv) >> 16);
+}
 // The query heads of an item.
 struct Heads {
   int first, rows;
   __device__ __forceinline__ Heads(const AttendParams& p, uint32_t sub) {
-    const int j = p.tiles == 1 ? (int)sub : (int)sub / p.tiles;
+    const int j = kv_head_of(p, sub);
     const int t = (int)sub - j * p.tiles;
     first = j * p.group + t * p.tile_heads;
     rows = min(p.tile_heads, p.group - t * p.tile_heads);
@@ -629,9 +641,8 @@ __global__ void __launch_bounds__(warps_of(HD, NT, kCluster) * 32, 1)
   if (kCluster) {
     most = (int)cluster_size();
     rank = (int)cluster_ctarank();
-    const int id = (int)blockIdx.x / most;
-    cur_r = id / items;
-    fixed_sub = (uint32_t)(id - cur_r * items);
+    cur_r = blockIdx.y;
+    fixed_sub = cluster_id();
     total = span_of(p, cur_r).units;
     if (tid == 0 && p.flags &&
         p.lens[cur_r] > p.max_blocks * kBlock)
@@ -796,8 +807,7 @@ __global__ void __launch_bounds__(warps_of(HD, NT, kCluster) * 32, 1)
       const uint32_t sub = b_sub & kSubMask;
       const uint32_t page = page_loads();
       const uint32_t dst = ring + st * L::kStage;
-      const int j = p.tiles == 1 ? (int)sub : (int)sub / p.tiles;
-      b_slab = j * (HD / 64);
+      b_slab = kv_head_of(p, sub) * (HD / 64);
       if (!kCluster && (i == 0 || (b_sub & kFirst))) {
         // the rows of an item's query heads are consecutive
         const Heads h(p, sub);
@@ -1355,8 +1365,7 @@ cudaError_t launch_as(const AttendParams& p, int cluster, int device,
     using L = Smem<HD, NT, true>;
     e = allow_smem(kernel, L::kBytes, device, ready[0], true);
     if (e == cudaSuccess)
-      e = launch_kernel(kernel,
-                        (unsigned)(p.R * p.kv_heads * p.tiles * cluster),
+      e = launch_kernel(kernel, dim3(p.kv_heads * p.tiles * cluster, p.R),
                         L::W * 32, L::kBytes, st, true, cluster, p);
     if (e == cudaSuccess) count_launch();
     return e;
@@ -1393,7 +1402,7 @@ int cluster_of(int R, int64_t items, int64_t max_blocks, int head_dim,
   if (items > kCtas) return 0;
   int cluster = items <= 7 ? 16 : items <= 15 ? 8 : items <= 36 ? 4
                 : items <= 76 ? 2 : 1;
-  const int64_t feeds = (int64_t)warps_of(head_dim, nt, true) * kLeast;
+  const int64_t feeds = warps_of(head_dim, nt, true);
   while (cluster > 1 && max_blocks <= feeds * (cluster / 2)) cluster /= 2;
   const double bytes = 2.0 * (double)max_blocks * page_bytes(head_dim);
   const double others = R == 1 ? 1.0 : 0.5 + 0.5 / R;
@@ -1540,6 +1549,7 @@ int kvtc_paged_attend(int cuda_device, int R, int heads, int kv_heads,
   p.group = group;
   p.tiles = (group + 8 * nt - 1) / (8 * nt);
   p.tile_heads = (group + p.tiles - 1) / p.tiles;
+  p.tiles_inv = (65536u + p.tiles - 1) / p.tiles;
   const int cluster = cluster_of(R, (int64_t)R * kv_heads * p.tiles,
                                  max_blocks, head_dim, nt);
   cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
