@@ -1394,9 +1394,9 @@ cudaError_t launch_as(const AttendParams& p, int cluster, int device,
 // across blocks, about 3 us; what they lose is that items * cluster blocks,
 // at about 90 GB/s a block, may read slower than all SMs at 7000 GB/s, which
 // is taken at the longest length that the table allows, for the others half
-// of that.  Clusters and runs, 32 heads on 8 of 128: one request of 2K 9.6
-// and 11.6 us, 8K 12.2 and 14.5, 16K 19.1 and 20.3, 32K 29.9 and 29.1; two of
-// 8K 18.2 and 17.1; 16 of up to 1K 14.1 and 16.5.
+// of that.  Clusters and runs, 32 heads on 8 of 128: one request of 2K 8.0
+// and 10.0 us, 8K 11.7 and 13.7, 16K 18.6 and 19.5, 32K 29.5 and 28.5; two of
+// 4K 11.5 and 11.5, of 8K 18.0 and 16.6; 16 of up to 1K 13.7 and 15.9.
 int cluster_of(int R, int64_t items, int64_t max_blocks, int head_dim,
                int nt) {
   if (items > kCtas) return 0;
