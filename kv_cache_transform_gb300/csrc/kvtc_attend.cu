@@ -39,7 +39,7 @@
 // flops a row element (50 TFLOP/s at eight query heads a KV head, a small
 // part of what mma.sync gives).  While all warps have pages to ask for, the
 // SMs read 7.8 TB/s together (570 MB, 16 requests up to 16K: 91 us in all,
-// 6.3 TB/s); the rest is latency: 3.6 us until the first page (lengths, block
+// 6.3 TB/s); the rest is latency: 3 us until the first page (lengths, block
 // table, page, one after the other), and after the last ones 4 us, more or
 // less, of warps that end apart, 2 us of the block's join, 2 to 3 us of the
 // launch behind.
