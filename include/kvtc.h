@@ -362,7 +362,7 @@ int64_t kvtc_paged_assign_workspace_bytes(int R);
  * only while the call's work runs on cuda_stream, 16-byte aligned; slots, cu,
  * head and head_out are 8-byte aligned, the int32 arrays 4.  One kernel
  * launch for up to 1024 requests, unless slot_capacity is above 16 R (or
- * 8192) and held_out is held or head_out is head; else two.
+ * 8192) or below R / 2 and held_out is held or head_out is head; else two.
  * Errors: EINVAL, ESIZE, EALIGN, ENOTSUP, ECUDA.
  */
 int kvtc_paged_assign(int cuda_device, int R, const int32_t* held,

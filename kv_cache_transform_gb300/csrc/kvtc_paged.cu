@@ -6,10 +6,10 @@
 // integer sums, so the result is exact and does not depend on the launch.
 //   few slots (decode steps): assign_small_kernel, one block, a thread per
 //     request: a chain of three loads, 1.8 us;
-//   more: assign_fill_kernel on the whole GPU writes the table entries and
-//     the slots; every block forms the sums itself, or assign_scan_kernel
-//     does so before it, in one block (more than 1024 requests, or a state
-//     that is kept in place).
+//   more, or no slot map: assign_fill_kernel on the whole GPU writes the
+//     table entries and the slots; every block forms the sums itself, or
+//     assign_scan_kernel does so before it, in one block (more than 1024
+//     requests, or a state that is kept in place).
 // kvtc_paged_append: append_kernel, a warp per row.
 #include <cuda_runtime.h>
 
@@ -122,7 +122,9 @@ __device__ __forceinline__ int64_t slot_of(int64_t id, int64_t t) {
 // tokens its thread writes their slots, else the warps share them.
 // (64 requests of 16 new tokens 4.6 us, where the warps share all above four
 // tokens 13.2, by assign_fill_kernel 7.3; of 32, 13.4 and 5.8; 1024 of 8, 8.6
-// and 10.9, of 16, 14.7 and 10.9.)
+// and 10.9, of 16, 14.7 and 10.9.  Table entries alone, without a slot map: 64
+// requests of 2 blocks 10.3 and 3.8, of 2048 blocks 315 and 13.4; of one
+// block 3.2 and 3.8.)
 constexpr int kSmallReq = 1024;
 constexpr int64_t kSmallSlots = 8192;  // and kSmallOwn a request
 constexpr int kSmallOwn = 16;          // tokens that a thread writes itself
@@ -493,7 +495,9 @@ int kvtc_paged_assign(int cuda_device, int R, const int32_t* held,
   p.flags = flags;
   p.R = R;
   p.max_blocks = max_blocks;
-  if (R <= kSmallReq &&
+  // (capacity is what the host knows of the tokens; a map of less than half a
+  // slot a request says that the table alone is wanted, of any length)
+  if (R <= kSmallReq && 2 * slot_capacity >= R &&
       slot_capacity <= std::min(kSmallSlots, (int64_t)kSmallOwn * R)) {
     if (launch_kernel(assign_small_kernel, 1, std::max(32, (R + 31) / 32 * 32),
                       0, st, true, 0, p) != cudaSuccess)
@@ -501,7 +505,6 @@ int kvtc_paged_assign(int cuda_device, int R, const int32_t* held,
     count_launch();
     return KVTC_OK;
   }
-  // (capacity is what the host knows of the tokens)
   const int64_t runs = std::max<int64_t>(
       (slot_capacity + kFillRun - 1) / kFillRun, 152 * 8);
   const unsigned grid = (unsigned)std::min<int64_t>((runs + 7) / 8, 4 * 152);

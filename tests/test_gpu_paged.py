@@ -174,6 +174,24 @@ def test_assign_lengths_far_beyond_the_map(kv, R, cap):
     assert int(c.flags.cpu()[0]) == kv.KVTC_FLAG_SPACE
 
 
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("R,blocks,cap", [
+    (1, 40, 0), (7, 300, 0), (64, 33, 0), (1024, 60, 0), (1025, 9, 0),
+    (64, 50, 31), (1024, 12, 511), (9, 30, 4)])
+def test_assign_of_the_table_alone(kv, R, blocks, cap, in_place):
+    """Long prompts with no slot map, or next to none: the table's entries
+    are the work, and one block does not write them alone (a state that is
+    kept in place is summed in a launch before the one that does)."""
+    rng = np.random.default_rng(R + blocks)
+    lens = rng.integers(0, 16 * blocks + 1, R)
+    lens[R // 2] = 16 * blocks
+    held = np.where(rng.random(R) < 0.3, lens // 3, 0)
+    free, head, table = start_state(rng, held, blocks, R * blocks)
+    n = kv.kvtc_launch_count()
+    run_assign(kv, held, lens, free, head, table, cap, in_place=in_place)
+    assert kv.kvtc_launch_count() - n == (2 if in_place or R > 1024 else 1)
+
+
 @pytest.mark.parametrize("R,hi", [(1024, 3), (1025, 3), (4096, 60), (600, 1),
                                   (64, 32), (64, 33), (64, 128), (64, 129)])
 def test_assign_with_many_empty_requests(kv, R, hi):
