@@ -419,6 +419,8 @@ int64_t kvtc_paged_attend_workspace_bytes(int cuda_device, int R, int heads,
  *   lens         : DEVICE int32 [R] (negative counts as 0; above
  *                  16 * max_blocks it counts as that and flags
  *                  KVTC_FLAG_SPACE).
+ *   scale        : at most 2^127 in magnitude, not NaN.  A product q_h . k_t
+ *                  or s_t log2(e) beyond fp32's range counts as infinite.
  *   out          : DEVICE [R][out_ld], laid out as q; elements between the
  *                  rows are untouched.
  *   lse          : DEVICE fp32 [R][heads], or NULL: the log-sum-exp, with

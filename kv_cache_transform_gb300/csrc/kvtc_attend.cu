@@ -71,6 +71,7 @@ constexpr int kCtas = 152;           // one block per SM
 constexpr int kFewReq = 128;         // requests that each warp sums itself
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kMaxScale = 0x1p127f;  // times log2 e still finite
 constexpr float kSlack = 6.f;        // log2; see the reference in the loop
 
 // Floats of a partial result of nt x 8 query heads: o in fragment order
@@ -1500,7 +1501,8 @@ int kvtc_paged_attend(int cuda_device, int R, int heads, int kv_heads,
   if (ret != KVTC_OK) return ret;
   if ((dtype != KVTC_DTYPE_BF16 && dtype != KVTC_DTYPE_FP16) || !k_cache ||
       !v_cache || num_blocks <= 0 || num_blocks > INT32_MAX ||
-      max_blocks <= 0 || sink < 0 || window < 0 || !std::isfinite(scale) ||
+      max_blocks <= 0 || sink < 0 || window < 0 ||
+      !(std::fabs(scale) <= kMaxScale) ||      // (nor NaN)
       !workspace || (R && (!q || !block_table || !lens || !out)))
     return KVTC_EINVAL;
   if (block_size != kBlock || max_blocks > kMaxTable) return KVTC_ENOTSUP;

@@ -194,7 +194,19 @@ def test_lengths_outside_the_table(kv):
     a.check(flags=kv.KVTC_FLAG_SPACE)
 
 
-MANY = dict(heads=28, kv_heads=4, hd=128)
+@pytest.mark.parametrize("form", [RUNS, CLUSTERS])
+@pytest.mark.parametrize("scale", [2.0 ** 127, -2.0 ** 127])
+def test_the_largest_scale(kv, scale, form):
+    """Scores of zero stay zero beside a scale near fp32's largest, and
+    products of 2^-122 with it are of order 32."""
+    q, k, v, table, lens = case(50, [90] * (60 if form == RUNS else 2), 8, 4,
+                                64)
+    k[:, :, 64:] *= 2.0 ** -60
+    q[:, 2:] *= 2.0 ** -62               # KV heads 1 to 3
+    q[:, :2] = 0.0                       # KV head 0: every score is zero
+    a = Formed(kv, (q, k, v, table, lens), form, scale=scale)
+    a.call()
+    a.check()
 
 
 def many(seed, R=64, longest=2000, columns=0, heads=28, kv_heads=4, hd=128):

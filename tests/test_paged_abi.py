@@ -114,6 +114,17 @@ def test_attend_sizes_and_alignment(kv, over, code):
     assert attend(kv, **over) == getattr(kv, "KVTC_" + code)
 
 
+@pytest.mark.parametrize("scale,fine", [
+    (3.4e38, False), (-3.4e38, False), (1.8e38, False),
+    (float("-inf"), False), (2.0 ** 127, True), (-2.0 ** 127, True),
+    (0.0, True), (1e-45, True)])
+def test_attend_scale(kv, scale, fine):
+    """scale log2(e) has to be finite in fp32: an infinite one makes NaN of
+    a score that is zero."""
+    assert attend(kv, R=0, scale=scale) == (kv.KVTC_OK if fine
+                                            else kv.KVTC_EINVAL)
+
+
 def test_workspace_queries(kv):
     L = kv.lib()
     assert L.kvtc_paged_assign_workspace_bytes(-1) == kv.KVTC_EINVAL
