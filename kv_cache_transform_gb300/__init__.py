@@ -179,6 +179,15 @@ def _stream_on(stream, device: int) -> int:
     return _raw_stream(device)
 
 
+def _device_of(device, x) -> int:
+    """The given device ordinal, or that of tensor x; 0 for an address (a
+    call without a calibration has nothing else to take it from)."""
+    if device is not None:
+        return device
+    get = getattr(x, "get_device", None)
+    return max(get(), 0) if get else 0
+
+
 class Calib:
     """Handle of a loaded calibration (owns device operands)."""
 
@@ -367,10 +376,12 @@ def kvtc_paged_assign_workspace_bytes(R: int) -> int:
 def kvtc_paged_assign(R: int, held, lens, free_blocks, n_free: int, head,
                       block_table, max_blocks: int, block_size: int, slots,
                       slot_capacity: int, cu, held_out, head_out, workspace,
-                      workspace_bytes: int, flags=None, device: int = 0,
-                      stream=None) -> None:
+                      workspace_bytes: int, flags=None,
+                      device: Optional[int] = None, stream=None) -> None:
     """Blocks for R requests that grow from held to lens tokens, and the
-    slots of their new tokens; flags: device uint32 word or None."""
+    slots of their new tokens; flags: device uint32 word or None.  All
+    tensors are on `device`, by default block_table's (0 for addresses)."""
+    device = _device_of(device, block_table)
     _check(lib().kvtc_paged_assign(
         device, R, _ptr(held), _ptr(lens),
         _ptr(free_blocks), n_free, _ptr(head),
@@ -383,10 +394,13 @@ def kvtc_paged_assign(R: int, held, lens, free_blocks, n_free: int, head,
 
 def kvtc_paged_append(src: Sequence, ld: int, N: int, slots, D: int,
                       block_size: int, cache: Sequence, num_blocks: int,
-                      flags=None, device: int = 0, stream=None) -> None:
-    """Rows src[j] [N][ld] into the pools cache[j] at row slots[i] each."""
+                      flags=None, device: Optional[int] = None,
+                      stream=None) -> None:
+    """Rows src[j] [N][ld] into the pools cache[j] at row slots[i] each.  All
+    tensors are on `device`, by default the first pool's (0 for addresses)."""
     if len(src) != len(cache):
         raise ValueError("src and cache differ in length")
+    device = _device_of(device, cache[0] if len(cache) else None)
     _check(lib().kvtc_paged_append(
         device, len(src), _ptr_array(src), ld, N, _ptr(slots), D,
         block_size, _ptr_array(cache), num_blocks, _ptr(flags),
@@ -405,10 +419,12 @@ def kvtc_paged_attend(R: int, heads: int, kv_heads: int, head_dim: int,
                       num_blocks: int, block_size: int, block_table,
                       max_blocks: int, lens, sink: int, window: int,
                       scale: float, out, out_ld: int, lse, workspace,
-                      workspace_bytes: int, flags=None, device: int = 0,
-                      stream=None) -> None:
+                      workspace_bytes: int, flags=None,
+                      device: Optional[int] = None, stream=None) -> None:
     """One new token's attention per request over its tokens in the pools;
-    lse: device fp32 [R][heads] or None."""
+    lse: device fp32 [R][heads] or None.  All tensors are on `device`, by
+    default k_cache's (0 for addresses)."""
+    device = _device_of(device, k_cache)
     _check(lib().kvtc_paged_attend(
         device, R, heads, kv_heads, head_dim, dtype, _ptr(q), q_ld,
         _ptr(k_cache), _ptr(v_cache), num_blocks, block_size,

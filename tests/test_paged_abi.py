@@ -154,3 +154,42 @@ def test_binding_raises(kv):
         kv.kvtc_paged_attend(1, 2, 3, 64, 0, A, 128, A, A, 1, 16, A, 1, A, 0,
                              0, 1.0, A, 128, None, A, 1 << 30, stream=0)
     assert e.value.code == kv.KVTC_EINVAL
+
+
+class OnDevice:
+    """Stands in for a tensor."""
+
+    def __init__(self, device):
+        self.device = device
+
+    def data_ptr(self):
+        return A
+
+    def get_device(self):
+        return self.device
+
+
+@pytest.mark.parametrize("where,given,used", [
+    (1, None, 1), (0, None, 0), (3, 2, 2), (None, None, 0), (None, 5, 5),
+    (-1, None, 0)])
+def test_calls_run_on_their_tensors_device(kv, monkeypatch, where, given,
+                                           used):
+    """By default, on the device of the table or the pools, whatever device
+    is current; a launch on device 0 could not read them."""
+    seen = []
+
+    class Lib:
+        def __getattr__(self, name):
+            return lambda *args: seen.append((name, args[0])) or 0
+    monkeypatch.setattr(kv, "_lib_handle", Lib())
+    x = A if where is None else OnDevice(where)
+    more = dict(stream=0, **({} if given is None else {"device": given}))
+    kv.kvtc_paged_assign(1, x, x, x, 1, x, x, 1, 16, x, 1, x, x, x, x, 256,
+                         **more)
+    kv.kvtc_paged_append([x], 8, 1, x, 8, 16, [x], 1, **more)
+    kv.kvtc_paged_attend(1, 1, 1, 64, 0, x, 64, x, x, 1, 16, x, 1, x, 0, 0,
+                         1.0, x, 64, None, x, 1 << 20, **more)
+    kv.kvtc_paged_append([], 8, 0, None, 8, 16, [], 1, **more)
+    assert seen == [("kvtc_paged_assign", used), ("kvtc_paged_append", used),
+                    ("kvtc_paged_attend", used),
+                    ("kvtc_paged_append", given or 0)]
