@@ -388,8 +388,9 @@ int kvtc_paged_assign(int cuda_device, int R, const int32_t* held,
  *              rows with one slot, either may supply each 16 bytes of it.
  *   cache    : HOST array [nstreams] of device pointers, each 16-bit
  *              [num_blocks][16][D]; rows that no slot names are untouched.
- * D % 8 == 0, 8 <= D <= 8192.  src and cache 16-byte aligned, slots 8.  One
- * kernel launch per 64 streams.
+ * D % 8 == 0, 8 <= D <= 8192.  src and cache 16-byte aligned, slots 8.  No
+ * cache may overlap another, a src or slots.  One kernel launch per 64
+ * streams.
  * Errors: EINVAL, ESIZE, EALIGN, ENOTSUP, ECUDA.
  */
 int kvtc_paged_append(int cuda_device, int nstreams, const void* const* src,
@@ -432,10 +433,16 @@ int64_t kvtc_paged_attend_workspace_bytes(int cuda_device, int R, int heads,
  * (no attended token, or every s_t = -inf) gets out = 0, lse = -inf; a NaN
  * or s_t = +inf in the attended tokens gives NaN, an infinity in V an
  * infinity (or NaN, where its weight is below 2^-20).  Products are summed,
- * and the softmax statistics held, in fp32; out is rounded once.  The result
- * does not depend on timing, so equal calls on one device give equal bits.
+ * and the softmax statistics held, in fp32.  A weight enters its product with
+ * v as two 16-bit terms, to 2^-15 of itself; exponentials and the reciprocal
+ * of their sum are the hardware's approximate ones (2^-22); out is rounded
+ * once.  Against fp32 weights that moves one value of out in a thousand in
+ * bf16, three in fp16, to its neighbour; the error against 64 bits stays.  The
+ * result does not depend on timing, so equal calls on one device give equal
+ * bits.
  *   head_dim 64, 128 or 256; kv_heads * head_dim <= 8192; at most 128 query
- * heads a KV head; num_blocks < 2^31, max_blocks < 2^27 - 1.  out must not overlap an input.
+ * heads a KV head; num_blocks < 2^31, max_blocks < 2^27 - 1.  out, lse and
+ * workspace must not overlap an input or one another.
  * workspace: device scratch of kvtc_paged_attend_workspace_bytes bytes, used
  * only while the call's work runs on cuda_stream: calls that may run at the
  * same time need one each.  q, pools, out and workspace 16-byte aligned,

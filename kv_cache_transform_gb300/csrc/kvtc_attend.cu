@@ -85,7 +85,10 @@ __host__ __device__ constexpr int slot_floats(int hd, int nt) {
 // of head_dim 64).  More warps with one page mostly beat fewer with two: 64
 // requests up to 4K at head_dim 128, 12 x 1 against 9 x 2: 48.5 and 49.7 us;
 // 64 of 2K to 4K at head_dim 64 (8 KV heads), 16 x 1 against 12 x 2: 73.0 and
-// 74.4 (32 of 4K to 8K, 4 KV heads: 40.0 and 38.3).
+// 74.4 (32 of 4K to 8K, 4 KV heads: 40.0 and 38.3).  At head_dim 256 two head
+// tiles' accumulators and queries alone are 192 registers: that form spills
+// (255 registers, 172 bytes stored and 156 loaded a thread; in a cluster 24
+// and 12).
 __host__ __device__ constexpr int warps_of(int hd, int nt, bool cluster) {
   return hd == 64    ? (nt == 1 ? 16 : nt == 2 ? 12 : 8)
          : hd == 128 ? (nt == 1 ? (cluster ? 14 : 12) : 8)
@@ -1303,11 +1306,14 @@ struct FarJoin {
 
 // Items that lie over several blocks: block c joins the one that began in
 // block c of the attention, its own part and those of the blocks after it, a
-// warp per channel tile.  With many items there are two or three parts mostly,
-// and blocks of that size find room beside the attention's and wait for its
-// end in place.  Where an item lies over kFewParts blocks or more on average,
-// join_groups groups of warps take every so-many-th part and are joined
-// through shared memory.  One group and join_groups: 64 requests up to 4K
+// warp per channel tile.  With many items there are two or three parts mostly.
+// Where an item lies over kFewParts blocks or more on average, join_groups
+// groups of warps take every so-many-th part and are joined through shared
+// memory.  The launch waits for no host, but its blocks start only as the
+// attention's leave their SMs: those hold 64,512 of an SM's 65,536 registers
+// at head_dim 128 with one head tile, where a block here takes 22,528 (9,984
+// are free at head_dim 256, and 45,056 taken), so that the start and the first
+// loads lie behind the attention's end.  One group and join_groups: 64 requests up to 4K
 // (256 items) 48.5 and 49.8 us; two of 32K (16 items) 39.6 and 39.0, one
 // (8 items) 30.5 and 29.2.
 constexpr int kFewParts = 8;
@@ -1398,6 +1404,9 @@ cudaError_t launch_as(const AttendParams& p, int cluster, int device,
 // of that.  Clusters and runs, 32 heads on 8 of 128: one request of 2K 8.0
 // and 10.0 us, 8K 11.7 and 13.7, 16K 18.6 and 19.5, 32K 29.5 and 28.5; two of
 // 4K 11.5 and 11.5, of 8K 18.0 and 16.6; 16 of up to 1K 13.7 and 15.9.
+// The lengths themselves are on the device: under a table of 2048 columns one
+// request of 256 tokens takes the runs' 9.9 us, not 6.8, of 1K 9.9 and not
+// 8.1, of 8K 13.5 and not 11.7.
 int cluster_of(int R, int64_t items, int64_t max_blocks, int head_dim,
                int nt) {
   if (items > kCtas) return 0;

@@ -281,7 +281,7 @@ __device__ __forceinline__ int request_at(const int64_t* cu, int lo, int hi,
 // the blocks 9.2, with half of them 8.4).
 //
 // kOwnSums: every block forms the sums itself, in shared memory, instead of a
-// launch before that does (7.4 and 10.5 us); not for a state kept in place,
+// launch before that does (7.4 and 10.9 us); not for a state kept in place,
 // which one block would change while another still reads it.
 constexpr int kFillRun = 256;
 constexpr int kFillThreads = 256;
