@@ -1313,9 +1313,9 @@ struct FarJoin {
 // attention's leave their SMs: those hold 64,512 of an SM's 65,536 registers
 // at head_dim 128 with one head tile, where a block here takes 22,528 (9,984
 // are free at head_dim 256, and 45,056 taken), so that the start and the first
-// loads lie behind the attention's end.  One group and join_groups: 64 requests up to 4K
-// (256 items) 48.5 and 49.8 us; two of 32K (16 items) 39.6 and 39.0, one
-// (8 items) 30.5 and 29.2.
+// loads lie behind the attention's end.  One group and join_groups: 64
+// requests up to 4K (256 items) 48.5 and 49.8 us; two of 32K (16 items) 39.6
+// and 39.0, one (8 items) 30.5 and 29.2.
 constexpr int kFewParts = 8;
 __host__ __device__ constexpr int join_groups(int tiles) {
   return tiles > 16 ? 1 : tiles > 8 ? 2 : 4;

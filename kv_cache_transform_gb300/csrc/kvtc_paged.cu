@@ -497,7 +497,7 @@ int kvtc_paged_assign(int cuda_device, int R, const int32_t* held,
   p.max_blocks = max_blocks;
   // (capacity is what the host knows of the tokens; a map of less than half a
   // slot a request says that the table alone is wanted, of any length)
-  if (R <= kSmallReq && 2 * slot_capacity >= R &&
+  if (R <= kSmallReq && slot_capacity >= (R + 1) / 2 &&
       slot_capacity <= std::min(kSmallSlots, (int64_t)kSmallOwn * R)) {
     if (launch_kernel(assign_small_kernel, 1, std::max(32, (R + 31) / 32 * 32),
                       0, st, true, 0, p) != cudaSuccess)
