@@ -460,6 +460,208 @@ int kvtc_paged_attend(int cuda_device, int R, int heads, int kv_heads,
                       void* cuda_stream);
 
 /*
+ * Chunks of new tokens -- the calls around kvtc_paged_attend where a request
+ * brings more than one new token at a time (a prompt, a piece of one, drafted
+ * tokens), and the calls that shrink a cache to what attention weighs.  What
+ * is said above of the paged serving calls (device, streams, graphs, flags,
+ * blocks of 16 tokens, R <= 4096) holds for these too.  The rows of all
+ * requests lie behind one another: those of request r are rows cu[r] ..
+ * cu[r + 1] - 1 of N (cu as kvtc_paged_assign writes it: DEVICE int64
+ * [R + 1], non-decreasing; values outside [0, N] count as the nearer end,
+ * and above N flag KVTC_FLAG_SPACE), and belong to the last tokens of lens[r]:
+ * row cu[r] + i of n is token lens[r] - n + i.  Rows of no request (a padded
+ * batch) are not read, and what belongs to them is left as it is.
+ */
+
+/* How kvtc_rotary_frequencies stretches positions for long contexts. */
+enum kvtc_rotary_scaling {
+  KVTC_ROTARY_PLAIN = 0,   /* f_i = base^(-2 i / rotary_dim) */
+  KVTC_ROTARY_LINEAR = 1,  /* f_i / factor: positions divided by factor */
+  KVTC_ROTARY_BASE = 2,    /* base * factor^(rotary_dim / (rotary_dim - 2)):
+                              the longest wavelength times factor, the
+                              shortest as it is */
+  KVTC_ROTARY_BANDS = 3    /* f_i (a + (1 - a) / factor), a from 0 to 1 as
+                              the turns of f_i in `context` tokens go from
+                              `low` to `high` */
+};
+
+/*
+ * kvtc_rotary_frequencies -- angles per position for kvtc_paged_rotate, into
+ * a HOST array of rotary_dim / 2 doubles (no device is touched).
+ *   base    : > 0, finite.
+ *   factor  : > 0, finite (not read for KVTC_ROTARY_PLAIN).
+ *   context, low, high : for KVTC_ROTARY_BANDS alone: context > 0,
+ *             0 <= low < high, all finite.
+ * rotary_dim is even and positive (above 2 for KVTC_ROTARY_BASE).
+ * Errors: EINVAL.
+ */
+int kvtc_rotary_frequencies(int rotary_dim, double base, int scaling,
+                            double factor, double context, double low,
+                            double high, double* inv_freq);
+
+/*
+ * kvtc_paged_rotate -- norms and rotary positions of N new tokens' queries
+ * and keys, the queries into q_out, keys and values into the pools.  Each
+ * head x of q (and of k):
+ *     y = x / sqrt(mean(x^2) + eps) * norm            (y = x where norm is
+ *                                                      NULL),
+ *     (y_a, y_b) -> rotary_scale (y_a cos t - y_b sin t, y_b cos t + y_a sin t)
+ * for the pairs i = 0 .. rotary_dim / 2 - 1, t = positions * inv_freq[i]; the
+ * elements behind rotary_dim stay y.  Values v are copied bit for bit.
+ *   q, k, v      : DEVICE rows of `dtype` elements, token n at n * ld: column
+ *                  slices of one projection's rows, heads side by side.
+ *                  v may be NULL with v_cache (keys alone).
+ *   positions    : DEVICE int32 [N], any value.  May be NULL when rotary_dim
+ *                  is 0.
+ *   inv_freq     : DEVICE fp64 [rotary_dim / 2], finite, as
+ *                  kvtc_rotary_frequencies gives them.  May be NULL when
+ *                  rotary_dim is 0.
+ *   rotary_dim   : % 8 == 0, 0 .. head_dim.
+ *   interleaved  : 0: pair i is elements i and i + rotary_dim / 2; else
+ *                  2 i and 2 i + 1.
+ *   q_norm, k_norm : DEVICE [head_dim] of `dtype` each, or NULL.
+ *   eps          : >= 0, finite.
+ *   q_out        : DEVICE [N][q_out_ld] of `dtype`, every row written; may be
+ *                  q itself with q_out_ld == ld.
+ *   slots        : DEVICE int64 [N] and
+ *   k_cache, v_cache : [num_blocks][16][kv_heads * head_dim], as for
+ *                  kvtc_paged_append (slots outside skip the token's k and v;
+ *                  above the pool they flag KVTC_FLAG_BLOCK).
+ * All arithmetic is in fp32, rounded once; the angle is taken modulo a turn
+ * in 64-bit fixed point, so it is as exact at far positions as at near ones
+ * (to p 2^-53 of a turn of f_i at position p, through inv_freq / 2 pi, and
+ * 2^-25 of a turn).
+ *   head_dim 64, 128 or 256; kv_heads * head_dim <= 8192, heads * head_dim <=
+ * 131072.  All pointers to rows, norms and pools 16-byte aligned, ld and
+ * q_out_ld % 8 == 0, slots and inv_freq 8, positions 4.  Other than as said no
+ * output may overlap an input or another output.  One kernel launch.
+ * Errors: EINVAL, ESIZE, EALIGN, ENOTSUP, ECUDA.
+ */
+int kvtc_paged_rotate(int cuda_device, int64_t N, int heads, int kv_heads,
+                      int head_dim, int dtype, const void* q, const void* k,
+                      const void* v, int64_t ld, const int32_t* positions,
+                      const double* inv_freq, int rotary_dim, int interleaved,
+                      float rotary_scale, const void* q_norm,
+                      const void* k_norm, float eps, void* q_out,
+                      int64_t q_out_ld, const int64_t* slots, int block_size,
+                      void* k_cache, void* v_cache, int64_t num_blocks,
+                      uint32_t* flags, void* cuda_stream);
+
+/* Device workspace bytes kvtc_paged_attend_chunks needs (< 0 on error). */
+int64_t kvtc_paged_attend_chunks_workspace_bytes(int cuda_device, int R,
+                                                 int64_t N, int heads,
+                                                 int kv_heads, int head_dim);
+
+/*
+ * kvtc_paged_attend_chunks -- attention of chunks of new tokens over their
+ * requests' tokens in the pools, the chunk's own among them (appended before
+ * the call).  The row of token p attends to tokens 0 .. p; with window > 0, of
+ * those only to the first `sink` and the last `window` (p is the last one):
+ * what kvtc_paged_attend computes for lens = p + 1.  Formulas, layouts and the
+ * meaning of q, k_cache, v_cache, block_table, lens, scale, out and lse are
+ * kvtc_paged_attend's, with N rows (q [N][q_ld], out [N][out_ld], lse
+ * [N][heads]) in the place of R.
+ * A row whose token is before the first (more rows than lens[r]) and a head
+ * whose weights sum to zero get out = 0, lse = -inf; tokens in blocks whose
+ * id is out of range are left out and flag KVTC_FLAG_BLOCK.  Infinities and
+ * NaN in K, V or q reach the rows that attend to them and no others.
+ * Products are summed, and the softmax statistics held, in fp32.
+ *   head_dim 64, 128 or 256; kv_heads * head_dim <= 8192; at most 128 query
+ * heads a KV head.  Alignment and overlap as for kvtc_paged_attend, cu 8.
+ * workspace: device scratch of kvtc_paged_attend_chunks_workspace_bytes
+ * bytes, used only while the call's work runs on cuda_stream.
+ * Errors: EINVAL, ESIZE, EALIGN, ENOTSUP, ECUDA.
+ */
+int kvtc_paged_attend_chunks(
+    int cuda_device, int R, int64_t N, int heads, int kv_heads, int head_dim,
+    int dtype, const void* q, int64_t q_ld, const void* k_cache,
+    const void* v_cache, int64_t num_blocks, int block_size,
+    const int32_t* block_table, int max_blocks, const int64_t* cu,
+    const int32_t* lens, int sink, int window, float scale, void* out,
+    int64_t out_ld, float* lse, void* workspace, int64_t workspace_bytes,
+    uint32_t* flags, void* cuda_stream);
+
+/* Device workspace bytes kvtc_paged_weigh needs (< 0 on error). */
+int64_t kvtc_paged_weigh_workspace_bytes(int cuda_device, int R, int64_t N,
+                                         int heads, int kv_heads,
+                                         int head_dim);
+
+/*
+ * kvtc_paged_weigh -- the attention weight that each cached token receives:
+ *     acc_out[r][t] = decay acc[r][t] + sum e^(scale q_ih . k_t - lse_ih)
+ * over request r's rows i that attend to t (as kvtc_paged_attend_chunks has
+ * it) and all query heads h, for t < lens[r]; other elements of acc_out are
+ * left as they are.
+ *   lse          : DEVICE fp32 [N][heads], what the attention of the same
+ *                  rows returned.  A head whose lse is -inf adds nothing.
+ *   decay        : finite; where it is 0, acc is not read and may be NULL.
+ *   acc, acc_out : DEVICE fp32 [R][acc_ld], acc_ld >= 16 * max_blocks,
+ *                  % 4 == 0; acc_out may be acc itself.
+ * The others are kvtc_paged_attend_chunks' (a few of its rows may be given,
+ * with a cu of their own, if they are the requests' last).  Tokens in blocks
+ * whose id is out of range receive nothing and, where attended, flag
+ * KVTC_FLAG_BLOCK.  Sums are in fp32, in a fixed order: equal calls on one
+ * device give equal bits.  acc, acc_out, q, k_cache and workspace 16-byte
+ * aligned, cu 8, the others 4.
+ * Errors: EINVAL, ESIZE, EALIGN, ENOTSUP, ECUDA.
+ */
+int kvtc_paged_weigh(int cuda_device, int R, int64_t N, int heads,
+                     int kv_heads, int head_dim, int dtype, const void* q,
+                     int64_t q_ld, const void* k_cache, int64_t num_blocks,
+                     int block_size, const int32_t* block_table,
+                     int max_blocks, const int64_t* cu, const int32_t* lens,
+                     int sink, int window, float scale, const float* lse,
+                     float decay, const float* acc, float* acc_out,
+                     int64_t acc_ld, void* workspace, int64_t workspace_bytes,
+                     uint32_t* flags, void* cuda_stream);
+
+/* Device workspace bytes kvtc_paged_evict needs (< 0 on error). */
+int64_t kvtc_paged_evict_workspace_bytes(int R, int max_blocks);
+
+/*
+ * kvtc_paged_evict -- cut requests down to `keep` cached tokens.  Of a
+ * request with more than `keep`, the first `sink`, the last `window` and, of
+ * the others, the keep - sink - window with the greatest acc stay (of equal
+ * ones those with the lowest index; -0 equals 0, a NaN is below -inf).  What
+ * stays keeps its order and becomes tokens 0 .. lens_out[r] - 1.
+ *   acc          : DEVICE fp32 [R][acc_ld] (as kvtc_paged_weigh's): a weight
+ *                  per token.
+ *   lens         : DEVICE int32 [R] (negative counts as 0; above 16 *
+ *                  max_blocks as that, and flags KVTC_FLAG_SPACE).
+ *   keep, sink, window : sink + window <= keep.
+ *   block_table  : DEVICE int32 [R][max_blocks]: the blocks that tokens are
+ *                  in.
+ *   out_table    : the blocks that they go to, laid out the same.  Either
+ *                  block_table itself (the call works in place, and the
+ *                  request's blocks must be its own), or a table none of
+ *                  whose blocks that are written to is read from in this
+ *                  call.  Its columns ceil(lens_out[r] / 16) and up are not
+ *                  read; giving blocks back is the caller's.
+ *   cache        : HOST array [nstreams] of pools [num_blocks][16][D] of
+ *                  16-bit elements (any number of layers' K and V that share
+ *                  the tables); D % 8 == 0, at most 8192.
+ *   kept         : DEVICE int32 [R][keep], written whole: where token j was,
+ *                  -1 from lens_out[r] on.  May be NULL when keep is 0.
+ *   acc_out      : DEVICE fp32 [R][acc_ld]: the weights of what stays, then
+ *                  zeros up to lens[r]; may be acc itself.
+ *   lens_out     : DEVICE int32 [R], written: min(lens[r], keep); may be lens
+ *                  itself.
+ * A token whose old or new block id is out of range stays in the list, its
+ * rows are not written, and KVTC_FLAG_BLOCK is set.  cache, acc, acc_out and
+ * workspace 16-byte aligned, acc_ld % 4 == 0, the others 4.  Other than as
+ * said no output may overlap an input or another output.
+ * Errors: EINVAL, ESIZE, EALIGN, ENOTSUP, ECUDA.
+ */
+int kvtc_paged_evict(int cuda_device, int R, const float* acc, int64_t acc_ld,
+                     const int32_t* lens, int keep, int sink, int window,
+                     const int32_t* block_table, const int32_t* out_table,
+                     int max_blocks, int block_size, int nstreams,
+                     void* const* cache, int D, int64_t num_blocks,
+                     int32_t* kept, float* acc_out, int32_t* lens_out,
+                     void* workspace, int64_t workspace_bytes,
+                     uint32_t* flags, void* cuda_stream);
+
+/*
  * kvtc_calibrate -- the one-time calibration of technical summary 2A, on
  * the GPU, writing a version-1 blob (format above).  Per stream: mu = mean of
  * the calibration rows; V = eigenvectors of their covariance, sorted by

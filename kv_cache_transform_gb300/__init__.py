@@ -10,7 +10,11 @@ mirror the C ABI in ``include/kvtc.h``:
     kvtc_fields_unpack, kvtc_decompress_packed, kvtc_device_status,
     kvtc_paged_assign_workspace_bytes, kvtc_paged_assign,
     kvtc_paged_append, kvtc_paged_attend_workspace_bytes,
-    kvtc_paged_attend, kvtc_launch_count, kvtc_strerror
+    kvtc_paged_attend, kvtc_rotary_frequencies, kvtc_paged_rotate,
+    kvtc_paged_attend_chunks_workspace_bytes, kvtc_paged_attend_chunks,
+    kvtc_paged_weigh_workspace_bytes, kvtc_paged_weigh,
+    kvtc_paged_evict_workspace_bytes, kvtc_paged_evict,
+    kvtc_launch_count, kvtc_strerror
 
 Tensor arguments are torch CUDA tensors (or raw integer device addresses);
 ``stream`` defaults to torch's current stream.  There is no CPU fallback: if
@@ -45,6 +49,11 @@ KVTC_FLAG_SPACE = 16
 KVTC_DTYPE_BF16 = 0
 KVTC_DTYPE_FP16 = 1
 
+KVTC_ROTARY_PLAIN = 0
+KVTC_ROTARY_LINEAR = 1
+KVTC_ROTARY_BASE = 2
+KVTC_ROTARY_BANDS = 3
+
 _lib_handle = None
 
 
@@ -66,6 +75,7 @@ def lib() -> ctypes.CDLL:
     L = ctypes.CDLL(LIB_PATH)
     c_vp, c_i, c_i64, c_sz = (ctypes.c_void_p, ctypes.c_int, ctypes.c_int64,
                               ctypes.c_size_t)
+    c_d, c_f = ctypes.c_double, ctypes.c_float
     c_pp = ctypes.POINTER(ctypes.c_void_p)
     c_ip = ctypes.POINTER(ctypes.c_int)
     sig = {
@@ -113,6 +123,29 @@ def lib() -> ctypes.CDLL:
                                     c_i64, c_vp, c_vp, c_i64, c_i, c_vp, c_i,
                                     c_vp, c_i, c_i, ctypes.c_float, c_vp,
                                     c_i64, c_vp, c_vp, c_i64, c_vp, c_vp]),
+        "kvtc_rotary_frequencies": (c_i, [c_i, c_d, c_i, c_d, c_d, c_d, c_d,
+                                          ctypes.POINTER(c_d)]),
+        "kvtc_paged_rotate": (c_i, [c_i, c_i64, c_i, c_i, c_i, c_i, c_vp,
+                                    c_vp, c_vp, c_i64, c_vp, c_vp, c_i, c_i,
+                                    c_f, c_vp, c_vp, c_f, c_vp, c_i64, c_vp,
+                                    c_i, c_vp, c_vp, c_i64, c_vp, c_vp]),
+        "kvtc_paged_attend_chunks_workspace_bytes": (
+            c_i64, [c_i, c_i, c_i64, c_i, c_i, c_i]),
+        "kvtc_paged_attend_chunks": (c_i, [
+            c_i, c_i, c_i64, c_i, c_i, c_i, c_i, c_vp, c_i64, c_vp, c_vp,
+            c_i64, c_i, c_vp, c_i, c_vp, c_vp, c_i, c_i, c_f, c_vp, c_i64,
+            c_vp, c_vp, c_i64, c_vp, c_vp]),
+        "kvtc_paged_weigh_workspace_bytes": (
+            c_i64, [c_i, c_i, c_i64, c_i, c_i, c_i]),
+        "kvtc_paged_weigh": (c_i, [
+            c_i, c_i, c_i64, c_i, c_i, c_i, c_i, c_vp, c_i64, c_vp, c_i64,
+            c_i, c_vp, c_i, c_vp, c_vp, c_i, c_i, c_f, c_vp, c_f, c_vp, c_vp,
+            c_i64, c_vp, c_i64, c_vp, c_vp]),
+        "kvtc_paged_evict_workspace_bytes": (c_i64, [c_i, c_i]),
+        "kvtc_paged_evict": (c_i, [
+            c_i, c_i, c_vp, c_i64, c_vp, c_i, c_i, c_i, c_vp, c_vp, c_i, c_i,
+            c_i, c_pp, c_i, c_i64, c_vp, c_vp, c_vp, c_vp, c_i64, c_vp,
+            c_vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -432,6 +465,124 @@ def kvtc_paged_attend(R: int, heads: int, kv_heads: int, head_dim: int,
         window, scale, _ptr(out), out_ld, _ptr(lse),
         _ptr(workspace), workspace_bytes, _ptr(flags),
         _stream_on(stream, device)), "kvtc_paged_attend")
+
+
+def kvtc_rotary_frequencies(rotary_dim: int, base: float,
+                            scaling: int = KVTC_ROTARY_PLAIN,
+                            factor: float = 1.0, context: float = 0.0,
+                            low: float = 0.0, high: float = 0.0) -> list:
+    """Angles per position of the rotary_dim / 2 pairs, as a list of floats:
+    torch.tensor(..., dtype=torch.float64) of it is what kvtc_paged_rotate
+    reads."""
+    out = (ctypes.c_double * max(1, rotary_dim // 2))()
+    _check(lib().kvtc_rotary_frequencies(rotary_dim, base, scaling, factor,
+                                         context, low, high, out),
+           "kvtc_rotary_frequencies")
+    return list(out)
+
+
+def kvtc_paged_rotate(N: int, heads: int, kv_heads: int, head_dim: int,
+                      dtype: int, q, k, v, ld: int, positions, inv_freq,
+                      rotary_dim: int, interleaved: bool,
+                      rotary_scale: float, q_norm, k_norm, eps: float, q_out,
+                      q_out_ld: int, slots, block_size: int, k_cache,
+                      v_cache, num_blocks: int, flags=None,
+                      device: Optional[int] = None, stream=None) -> None:
+    """Norms (q_norm, k_norm: [head_dim] or None) and rotation of N tokens'
+    queries, into q_out, and keys, into k_cache at row slots[i] each; values
+    into v_cache.  All tensors are on `device`, by default k_cache's (0 for
+    addresses)."""
+    device = _device_of(device, k_cache)
+    _check(lib().kvtc_paged_rotate(
+        device, N, heads, kv_heads, head_dim, dtype, _ptr(q), _ptr(k),
+        _ptr(v), ld, _ptr(positions), _ptr(inv_freq), rotary_dim,
+        int(interleaved), rotary_scale, _ptr(q_norm), _ptr(k_norm), eps,
+        _ptr(q_out), q_out_ld, _ptr(slots), block_size, _ptr(k_cache),
+        _ptr(v_cache), num_blocks, _ptr(flags),
+        _stream_on(stream, device)), "kvtc_paged_rotate")
+
+
+def kvtc_paged_attend_chunks_workspace_bytes(R: int, N: int, heads: int,
+                                             kv_heads: int, head_dim: int,
+                                             device: int = 0) -> int:
+    return _check(lib().kvtc_paged_attend_chunks_workspace_bytes(
+        device, R, N, heads, kv_heads, head_dim),
+        "kvtc_paged_attend_chunks_workspace_bytes")
+
+
+def kvtc_paged_attend_chunks(R: int, N: int, heads: int, kv_heads: int,
+                             head_dim: int, dtype: int, q, q_ld: int,
+                             k_cache, v_cache, num_blocks: int,
+                             block_size: int, block_table, max_blocks: int,
+                             cu, lens, sink: int, window: int, scale: float,
+                             out, out_ld: int, lse, workspace,
+                             workspace_bytes: int, flags=None,
+                             device: Optional[int] = None,
+                             stream=None) -> None:
+    """Attention of rows cu[r] .. cu[r + 1] - 1 of q, the last of request r's
+    lens[r] tokens, each over the tokens up to itself; lse: device fp32
+    [N][heads] or None.  All tensors are on `device`, by default k_cache's (0
+    for addresses)."""
+    device = _device_of(device, k_cache)
+    _check(lib().kvtc_paged_attend_chunks(
+        device, R, N, heads, kv_heads, head_dim, dtype, _ptr(q), q_ld,
+        _ptr(k_cache), _ptr(v_cache), num_blocks, block_size,
+        _ptr(block_table), max_blocks, _ptr(cu), _ptr(lens), sink, window,
+        scale, _ptr(out), out_ld, _ptr(lse), _ptr(workspace),
+        workspace_bytes, _ptr(flags), _stream_on(stream, device)),
+        "kvtc_paged_attend_chunks")
+
+
+def kvtc_paged_weigh_workspace_bytes(R: int, N: int, heads: int,
+                                     kv_heads: int, head_dim: int,
+                                     device: int = 0) -> int:
+    return _check(lib().kvtc_paged_weigh_workspace_bytes(
+        device, R, N, heads, kv_heads, head_dim),
+        "kvtc_paged_weigh_workspace_bytes")
+
+
+def kvtc_paged_weigh(R: int, N: int, heads: int, kv_heads: int,
+                     head_dim: int, dtype: int, q, q_ld: int, k_cache,
+                     num_blocks: int, block_size: int, block_table,
+                     max_blocks: int, cu, lens, sink: int, window: int,
+                     scale: float, lse, decay: float, acc, acc_out,
+                     acc_ld: int, workspace, workspace_bytes: int,
+                     flags=None, device: Optional[int] = None,
+                     stream=None) -> None:
+    """acc_out[r][t] = decay * acc[r][t] + the weight that request r's rows
+    give to its token t, over all heads; lse as the attention returned it.
+    All tensors are on `device`, by default k_cache's (0 for addresses)."""
+    device = _device_of(device, k_cache)
+    _check(lib().kvtc_paged_weigh(
+        device, R, N, heads, kv_heads, head_dim, dtype, _ptr(q), q_ld,
+        _ptr(k_cache), num_blocks, block_size, _ptr(block_table), max_blocks,
+        _ptr(cu), _ptr(lens), sink, window, scale, _ptr(lse), decay,
+        _ptr(acc), _ptr(acc_out), acc_ld, _ptr(workspace), workspace_bytes,
+        _ptr(flags), _stream_on(stream, device)), "kvtc_paged_weigh")
+
+
+def kvtc_paged_evict_workspace_bytes(R: int, max_blocks: int) -> int:
+    return _check(lib().kvtc_paged_evict_workspace_bytes(R, max_blocks),
+                  "kvtc_paged_evict_workspace_bytes")
+
+
+def kvtc_paged_evict(R: int, acc, acc_ld: int, lens, keep: int, sink: int,
+                     window: int, block_table, out_table, max_blocks: int,
+                     block_size: int, cache: Sequence, D: int,
+                     num_blocks: int, kept, acc_out, lens_out, workspace,
+                     workspace_bytes: int, flags=None,
+                     device: Optional[int] = None, stream=None) -> None:
+    """Requests longer than keep tokens are cut to the first sink, the last
+    window and the heaviest of the others; their rows in all pools of `cache`
+    go to the blocks of out_table (block_table itself: in place).  All tensors
+    are on `device`, by default acc's (0 for addresses)."""
+    device = _device_of(device, acc)
+    _check(lib().kvtc_paged_evict(
+        device, R, _ptr(acc), acc_ld, _ptr(lens), keep, sink, window,
+        _ptr(block_table), _ptr(out_table), max_blocks, block_size,
+        len(cache), _ptr_array(cache), D, num_blocks, _ptr(kept),
+        _ptr(acc_out), _ptr(lens_out), _ptr(workspace), workspace_bytes,
+        _ptr(flags), _stream_on(stream, device)), "kvtc_paged_evict")
 
 
 def kvtc_wait_selftest(calib: Calib, limit_us: int, stream=None) -> None:
