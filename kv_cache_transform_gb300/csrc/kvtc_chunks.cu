@@ -1,9 +1,44 @@
 // Attention of chunks of new tokens over paged K and V pools.
+//
+// Rows of a matrix product are (token, query head) pairs that read one KV
+// head: row i * group + g is token i of the chunk and head g of the group, so
+// that few tokens fill a tile too.  For a row, with a running reference m near
+// the maximum,
+//     S = Q K^T,  P = 2^(scale log2(e) S - m),  l += sum P,  O += P V,
+// where a tile's maximum lies more than 2^8 above m, m moves to it, and l and
+// O are multiplied by 2^(m_old - m_new); out = O / l, lse = (m + log2 l) ln 2.
+//
+// Work.  An item is (request, KV head, up to two tiles of 128 rows), a unit
+// 128 tokens of K and V that an item's rows attend to.  All units of the call
+// are dealt out to one block per SM in equal runs, whatever the lengths are
+// (they are on the device: each block sums them itself).  A block whose run
+// begins or ends inside an item leaves m, l and O of its part, and
+// chunk_join_kernel joins the parts in a fixed order: equal calls give equal
+// bits.
+//
+// Inside a block:
+//   producer   goes through the run: item descriptors, Q, and the pages of K
+//              and V by TMA into a ring of stages (128 tokens x up to 128
+//              channels each);
+//   MMA        one thread issues S = Q K^T and O += P V (tcgen05, S, P and O
+//              in TMEM, P over the S that it came from);
+//   softmax    two warpgroups, a thread per row.  With two row tiles each has
+//              one, and the tensor cores work on one while the other's
+//              exponentials are formed; with one (few rows, head_dim 256) the
+//              first takes all units, S in two buffers;
+//   cleaner    rows of V in units that not every row attends to whole: those
+//              that none attends to are zeroed, and infinities and NaN taken
+//              out of the others (a weight of zero times them would be NaN);
+//              the softmax threads add them to the rows that attend to them.
+//
+// P is rounded to 16 bits for the product with V; l is the sum of the
+// unrounded weights.  Everything else is fp32.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -11,132 +46,1297 @@
 #include "../../include/kvtc.h"
 #include "kvtc_hostutil.cuh"
 #include "kvtc_internal.cuh"
+#include "ptx.cuh"
 
 namespace kvtc {
 namespace {
 
-constexpr int kBlock = 16;           // tokens per pool block
+constexpr int kBlock = 16;           // tokens per pool block (a page)
 constexpr int kMaxReq = 4096;        // requests per call
 constexpr int kMaxGroup = 128;       // query heads per KV head
 constexpr int kMaxTable = INT32_MAX / kBlock - 1;
-constexpr float kMaxScale = 0x1p127f;
+constexpr int kCtas = 152;           // one block per SM
+constexpr int kRows = 128;           // rows of a tile (TMEM lanes)
+constexpr int kUnit = 128;           // tokens of a unit
+constexpr int kPages = kUnit / kBlock;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kMaxScale = 0x1p127f;  // times log2 e still finite
+constexpr float kSlack = 8.f;          // log2
+constexpr int kWarps = 12;            // (the last one only fills its warpgroup)
+constexpr int kProducer = 8, kMma = 9, kCleaner = 10;
+constexpr int kThreads = kWarps * 32;
+constexpr int kItems = 4, kMetas = 8;  // entries of the rings
+
+// Which blocks hold parts of an item that began in a block and did not end
+// there; r < 0: there is none.
+struct __align__(16) JoinDesc {
+  int64_t row0;
+  int32_t r, j, ntok, last;
+};
 
 struct ChunkParams {
-  const void* q;
-  const void* k;
-  const void* v;
+  CUtensorMap tm_q;         // {64, HD / 64, heads, N}, box {64, 1, group, tq}
+  CUtensorMap tm_k, tm_v;   // {64, 16, D / 64, num_blocks}, box {64, 16, 1, 1}
   const int32_t* table;
   const int64_t* cu;
   const int32_t* lens;
+  const void* v;
   void* out;
   float* lse;
   unsigned* flags;
-  int64_t N, q_ld, out_ld, num_blocks;
-  float scale;
+  JoinDesc* desc;           // [kCtas]
+  float* slots;             // [kCtas][2] parts: 0 of an item begun in an
+                            // earlier block, 1 of one begun in this block
+  int64_t N, out_ld, num_blocks;
+  float scale;              // times log2 e; positive, else as pre
+  float pre;                // where pre_on: scores are multiplied by it first
+  int32_t pre_on;
   int32_t R, heads, kv_heads, max_blocks, sink, window;
+  int32_t group, tq;        // query heads a KV head; tokens per row tile
 };
 
-__device__ __forceinline__ float to_float(__nv_bfloat16 x) {
-  return __bfloat162float(x);
+template <int HD_>
+struct Cfg {
+  static constexpr int HD = HD_;
+  static constexpr int QT = HD == 256 ? 1 : 2;        // row tiles per item
+  static constexpr int SC = HD < 128 ? HD : 128;      // channels per stage
+  static constexpr int NS = HD / SC;                  // stages per K or V tile
+  static constexpr int kSlabs = SC / 64;              // per stage
+  static constexpr int kStage = kUnit * SC * 2;
+  static constexpr int S = HD == 64 ? 8 : 5;
+  static constexpr int kQ = QT * kRows * HD * 2;
+  static constexpr int kRing = kQ;
+  static constexpr int kMisc = kRing + S * kStage;
+  static constexpr int kBytes = kMisc + 1536 + 1024;  // + alignment slack
+  static_assert(kBytes <= 232448, "shared memory of a block");
+  static_assert(S * kStage >= 8 * (kMaxReq + 1), "prefix of the requests");
+  // TMEM columns
+  static constexpr int kO = 256;                      // O of tile t: + 128 t
+  static constexpr int kPart = kRows * (HD + 2);      // floats of a part tile
+};
+
+struct __align__(16) Item {
+  int64_t row0;             // first row (token) of the call
+  int32_t r, j;             // request, KV head
+  int32_t ntok, pf;         // tokens, position of the first
+  int32_t units;            // of this block; 0: the end
+  int32_t flags;
+};
+constexpr int kStarts = 1, kEnds = 2, kDual = 4;
+
+struct __align__(16) Meta {
+  int32_t t0;               // first token
+  uint32_t pages;           // which of its pages are there
+  int32_t mixed;            // not every row attends to all of it
+  int32_t pad;
+  uint32_t odd[4];          // tokens whose V held infinities or NaN
+};
+
+// ------------------------------------------------------------ PTX wrappers
+__device__ __forceinline__ void tma_load_4d(uint32_t smem_dst,
+                                            const void* tmap, int32_t x,
+                                            int32_t y, int32_t z, int32_t w,
+                                            uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_"
+      "tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_dst),
+      "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+      : "memory");
 }
-__device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
-template <class T>
-__device__ __forceinline__ T from_float(float x);
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_float(float x) {
-  return __float2bfloat16(x);
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]),
+      "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]),
+      "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
 }
-template <>
-__device__ __forceinline__ __half from_float(float x) {
-  return __float2half(x);
+__device__ __forceinline__ uint32_t tmem_ld1(uint32_t taddr) {
+  uint32_t r;
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];"
+               : "=r"(r)
+               : "r"(taddr));
+  return r;
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float rcp_fast(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t d, x = *reinterpret_cast<uint64_t*>(&a),
+              y = *reinterpret_cast<uint64_t*>(&b),
+              z = *reinterpret_cast<uint64_t*>(&c);
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(x), "l"(y), "l"(z));
+  return *reinterpret_cast<float2*>(&d);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  uint64_t d, x = *reinterpret_cast<uint64_t*>(&a),
+              y = *reinterpret_cast<uint64_t*>(&b);
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(x), "l"(y));
+  return *reinterpret_cast<float2*>(&d);
+}
+// A V tile as the B operand: channels contiguous (64 of them in the swizzle's
+// 128 bytes, the next 64 a slab further on), eight tokens an atom.
+__device__ __forceinline__ uint64_t v_desc(uint32_t smem_addr) {
+  return (sw128_desc(smem_addr) & ~((uint64_t)0x3FFF << 16)) |
+         ((uint64_t)(kUnit * 128 >> 4) << 16);
 }
 
-// A block per row, a warp per query head: one token after the other.
-template <class T, int HD>
-__global__ void __launch_bounds__(256)
-    chunk_simple_kernel(const __grid_constant__ ChunkParams p) {
-  constexpr int kEach = HD / 32;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t row = blockIdx.x;
-  int lo = 0, hi = p.R;               // cu[lo] <= row < cu[hi]
-  if (row < p.cu[0] || row >= p.cu[p.R]) {
-    if (row == 0 && threadIdx.x == 0 && p.cu[p.R] > p.N && p.flags)
-      atomicOr(p.flags, KVTC_FLAG_SPACE);
-    return;
+template <class T>
+struct Elem;
+template <>
+struct Elem<__nv_bfloat16> {
+  static constexpr uint32_t kFormat = 1;
+  static constexpr float kShift = 0.f;
+  static constexpr uint32_t kExp = 0x7F807F80u, kOne = 0x00800080u;
+  static __device__ __forceinline__ uint32_t pack(float a, float b) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
   }
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (p.cu[mid] <= row) lo = mid; else hi = mid;
+  static __device__ __forceinline__ float2 unpack(uint32_t x) {
+    return make_float2(__uint_as_float(x << 16),
+                       __uint_as_float(x & 0xFFFF0000u));
   }
-  const int r = lo;
-  const int64_t c0 = min(max(p.cu[r], (int64_t)0), p.N);
-  const int64_t c1 = min(max(p.cu[r + 1], (int64_t)0), p.N);
-  const int64_t most = (int64_t)p.max_blocks * kBlock;
-  const int64_t len = min(max((int64_t)p.lens[r], (int64_t)0), most);
-  if (p.flags && threadIdx.x == 0 &&
-      (p.lens[r] > most || p.cu[r + 1] > p.N))
-    atomicOr(p.flags, KVTC_FLAG_SPACE);
-  const int64_t pos = len - (c1 - c0) + (row - c0);
-  const int group = p.heads / p.kv_heads;
-  for (int h = warp; h < p.heads; h += 8) {
-    const T* q = static_cast<const T*>(p.q) + row * p.q_ld + h * HD;
-    float qv[kEach], o[kEach], m = -INFINITY, l = 0.f;
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      qv[i] = to_float(q[i * 32 + lane]) * p.scale;
-      o[i] = 0.f;
+};
+// fp16 holds numbers from 2^-24 to 2^16: weights are formed 2^7 times as
+// large, up to 2^15, and what is lost lies 2^-32 below the largest.
+template <>
+struct Elem<__half> {
+  static constexpr uint32_t kFormat = 0;
+  static constexpr float kShift = 7.f;
+  static constexpr uint32_t kExp = 0x7C007C00u, kOne = 0x04000400u;
+  static __device__ __forceinline__ uint32_t pack(float a, float b) {
+    const __half2 v = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+  static __device__ __forceinline__ float2 unpack(uint32_t x) {
+    return __half22float2(*reinterpret_cast<const __half2*>(&x));
+  }
+};
+// Halves of a word that are infinite or NaN, as bits 15 and 31.
+template <class T>
+__device__ __forceinline__ uint32_t odd_of(uint32_t w) {
+  return ((w & Elem<T>::kExp) + Elem<T>::kOne) & 0x80008000u;
+}
+
+// ------------------------------------------------------------------- spans
+// Units of an item whose rows are at positions pf .. pl: `units` of them, the
+// first `front` at their own place, the others `gap` further on.  An item
+// whose rows attend to nothing still has one, which is empty.
+struct Span {
+  int32_t units, front, gap;
+  __device__ __forceinline__ Span(const ChunkParams& p, int32_t pf,
+                                  int32_t pl) {
+    const int32_t all = pl >= 0 ? pl / kUnit + 1 : 0;
+    front = all;
+    gap = 0;
+    if (p.window) {
+      const int64_t lo = (int64_t)pf - p.window + 1;
+      const int32_t back = lo > 0 ? (int32_t)(lo / kUnit) : 0;
+      front = (int32_t)min(((int64_t)p.sink + kUnit - 1) / kUnit,
+                           (int64_t)all);
+      gap = max(back - front, 0);
     }
-    for (int64_t t = 0; t <= pos; ++t) {
-      if (p.window && t >= p.sink && t <= pos - p.window) continue;
-      const int64_t id = p.table[(int64_t)r * p.max_blocks + t / kBlock];
-      if (id < 0 || id >= p.num_blocks) {
-        if (lane == 0 && p.flags) atomicOr(p.flags, KVTC_FLAG_BLOCK);
-        continue;
+    units = max(all - gap, 1);
+  }
+};
+// A request's rows and length.
+struct Request {
+  int64_t c0;
+  int32_t n, len;
+  __device__ __forceinline__ Request(const ChunkParams& p, int r) {
+    c0 = 0;
+    n = len = 0;
+    if (r < p.R) {
+      c0 = min(max(p.cu[r], (int64_t)0), p.N);
+      n = (int32_t)max(min(max(p.cu[r + 1], (int64_t)0), p.N) - c0,
+                       (int64_t)0);
+      len = min(max(p.lens[r], 0), p.max_blocks * kBlock);
+    }
+  }
+  __device__ __forceinline__ Request(int64_t c0, int32_t n, int32_t len)
+      : c0(c0), n(n), len(len) {}
+};
+// Cost of item i of a request (per KV head), in units: one more than it has,
+// for the begin and the end.
+__device__ __forceinline__ int64_t item_cost(const ChunkParams& p,
+                                             int32_t n, int32_t len, int32_t i,
+                                             int32_t per) {
+  const int32_t first = i * per, last = min(first + per, n) - 1;
+  return Span(p, len - n + first, len - n + last).units + 1;
+}
+// `total` costs in equal runs over the first `ctas` blocks.
+struct Deal {
+  int64_t least;
+  int32_t more, ctas;
+  __device__ __forceinline__ explicit Deal(int64_t total) {
+    ctas = (int32_t)min((int64_t)kCtas, max(total / 3, (int64_t)1));
+    least = total / ctas;
+    more = (int32_t)(total - least * ctas);
+  }
+  __device__ __forceinline__ int64_t begin(int c) const {
+    return c >= ctas ? least * ctas + more : c * least + min(c, more);
+  }
+  __device__ __forceinline__ int cta_of(int64_t x) const {
+    const int64_t wide = more * (least + 1);
+    return (int)(x < wide ? x / (least + 1) : more + (x - wide) / least);
+  }
+};
+
+__device__ __forceinline__ uint32_t low_bits(int64_t n) {
+  return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << (int)n) - 1u;
+}
+// Which of the tokens t0 + 32 w .. + 31 the row at `pos` attends to.
+__device__ __forceinline__ uint32_t seen_bits(const ChunkParams& p,
+                                              const Meta& m, int64_t pos,
+                                              int w) {
+  const int64_t t = (int64_t)m.t0 + 32 * w;
+  uint32_t bits = low_bits(pos - t + 1);
+  if (p.window)
+    bits &= low_bits(p.sink - t) | ~low_bits(pos - p.window + 1 - t);
+  const uint32_t pages = m.pages >> (2 * w);
+  return bits & ((pages & 1 ? 0xFFFFu : 0u) | (pages & 2 ? 0xFFFF0000u : 0u));
+}
+
+// A phase of a ring of N barriers.
+template <int N>
+struct Turn {
+  int at = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++at == N) {
+      at = 0;
+      phase ^= 1;
+    }
+  }
+};
+
+struct Bars {
+  uint64_t full[8], empty[8];      // stages
+  uint64_t q_full, q_empty;
+  uint64_t item_full[kItems], item_empty[kItems];
+  uint64_t meta[kMetas], clean[kMetas];       // units
+  uint64_t s_full[4], p_full[4];   // tiles 0, 1; buffers 0, 1 of a lone tile
+  uint64_t pv_done[2], fin;
+};
+
+struct Smem {
+  Bars bars;
+  Item items[kItems];
+  Meta metas[kMetas];
+  int64_t sums[kWarps];
+  uint32_t tmem;
+  int abort_flag;
+};
+static_assert(sizeof(Smem) <= 1536, "the kernels' shared variables");
+
+// A wait that all lanes leave with the same answer.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity,
+                                          const volatile int* stop) {
+  return __all_sync(~0u, mbar_wait(bar, parity, stop));
+}
+
+// --------------------------------------------------------------- producer
+template <class T, class C>
+__device__ __forceinline__ bool produce(const ChunkParams& p, Smem& sm,
+                                        uint32_t smem, const int64_t* pre) {
+  constexpr int HD = C::HD, NS = C::NS, S = C::S;
+  const int lane = (int)lane_id();
+  Bars& b = sm.bars;
+  volatile int* stop = &sm.abort_flag;
+  Turn<S> st;
+  Turn<kItems> it;
+  Turn<kMetas> mt;
+  uint32_t q_phase = 0;
+  int fills = 0;                       // times that the ring went round
+  const int64_t total = pre[p.R];
+  const Deal deal(total);
+  int64_t x = deal.begin(blockIdx.x);
+  const int64_t end = deal.begin(blockIdx.x + 1);
+  const int32_t per = C::QT * p.tq;
+  int r = 0, j = 0, i = 0;
+  int64_t y = 0;                       // x within its item
+  if (x < end) {
+    // the request (the last one that begins at or before x and is not empty)
+    int lo = 0, hi = p.R;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (pre[mid] <= x) lo = mid; else hi = mid;
+    }
+    r = lo;
+    const Request q(p, r);
+    const int64_t head = (pre[r + 1] - pre[r]) / p.kv_heads;
+    y = x - pre[r];
+    j = (int)(y / head);
+    y -= j * head;
+    // the item, 32 at a time
+    const int items = (q.n + per - 1) / per;
+    for (;;) {
+      const int64_t cost =
+          i + lane < items ? item_cost(p, q.n, q.len, i + lane, per) : 0;
+      int64_t upto = cost;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int64_t o = __shfl_up_sync(~0u, upto, d);
+        if (lane >= d) upto += o;
       }
-      const int64_t at =
-          ((id * kBlock + t % kBlock) * p.kv_heads + h / group) * HD + lane;
-      const T* k = static_cast<const T*>(p.k) + at;
-      const T* v = static_cast<const T*>(p.v) + at;
-      float s = 0.f;
-#pragma unroll
-      for (int i = 0; i < kEach; ++i)
-        s = fmaf(qv[i], to_float(k[i * 32]), s);
-#pragma unroll
-      for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(~0u, s, d);
-      if (s == -INFINITY) continue;
-      const float top = fmaxf(m, s);
-      const float was = expf(m - top), w = expf(s - top);
-      m = top;
-      l = l * was + w;
-#pragma unroll
-      for (int i = 0; i < kEach; ++i)
-        o[i] = fmaf(w, to_float(v[i * 32]), o[i] * was);
+      const uint32_t past = __ballot_sync(~0u, upto > y);
+      if (past) {
+        const int at = __ffs(past) - 1;
+        y -= __shfl_sync(~0u, upto - cost, at);
+        i += at;
+        break;
+      }
+      y -= __shfl_sync(~0u, upto, 31);
+      i += 32;
     }
-    T* out = static_cast<T*>(p.out) + row * p.out_ld + h * HD;
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-    for (int i = 0; i < kEach; ++i)
-      out[i * 32 + lane] = from_float<T>(o[i] * inv);
-    if (lane == 0 && p.lse)
-      p.lse[row * p.heads + h] = l == 0.f ? -INFINITY : m + logf(l);
   }
+  __syncwarp();
+  // the prefix sums lay where the TMA is going to write
+  asm volatile("fence.proxy.async;" ::: "memory");
+  bool ok = true, left_desc = false;
+  int base = r;                        // requests base .. base + 31
+  Request batch(p, base + lane);
+  while (x < end && ok) {
+    if (r >= base + 32) {
+      base = r;
+      batch = Request(p, base + lane);
+    }
+    const Request q(__shfl_sync(~0u, batch.c0, r - base),
+                    __shfl_sync(~0u, batch.n, r - base),
+                    __shfl_sync(~0u, batch.len, r - base));
+    const int items = (q.n + per - 1) / per;
+    if (items == 0) {
+      ++r;
+      continue;
+    }
+    const int32_t first = i * per, ntok = min(per, q.n - first);
+    const int32_t pf = q.len - q.n + first, pl = pf + ntok - 1;
+    const Span span(p, pf, pl);
+    const int64_t k0 = max(y - 1, (int64_t)0);
+    const int64_t k1 = min((int64_t)span.units, y + (end - x) - 1);
+    const bool dual = ntok > p.tq;
+    if (k1 > k0) {
+      if (!warp_wait(&b.item_empty[it.at], it.phase ^ 1, stop)) {
+        ok = false;
+        break;
+      }
+      if (lane == 0) {
+        Item d;
+        d.row0 = q.c0 + first;
+        d.r = r;
+        d.j = j;
+        d.ntok = ntok;
+        d.pf = pf;
+        d.units = (int32_t)(k1 - k0);
+        d.flags = (k0 == 0 ? kStarts : 0) | (k1 == span.units ? kEnds : 0) |
+                  (dual ? kDual : 0);
+        sm.items[it.at] = d;
+        mbar_arrive(&b.item_full[it.at]);
+        if (k0 == 0 && k1 < span.units) {
+          JoinDesc jd;
+          jd.row0 = d.row0;
+          jd.r = r;
+          jd.j = j;
+          jd.ntok = ntok;
+          jd.last = deal.cta_of(x - y + span.units);
+          p.desc[blockIdx.x] = jd;
+          left_desc = true;
+        }
+      }
+      it.next();
+      const int32_t* row = p.table + (int64_t)r * p.max_blocks;
+      // lane l: page l % 8, slab l / 8
+      const int page = lane % kPages, slab = lane / kPages;
+      const int slab_all = j * (HD / 64) + slab;
+      auto id_at = [&](int64_t k) -> int32_t {
+        const int32_t t0 =
+            (int32_t)(k < span.front ? k : k + span.gap) * kUnit;
+        const int32_t tp = t0 + page * kBlock;
+        const bool need =
+            pl >= 0 && tp <= pl &&
+            (!p.window || tp < p.sink ||
+             (int64_t)tp + kBlock - 1 > (int64_t)pf - p.window);
+        return need ? row[tp / kBlock] : -1 - INT_MAX;
+      };
+      int32_t id = id_at(k0);
+      for (int64_t k = k0; k < k1 && ok; ++k) {
+        const int32_t next_id = k + 1 < k1 ? id_at(k + 1) : 0;
+        const int32_t t0 =
+            (int32_t)(k < span.front ? k : k + span.gap) * kUnit;
+        const bool fine = id >= 0 && id < p.num_blocks;
+        const int32_t tp = t0 + page * kBlock;
+        // (ids that are not asked for are -2^31; one in the table is bad too)
+        if (!fine && slab == 0 && p.flags && pl >= 0 && tp <= pl &&
+            (!p.window || tp < p.sink ||
+             (int64_t)tp + kBlock - 1 > (int64_t)pf - p.window))
+          atomicOr(p.flags, KVTC_FLAG_BLOCK);
+        const uint32_t pages = __ballot_sync(~0u, fine) & 0xFFu;
+        if (lane == 0) {
+          Meta m;
+          m.t0 = t0;
+          m.pages = pages;
+          const int64_t tl = (int64_t)t0 + kUnit - 1;
+          m.mixed = !(pages == 0xFF && tl <= pf &&
+                      (!p.window || tl < p.sink ||
+                       (int64_t)t0 > (int64_t)pl - p.window));
+          sm.metas[mt.at].t0 = m.t0;
+          sm.metas[mt.at].pages = m.pages;
+          sm.metas[mt.at].mixed = m.mixed;
+          mbar_arrive(&b.meta[mt.at]);
+        }
+        mt.next();
+        const uint32_t bytes = __popc(pages) * C::kSlabs * 2048;
+#pragma unroll
+        for (int kv = 0; kv < 2 && ok; ++kv) {
+          const void* map = kv ? &p.tm_v : &p.tm_k;
+#pragma unroll
+          for (int s = 0; s < NS; ++s) {
+            if (!warp_wait(&b.empty[st.at], st.phase ^ 1, stop)) {
+              ok = false;
+              break;
+            }
+            if (lane == 0) mbar_arrive_expect_tx(&b.full[st.at], bytes);
+            __syncwarp();
+            if (fine && slab >= s * C::kSlabs && slab < (s + 1) * C::kSlabs)
+              tma_load_4d(smem + C::kRing + st.at * C::kStage +
+                              (slab - s * C::kSlabs) * (kUnit * 128) +
+                              page * 2048,
+                          map, 0, 0, slab_all, id, &b.full[st.at]);
+            st.next();
+            ++fills;
+          }
+        }
+        id = next_id;
+        if (k == k0 && ok) {
+          // Q, behind the first unit: the item before has to be done with it
+          if (!warp_wait(&b.q_empty, q_phase ^ 1, stop)) {
+            ok = false;
+            break;
+          }
+          const int tiles = dual ? 2 : 1;
+          if (lane == 0)
+            mbar_arrive_expect_tx(
+                &b.q_full, tiles * (HD / 64) * p.tq * p.group * 128);
+          __syncwarp();
+          if (lane < tiles * (HD / 64)) {
+            const int t = lane / (HD / 64), sl = lane % (HD / 64);
+            tma_load_4d(smem + t * (kRows * HD * 2) + sl * (kRows * 128),
+                        &p.tm_q, 0, sl, j * p.group,
+                        (int32_t)(q.c0 + first) + t * p.tq, &b.q_full);
+          }
+          q_phase ^= 1;
+        }
+      }
+    }
+    const int64_t step = min((int64_t)span.units + 1 - y, end - x);
+    x += step;
+    y = 0;
+    if (++i == items) {
+      i = 0;
+      if (++j == p.kv_heads) {
+        j = 0;
+        ++r;
+      }
+    }
+  }
+  if (ok && warp_wait(&b.item_empty[it.at], it.phase ^ 1, stop)) {
+    if (lane == 0) {
+      sm.items[it.at].units = 0;
+      mbar_arrive(&b.item_full[it.at]);
+    }
+  } else {
+    ok = false;
+  }
+  if (lane == 0 && !left_desc) p.desc[blockIdx.x].r = -1;
+  // loads under way land before the block's memory is given up
+  __syncwarp();
+  if (lane == 0) {
+    mbar_drain(&b.q_full, q_phase ^ 1);
+    Turn<S> back = st;
+    for (int k = min(fills, S); k > 0; --k) {
+      if (back.at-- == 0) {
+        back.at = S - 1;
+        back.phase ^= 1;
+      }
+      mbar_drain(&b.full[back.at], back.phase);
+    }
+  }
+  return ok;
+}
+
+// -------------------------------------------------------------------- MMA
+template <class T, class C>
+__device__ __forceinline__ bool multiply(const ChunkParams& p, Smem& sm,
+                                         uint32_t smem, uint32_t tmem) {
+  constexpr int HD = C::HD, NS = C::NS, S = C::S, SC = C::SC;
+  constexpr uint32_t kIdS = make_idesc(kRows, kUnit, Elem<T>::kFormat);
+  // (bit 16: B's rows are contiguous)
+  constexpr uint32_t kIdO =
+      make_idesc(kRows, SC, Elem<T>::kFormat) | (1u << 16);
+  Bars& b = sm.bars;
+  volatile int* stop = &sm.abort_flag;
+  Turn<S> st;                    // the unit's first stage
+  Turn<kItems> it;
+  Turn<kMetas> mt;
+  uint32_t q_phase = 0;
+  uint32_t p_phase = 0;          // a bit per barrier
+  const uint32_t ring = smem + C::kRing;
+
+  // S of tile t into buffer `to`, from the K tile that begins at stage k
+  auto qk = [&](int t, int to, Turn<S> k) {
+    const uint32_t d = tmem + to * kUnit;
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      const uint64_t bd = sw128_desc(ring + k.at * C::kStage);
+      const uint64_t ad = sw128_desc(smem + t * (kRows * HD * 2) +
+                                     s * C::kSlabs * (kRows * 128));
+#pragma unroll
+      for (int e = 0; e < SC / 16; ++e) {
+        const uint32_t off = (e / 4) * (kUnit * 128 >> 4) + (e % 4) * 2;
+        mma_ss(d, ad + off, bd + off, kIdS, (s | e) > 0);
+      }
+      k.next();
+    }
+  };
+  // O of tile t, from P in buffer `from` and the V tile that begins at v
+  auto pv = [&](int t, int from, Turn<S> v, bool more) {
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      const uint64_t bd = v_desc(ring + v.at * C::kStage);
+      const uint32_t d = tmem + C::kO + t * 128 + s * SC;
+#pragma unroll
+      for (int e = 0; e < kUnit / 16; ++e)
+        mma_ts(d, tmem + from * kUnit + e * 8, bd + e * (2048 >> 4), kIdO,
+               more || e > 0);
+      v.next();
+    }
+  };
+  auto wait_k = [&](Turn<S> k) {
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      if (!mbar_wait(&b.full[k.at], k.phase, stop)) return false;
+      k.next();
+    }
+    return true;
+  };
+  auto wait_v = [&] {
+    const bool ok = mbar_wait(&b.clean[mt.at], mt.phase, stop);
+    mt.next();
+    return ok;
+  };
+  auto wait_p = [&](int i) {
+    const bool ok = mbar_wait(&b.p_full[i], (p_phase >> i) & 1, stop);
+    p_phase ^= 1u << i;
+    tc_fence_after();
+    return ok;
+  };
+  auto release = [&](Turn<S> k) {
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      tc_commit(&b.empty[k.at]);
+      k.next();
+    }
+  };
+  auto ahead = [&](Turn<S> k, int stages) {
+    for (int s = 0; s < stages; ++s) k.next();
+    return k;
+  };
+  for (;;) {
+    if (!mbar_wait(&b.item_full[it.at], it.phase, stop)) return false;
+    const int units = sm.items[it.at].units;
+    const bool dual = sm.items[it.at].flags & kDual;
+    if (units == 0) return true;
+    if (!mbar_wait(&b.q_full, q_phase, stop)) return false;
+    q_phase ^= 1;
+    // stages of unit k: K at st + 2 NS k, V NS further on
+    if (!wait_k(st)) return false;
+    tc_fence_after();
+    if (dual) {
+      qk(0, 0, st);
+      tc_commit(&b.s_full[0]);
+      qk(1, 1, st);
+      tc_commit(&b.s_full[1]);
+      release(st);
+      if (units == 1) tc_commit(&b.q_empty);
+      for (int k = 0; k < units; ++k) {
+        const Turn<S> v = ahead(st, NS), next = ahead(st, 2 * NS);
+        const bool more = k + 1 < units;
+        if (!wait_v() || !wait_p(0)) return false;
+        pv(0, 0, v, k > 0);
+        tc_commit(&b.pv_done[0]);
+        if (more) {
+          if (!wait_k(next)) return false;
+          tc_fence_after();
+          qk(0, 0, next);
+          tc_commit(&b.s_full[0]);
+        }
+        if (!wait_p(1)) return false;
+        pv(1, 1, v, k > 0);
+        tc_commit(&b.pv_done[1]);
+        release(v);
+        if (more) {
+          qk(1, 1, next);
+          tc_commit(&b.s_full[1]);
+          release(next);
+          if (k + 2 == units) tc_commit(&b.q_empty);
+        }
+        st = next;
+      }
+    } else {
+      qk(0, 0, st);
+      tc_commit(&b.s_full[2]);
+      release(st);
+      if (units == 1) tc_commit(&b.q_empty);
+      for (int k = 0; k < units; ++k) {
+        const Turn<S> v = ahead(st, NS), next = ahead(st, 2 * NS);
+        if (k + 1 < units) {
+          // the other buffer's P went into its product before this one's S
+          if (!wait_k(next)) return false;
+          tc_fence_after();
+          qk(0, (k + 1) & 1, next);
+          tc_commit(&b.s_full[2 + ((k + 1) & 1)]);
+          release(next);
+          if (k + 2 == units) tc_commit(&b.q_empty);
+        }
+        if (!wait_v() || !wait_p(2 + (k & 1))) return false;
+        pv(0, k & 1, v, k > 0);
+        tc_commit(&b.pv_done[0]);
+        release(v);
+        st = next;
+      }
+    }
+    mbar_arrive(&b.item_empty[it.at]);
+    it.next();
+  }
+}
+
+// ---------------------------------------------------------------- cleaner
+template <class T, class C>
+__device__ __forceinline__ bool clean(const ChunkParams& p, Smem& sm,
+                                      uint8_t* smem) {
+  constexpr int NS = C::NS, S = C::S;
+  const int lane = (int)lane_id();
+  Bars& b = sm.bars;
+  volatile int* stop = &sm.abort_flag;
+  Turn<S> st;
+  Turn<kItems> it;
+  Turn<kMetas> mt;
+  for (;;) {
+    if (!warp_wait(&b.item_full[it.at], it.phase, stop)) return false;
+    const Item item = sm.items[it.at];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&b.item_empty[it.at]);
+    it.next();
+    if (item.units == 0) return true;
+    const int64_t pf = item.pf, pl = pf + item.ntok - 1;
+    for (int k = 0; k < item.units; ++k) {
+      if (!warp_wait(&b.meta[mt.at], mt.phase, stop)) return false;
+      Meta& m = sm.metas[mt.at];
+      const int32_t t0 = m.t0;
+      const uint32_t pages = m.pages;
+      const bool mixed = m.mixed;
+      for (int s = 0; s < NS; ++s) st.next();     // K's
+      uint32_t found[4] = {0, 0, 0, 0};
+#pragma unroll
+      for (int s = 0; s < NS; ++s) {
+        if (!warp_wait(&b.full[st.at], st.phase, stop)) return false;
+        if (mixed) {
+          uint8_t* tile = smem + C::kRing + st.at * C::kStage;
+          // four tokens at a time, eight lanes each
+#pragma unroll 1
+          for (int g = 0; g < kUnit / 4; ++g) {
+            const int row = g * 4 + lane / 8;
+            const int64_t t = (int64_t)t0 + row;
+            const bool none =
+                !((pages >> (row / kBlock)) & 1) || t > pl ||
+                (p.window && t >= p.sink && t <= pf - p.window);
+            const bool every = t <= pf && (!p.window || t < p.sink ||
+                                           t > pl - p.window);
+            if (!__any_sync(~0u, none || !every)) continue;
+            bool odd = false;
+#pragma unroll
+            for (int sl = 0; sl < C::kSlabs; ++sl) {
+              uint4* at = reinterpret_cast<uint4*>(
+                  tile + sl * (kUnit * 128) + row * 128 + (lane % 8) * 16);
+              if (none) {
+                *at = make_uint4(0, 0, 0, 0);
+              } else if (!every) {
+                const uint4 w = *at;
+                const uint32_t o[4] = {odd_of<T>(w.x), odd_of<T>(w.y),
+                                       odd_of<T>(w.z), odd_of<T>(w.w)};
+                if (o[0] | o[1] | o[2] | o[3]) {
+                  odd = true;
+                  // (bit 15 of a half: all of its 16 bits)
+                  auto keep = [](uint32_t x, uint32_t bits) {
+                    return x & ~((bits >> 15) * 0xFFFFu);
+                  };
+                  *at = make_uint4(keep(w.x, o[0]), keep(w.y, o[1]),
+                                   keep(w.z, o[2]), keep(w.w, o[3]));
+                }
+              }
+            }
+            const uint32_t who = __ballot_sync(~0u, odd);
+            if (who) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if ((who >> (8 * e)) & 0xFF) {
+                  const int at = g * 4 + e;
+#pragma unroll
+                  for (int w = 0; w < 4; ++w)
+                    if (at / 32 == w) found[w] |= 1u << (at % 32);
+                }
+            }
+          }
+          if (s == NS - 1 && lane == 0) {
+#pragma unroll
+            for (int w = 0; w < 4; ++w) m.odd[w] = found[w];
+          }
+          fence_proxy_async_smem();
+        }
+        st.next();
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&b.clean[mt.at]);
+      mt.next();
+    }
+  }
+}
+
+// ---------------------------------------------------------------- softmax
+// Infinities and NaN that the cleaner took out of V, for the rows that attend
+// to them: v times the row's weight, added to O behind the unit's product.
+// `has`: tokens of the unit that this row attends to with a weight above 0,
+// `none`: with one of 0.
+template <class T, int HD>
+__device__ __noinline__ void add_odd(const ChunkParams& p, const Item& item,
+                                     int32_t t0, const uint32_t (&odd)[4],
+                                     const uint32_t (&has)[4],
+                                     const uint32_t (&none)[4], uint32_t o) {
+  for (int w = 0; w < 4; ++w) {
+    for (uint32_t m = odd[w]; m; m &= m - 1) {
+      const int bit = __ffs(m) - 1;
+      const int64_t t = (int64_t)t0 + 32 * w + bit;
+      const int64_t id =
+          p.table[(int64_t)item.r * p.max_blocks + t / kBlock];
+      const T* v = static_cast<const T*>(p.v) +
+                   ((id * kBlock + t % kBlock) * p.kv_heads + item.j) * HD;
+      const float weight = (has[w] >> bit) & 1    ? 1.f
+                           : (none[w] >> bit) & 1 ? 0.f
+                                                  : -1.f;
+#pragma unroll 1
+      for (int c = 0; c < HD; c += 16) {
+        float acc[16];
+        tmem_ld16(o + c, acc);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float2 x = Elem<T>::unpack(
+              reinterpret_cast<const uint32_t*>(v + c)[e]);
+          if (weight >= 0.f && !isfinite(x.x)) acc[2 * e] += x.x * weight;
+          if (weight >= 0.f && !isfinite(x.y)) acc[2 * e + 1] += x.y * weight;
+        }
+        uint32_t r[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(acc[e]);
+        tmem_st16(o + c, r);
+        tmem_wait_st();
+      }
+    }
+  }
+}
+
+template <class T, class C>
+__device__ __forceinline__ bool soften(const ChunkParams& p, Smem& sm,
+                                       uint32_t tmem, int warp) {
+  constexpr int HD = C::HD;
+  const int lane = (int)lane_id(), wg = warp >> 2;
+  const int row = (warp & 3) * 32 + lane;
+  const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);
+  const uint32_t o_at = lanes + C::kO + wg * 128;
+  Bars& b = sm.bars;
+  volatile int* stop = &sm.abort_flag;
+  Turn<kItems> it;
+  Turn<kMetas> mt;
+  uint32_t s_phase = 0;          // a bit per barrier
+  uint32_t pv_phase = 0;         // of the next product
+  const float shift = Elem<T>::kShift;
+  const int tok = row / p.group, head = row - tok * p.group;
+  for (;;) {
+    if (!warp_wait(&b.item_full[it.at], it.phase, stop)) return false;
+    const Item item = sm.items[it.at];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&b.item_empty[it.at]);
+    it.next();
+    if (item.units == 0) return true;
+    const bool dual = item.flags & kDual;
+    if (wg && !dual) {           // not this warpgroup's
+      for (int k = 0; k < item.units; ++k) mt.next();
+      continue;
+    }
+    const int32_t mine = wg * p.tq + tok;         // the row's token
+    const int64_t pos = (int64_t)item.pf + mine;
+    const bool valid = tok < p.tq && mine < item.ntok;
+    float m = -INFINITY;
+    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+    for (int k = 0; k < item.units; ++k) {
+      const int buf = dual ? wg : k & 1;
+      const int bar = dual ? wg : 2 + buf;
+      const uint32_t s_at = lanes + buf * kUnit;
+      if (!warp_wait(&b.meta[mt.at], mt.phase, stop)) return false;
+      if (!warp_wait(&b.s_full[bar], (s_phase >> bar) & 1, stop)) return false;
+      s_phase ^= 1u << bar;
+      tc_fence_after();
+      const Meta& meta = sm.metas[mt.at];
+      const bool mixed = meta.mixed;
+      float s[kUnit];
+#pragma unroll
+      for (int c = 0; c < kUnit; c += 32) tmem_ld32(s_at + c, s + c);
+      tmem_wait_ld();
+      if (p.pre_on) {
+#pragma unroll
+        for (int c = 0; c < kUnit; ++c) s[c] *= p.pre;
+      }
+      if (mixed) {
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const uint32_t seen = seen_bits(p, meta, pos, w);
+#pragma unroll
+          for (int c = 0; c < 32; ++c)
+            if (!((seen >> c) & 1)) s[w * 32 + c] = -INFINITY;
+        }
+      }
+      float top[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+      for (int c = 4; c < kUnit; c += 4) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) top[e] = fmaxf(top[e], s[c + e]);
+      }
+      const float most =
+          fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * p.scale;
+      const bool moves = most > m + kSlack;
+      if (__any_sync(~0u, moves)) {
+        const float factor = moves ? exp2_fast(m - most) : 1.f;
+        if (moves) m = most;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          sum[e].x *= factor;
+          sum[e].y *= factor;
+        }
+        if (k > 0) {
+          if (!warp_wait(&b.pv_done[wg], pv_phase ^ 1, stop)) return false;
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < HD; c += 32) {
+            float o[32];
+            tmem_ld32(o_at + c, o);
+            tmem_wait_ld();
+            uint32_t r[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(o[e] * factor);
+            tmem_st16(o_at + c, r);
+            tmem_st16(o_at + c + 16, r + 16);
+          }
+        }
+      }
+      // 0 where no score is finite; a score of +inf gives NaN
+      const float base = m == -INFINITY  ? 0.f
+                         : m == INFINITY ? __int_as_float(0x7FC00000)
+                                         : m;
+      const float2 scale2 = make_float2(p.scale, p.scale);
+      const float2 base2 = make_float2(shift - base, shift - base);
+#pragma unroll
+      for (int c = 0; c < kUnit; c += 32) {
+        uint32_t w[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const float2 x =
+              fma2(make_float2(s[c + 2 * e], s[c + 2 * e + 1]), scale2, base2);
+          const float2 y = make_float2(exp2_fast(x.x), exp2_fast(x.y));
+          sum[e & 1] = add2(sum[e & 1], y);
+          w[e] = Elem<T>::pack(y.x, y.y);
+        }
+        tmem_st16(s_at + c / 2, w);
+      }
+      tmem_wait_st();
+      // infinities and NaN of V, rarely
+      uint32_t odd[4] = {0, 0, 0, 0}, has[4], none[4];
+      bool any_odd = false;
+      int32_t t0 = 0;
+      if (mixed) {
+        if (!warp_wait(&b.clean[mt.at], mt.phase, stop)) return false;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          odd[w] = meta.odd[w];
+          any_odd |= odd[w] != 0;
+        }
+        if (any_odd) {
+          t0 = meta.t0;
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const uint32_t seen = seen_bits(p, meta, pos, w);
+            has[w] = none[w] = 0;
+            for (uint32_t x = odd[w]; x; x &= x - 1) {
+              const int bit = __ffs(x) - 1;
+              const uint32_t word = tmem_ld1(s_at + w * 16 + bit / 2);
+              tmem_wait_ld();
+              const uint32_t half = bit & 1 ? word >> 16 : word & 0xFFFFu;
+              if ((seen >> bit) & 1) {
+                if (half) has[w] |= 1u << bit; else none[w] |= 1u << bit;
+              }
+            }
+          }
+        }
+      }
+      // A lone tile's last product may still be under way (with two tiles it
+      // ended before this S): a second one behind it would make its phase
+      // of the barrier look like the one before.
+      if (!dual && k > 0 && !warp_wait(&b.pv_done[0], pv_phase ^ 1, stop))
+        return false;
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&b.p_full[bar]);
+      pv_phase ^= 1;
+      if (any_odd) {
+        if (!warp_wait(&b.pv_done[wg], pv_phase ^ 1, stop)) return false;
+        tc_fence_after();
+        add_odd<T, HD>(p, item, t0, odd, has, none, o_at);
+      }
+      mt.next();
+    }
+    // the item's result, or this block's part of it
+    if (!warp_wait(&b.pv_done[wg], pv_phase ^ 1, stop)) return false;
+    tc_fence_after();
+    const float l = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+    if ((item.flags & (kStarts | kEnds)) == (kStarts | kEnds)) {
+      const float inv = l == 0.f ? 0.f : rcp_fast(l);
+      const int64_t n = item.row0 + mine;
+      const int h = item.j * p.group + head;
+      T* out = static_cast<T*>(p.out) + n * p.out_ld + (int64_t)h * HD;
+#pragma unroll 1
+      for (int c = 0; c < HD; c += 32) {
+        float o[32];
+        tmem_ld32(o_at + c, o);
+        tmem_wait_ld();
+        if (valid) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 8)
+            *reinterpret_cast<uint4*>(out + c + e) = make_uint4(
+                Elem<T>::pack(l == 0.f ? 0.f : o[e] * inv,
+                              l == 0.f ? 0.f : o[e + 1] * inv),
+                Elem<T>::pack(l == 0.f ? 0.f : o[e + 2] * inv,
+                              l == 0.f ? 0.f : o[e + 3] * inv),
+                Elem<T>::pack(l == 0.f ? 0.f : o[e + 4] * inv,
+                              l == 0.f ? 0.f : o[e + 5] * inv),
+                Elem<T>::pack(l == 0.f ? 0.f : o[e + 6] * inv,
+                              l == 0.f ? 0.f : o[e + 7] * inv));
+        }
+      }
+      if (valid && p.lse)
+        p.lse[n * p.heads + h] =
+            l == 0.f ? -INFINITY : (m + (log2f(l) - shift)) * kLn2;
+    } else {
+      float* part = p.slots + ((int64_t)(blockIdx.x * 2 +
+                                         (item.flags & kStarts ? 1 : 0)) *
+                                   C::QT + wg) * C::kPart;
+#pragma unroll 1
+      for (int c = 0; c < HD; c += 32) {
+        float o[32];
+        tmem_ld32(o_at + c, o);
+        tmem_wait_ld();
+        if (valid) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            reinterpret_cast<float4*>(part)[(c + e) / 4 * kRows + row] =
+                make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+        }
+      }
+      if (valid) {
+        part[HD * kRows + row] = m;
+        part[HD * kRows + kRows + row] = l;
+      }
+    }
+    // (the next product into O comes after the next arrival at p_full)
+    tc_fence_before();
+  }
+}
+
+// ------------------------------------------------------------------ kernel
+template <class T, int HD>
+__global__ void __launch_bounds__(kThreads, 1)
+    chunk_kernel(const __grid_constant__ ChunkParams p) {
+  using C = Cfg<HD>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  Smem& sm = *reinterpret_cast<Smem*>(smem + C::kMisc);
+  Bars& b = sm.bars;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) {
+    for (int i = 0; i < C::S; ++i) {
+      mbar_init(&b.full[i], 1);
+      mbar_init(&b.empty[i], 1);
+    }
+    mbar_init(&b.q_full, 1);
+    mbar_init(&b.q_empty, 1);
+    for (int i = 0; i < kItems; ++i) {
+      mbar_init(&b.item_full[i], 1);
+      mbar_init(&b.item_empty[i], 10);    // softmax warps, MMA, cleaner
+    }
+    for (int i = 0; i < kMetas; ++i) {
+      mbar_init(&b.meta[i], 1);
+      mbar_init(&b.clean[i], 1);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&b.s_full[i], 1);
+      mbar_init(&b.p_full[i], 4);
+    }
+    mbar_init(&b.pv_done[0], 1);
+    mbar_init(&b.pv_done[1], 1);
+    mbar_init(&b.fin, 1);
+    sm.abort_flag = 0;
+    prefetch_tmap(&p.tm_q);
+    prefetch_tmap(&p.tm_k);
+    prefetch_tmap(&p.tm_v);
+  }
+  fence_mbar_init();
+  // Everything this call reads may come from the launch before it.  (TMEM is
+  // taken behind this wait, too: a block of that launch may need it.)
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (warp == kMma) {
+    tmem_alloc(&sm.tmem, 512);
+    tmem_relinquish();
+  }
+  // costs of the requests, and their sums
+  int64_t* pre = reinterpret_cast<int64_t*>(smem + C::kRing);
+  const int32_t per = C::QT * p.tq;
+  for (int r0 = warp * 32; r0 < p.R; r0 += kThreads) {
+    const Request q(p, r0 + lane);
+    const int items = (q.n + per - 1) / per;
+    int64_t cost = 0;
+    constexpr int kOwn = 4;             // items that a lane sums itself
+    if (items <= kOwn)
+      for (int i = 0; i < items; ++i)
+        cost += item_cost(p, q.n, q.len, i, per);
+    for (uint32_t m = __ballot_sync(~0u, items > kOwn); m; m &= m - 1) {
+      const int l = __ffs(m) - 1;
+      const int32_t n = __shfl_sync(~0u, q.n, l);
+      const int32_t len = __shfl_sync(~0u, q.len, l);
+      int64_t part = 0;
+      for (int i = lane; i < (n + per - 1) / per; i += 32)
+        part += item_cost(p, n, len, i, per);
+#pragma unroll
+      for (int d = 16; d; d >>= 1) part += __shfl_xor_sync(~0u, part, d);
+      if (lane == l) cost = part;
+    }
+    if (r0 + lane < p.R) pre[r0 + lane] = cost * p.kv_heads;
+    if (blockIdx.x == 0 && p.flags && r0 + lane < p.R &&
+        (p.lens[r0 + lane] > p.max_blocks * kBlock ||
+         p.cu[r0 + lane + 1] > p.N))
+      atomicOr(p.flags, KVTC_FLAG_SPACE);
+  }
+  __syncthreads();
+  {
+    const int each = (p.R + kThreads - 1) / kThreads;
+    int64_t sum = 0;
+    for (int i = 0; i < each; ++i) {
+      const int r = tid * each + i;
+      if (r < p.R) sum += pre[r];
+    }
+    int64_t upto = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t o = __shfl_up_sync(~0u, upto, d);
+      if (lane >= d) upto += o;
+    }
+    if (lane == 31) sm.sums[warp] = upto;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) upto += sm.sums[w];
+    int64_t before = upto - sum;
+    for (int i = 0; i < each; ++i) {
+      const int r = tid * each + i;
+      if (r < p.R) {
+        const int64_t cost = pre[r];
+        pre[r] = before;
+        before += cost;
+      }
+    }
+    if (tid == kThreads - 1) pre[p.R] = upto;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const uint32_t tmem = sm.tmem, base = smem_u32(smem);
+  bool ok = true;
+  // The launch gives every thread 168 registers (384 x 168); a row of S takes
+  // 128: 256 x 208 + 128 x 88 is the same number.
+  if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    ok = soften<T, C>(p, sm, tmem, warp);
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (warp == kProducer) {
+      ok = produce<T, C>(p, sm, base, pre);
+    } else if (warp == kMma) {
+      if (lane == 0) {
+        ok = multiply<T, C>(p, sm, base, tmem);
+        // products under way end before the block's memory is given up
+        tc_commit(&b.fin);
+        mbar_drain(&b.fin, 0);
+      }
+      __syncwarp();
+    } else if (warp == kCleaner) {
+      ok = clean<T, C>(p, sm, smem);
+    }
+  }
+  if (!ok) {
+    *(volatile int*)&sm.abort_flag = 1;
+    if (p.flags) atomicOr(p.flags, KVTC_FLAG_TIMEOUT);
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kMma) tmem_dealloc(tmem, 512);
+}
+
+// Parts of items that cross blocks: block x joins the one begun in block x,
+// row tile y, 32 channels z; a thread per row.
+template <class T, int HD>
+__global__ void __launch_bounds__(kRows)
+    chunk_join_kernel(const __grid_constant__ ChunkParams p) {
+  using C = Cfg<HD>;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int c = blockIdx.x, tile = blockIdx.y, ch = blockIdx.z * 32;
+  const JoinDesc d = p.desc[c];
+  if (d.r < 0) return;
+  const int row = threadIdx.x;
+  const int tok = row / p.group, head = row - tok * p.group;
+  const int32_t mine = tile * p.tq + tok;
+  if (tok >= p.tq || mine >= d.ntok) return;
+  auto part_of = [&](int i) {
+    return p.slots +
+           ((int64_t)((c + i) * 2 + (i == 0 ? 1 : 0)) * C::QT + tile) *
+               C::kPart;
+  };
+  const int parts = d.last - c + 1;
+  float m = -INFINITY, l = 0.f, o[32];
+#pragma unroll
+  for (int e = 0; e < 32; ++e) o[e] = 0.f;
+  for (int i = 0; i < parts; ++i) {
+    const float* part = part_of(i);
+    const float mi = part[HD * kRows + row];
+    const float li = part[HD * kRows + kRows + row];
+    float4 x[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      x[e] = reinterpret_cast<const float4*>(part)[(ch / 4 + e) * kRows + row];
+    const float top = fmaxf(m, mi);
+    const float base = top == -INFINITY ? 0.f : top;
+    const float fo = exp2_fast(m - base), fi = exp2_fast(mi - base);
+    m = top;
+    l = l * fo + li * fi;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      o[4 * e] = o[4 * e] * fo + x[e].x * fi;
+      o[4 * e + 1] = o[4 * e + 1] * fo + x[e].y * fi;
+      o[4 * e + 2] = o[4 * e + 2] * fo + x[e].z * fi;
+      o[4 * e + 3] = o[4 * e + 3] * fo + x[e].w * fi;
+    }
+  }
+  const float inv = l == 0.f ? 0.f : rcp_fast(l);
+  const int64_t n = d.row0 + mine;
+  const int h = d.j * p.group + head;
+  T* out = static_cast<T*>(p.out) + n * p.out_ld + (int64_t)h * HD + ch;
+#pragma unroll
+  for (int e = 0; e < 32; e += 8) {
+    uint32_t w[4];
+#pragma unroll
+    for (int f = 0; f < 4; ++f)
+      w[f] = Elem<T>::pack(l == 0.f ? 0.f : o[e + 2 * f] * inv,
+                           l == 0.f ? 0.f : o[e + 2 * f + 1] * inv);
+    *reinterpret_cast<uint4*>(out + e) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  if (p.lse && ch == 0)
+    p.lse[n * p.heads + h] =
+        l == 0.f ? -INFINITY
+                 : (m + (log2f(l) - Elem<T>::kShift)) * kLn2;
 }
 
 inline bool misaligned(const void* p, unsigned bytes) {
   return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0;
 }
 
+template <class T, int HD>
+cudaError_t launch_as(const ChunkParams& p, int device, cudaStream_t st) {
+  using C = Cfg<HD>;
+  static std::atomic<uint64_t> ready;          // devices, as bits
+  const auto kernel = chunk_kernel<T, HD>;
+  cudaError_t e = allow_smem(kernel, C::kBytes, device, ready);
+  if (e == cudaSuccess)
+    e = launch_kernel(kernel, kCtas, kThreads, C::kBytes, st, true, 0, p);
+  if (e != cudaSuccess) return e;
+  count_launch();
+  e = launch_kernel(chunk_join_kernel<T, HD>, dim3(kCtas, C::QT, HD / 32),
+                    kRows, 0, st, true, 0, p);
+  if (e == cudaSuccess) count_launch();
+  return e;
+}
+
 template <class T>
-cudaError_t launch(const ChunkParams& p, int head_dim, cudaStream_t st) {
-  const unsigned grid = (unsigned)std::max<int64_t>(p.N, 1);
-  if (head_dim == 64)
-    return launch_kernel(chunk_simple_kernel<T, 64>, grid, 256, 0, st, false,
-                         0, p);
-  if (head_dim == 128)
-    return launch_kernel(chunk_simple_kernel<T, 128>, grid, 256, 0, st, false,
-                         0, p);
-  return launch_kernel(chunk_simple_kernel<T, 256>, grid, 256, 0, st, false,
-                       0, p);
+cudaError_t launch(const ChunkParams& p, int head_dim, int device,
+                   cudaStream_t st) {
+  return head_dim == 64    ? launch_as<T, 64>(p, device, st)
+         : head_dim == 128 ? launch_as<T, 128>(p, device, st)
+                           : launch_as<T, 256>(p, device, st);
+}
+
+// A pool [num_blocks][16][D] as {64 channels, 16 tokens, D / 64, num_blocks}.
+bool encode_pages(CUtensorMap* m, const void* base, uint64_t D,
+                  uint64_t num_blocks) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return false;
+  cuuint64_t dims[4] = {64, kBlock, D / 64, num_blocks};
+  cuuint64_t strides[3] = {D * 2, 128, D * 2 * kBlock};
+  cuuint32_t box[4] = {64u, (cuuint32_t)kBlock, 1u, 1u};
+  cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base),
+             dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// Rows [N][ld] of `heads` heads as {64 channels, head_dim / 64, heads, N}: a
+// box is 64 channels of the `group` heads of `tokens` rows.
+bool encode_rows(CUtensorMap* m, const void* base, uint64_t head_dim,
+                 uint64_t heads, uint64_t N, uint64_t ld, uint32_t group,
+                 uint32_t tokens) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return false;
+  cuuint64_t dims[4] = {64, head_dim / 64, heads, N};
+  cuuint64_t strides[3] = {128, head_dim * 2, ld * 2};
+  cuuint32_t box[4] = {64u, 1u, group, tokens};
+  cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base),
+             dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+constexpr int64_t kDescBytes =
+    (kCtas * sizeof(JoinDesc) + 255) / 256 * 256;
+template <int HD>
+constexpr int64_t part_bytes() {
+  return 4ll * kCtas * 2 * Cfg<HD>::QT * Cfg<HD>::kPart;
 }
 
 }  // namespace
@@ -155,7 +1355,9 @@ int64_t kvtc_paged_attend_chunks_workspace_bytes(int cuda_device, int R,
   if ((head_dim != 64 && head_dim != 128 && head_dim != 256) ||
       (int64_t)kv_heads * head_dim > kMaxD || heads / kv_heads > kMaxGroup)
     return KVTC_ENOTSUP;
-  return 256;
+  return kDescBytes + (head_dim == 64    ? part_bytes<64>()
+                       : head_dim == 128 ? part_bytes<128>()
+                                         : part_bytes<256>());
 }
 
 int kvtc_paged_attend_chunks(
@@ -189,33 +1391,41 @@ int kvtc_paged_attend_chunks(
   DeviceGuard guard(cuda_device);
   if (!guard.ok) return KVTC_ECUDA;
   ChunkParams p;
-  p.q = q;
-  p.k = k_cache;
-  p.v = v_cache;
+  p.group = heads / kv_heads;
+  p.tq = kRows / p.group;
+  const uint64_t D = (uint64_t)kv_heads * head_dim;
+  if (!encode_pages(&p.tm_k, k_cache, D, num_blocks) ||
+      !encode_pages(&p.tm_v, v_cache, D, num_blocks) ||
+      !encode_rows(&p.tm_q, q, head_dim, heads, N, q_ld, p.group, p.tq))
+    return KVTC_ECUDA;
   p.table = block_table;
   p.cu = cu;
   p.lens = lens;
+  p.v = v_cache;
   p.out = out;
   p.lse = lse;
   p.flags = flags;
+  p.desc = static_cast<JoinDesc*>(workspace);
+  p.slots = reinterpret_cast<float*>(static_cast<char*>(workspace) +
+                                     kDescBytes);
   p.N = N;
-  p.q_ld = q_ld;
   p.out_ld = out_ld;
   p.num_blocks = num_blocks;
-  p.scale = scale;
+  // (the maximum is taken of the products, before the scale)
+  p.pre_on = !(scale > 0.f);
+  p.pre = scale * kLog2e;
+  p.scale = p.pre_on ? 1.f : scale * kLog2e;
   p.R = R;
   p.heads = heads;
   p.kv_heads = kv_heads;
   p.max_blocks = max_blocks;
-  p.sink = sink;
+  p.sink = window ? sink : 0;
   p.window = window;
   cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
   const cudaError_t e = dtype == KVTC_DTYPE_BF16
-                            ? launch<__nv_bfloat16>(p, head_dim, st)
-                            : launch<__half>(p, head_dim, st);
-  if (e != cudaSuccess) return KVTC_ECUDA;
-  count_launch();
-  return KVTC_OK;
+                            ? launch<__nv_bfloat16>(p, head_dim, cuda_device, st)
+                            : launch<__half>(p, head_dim, cuda_device, st);
+  return e == cudaSuccess ? KVTC_OK : KVTC_ECUDA;
 }
 
 }  // extern "C"
