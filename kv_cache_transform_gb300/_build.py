@@ -17,9 +17,10 @@ FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
 SOURCES = ["kvtc_host.cu", "kvtc_kernels.cu", "kvtc_calib.cu",
            "kvtc_static.cu", "kvtc_fieldpack.cu", "kvtc_paged.cu",
            "kvtc_attend.cu", "kvtc_rotate.cu", "kvtc_chunks.cu",
-           "kvtc_evict.cu"]
+           "kvtc_weigh.cu", "kvtc_evict.cu"]
 LIBS = ["-lcusolver"]
-DEPS = SOURCES + ["kvtc_internal.cuh", "kvtc_hostutil.cuh", "ptx.cuh"]
+DEPS = SOURCES + ["kvtc_internal.cuh", "kvtc_hostutil.cuh",
+                  "kvtc_chunk.cuh", "ptx.cuh"]
 
 
 def _nvcc() -> str:

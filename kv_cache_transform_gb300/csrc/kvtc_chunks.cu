@@ -44,6 +44,7 @@
 #include <cstdint>
 
 #include "../../include/kvtc.h"
+#include "kvtc_chunk.cuh"
 #include "kvtc_hostutil.cuh"
 #include "kvtc_internal.cuh"
 #include "ptx.cuh"
@@ -51,17 +52,7 @@
 namespace kvtc {
 namespace {
 
-constexpr int kBlock = 16;           // tokens per pool block (a page)
-constexpr int kMaxReq = 4096;        // requests per call
-constexpr int kMaxGroup = 128;       // query heads per KV head
-constexpr int kMaxTable = INT32_MAX / kBlock - 1;
-constexpr int kCtas = 152;           // one block per SM
-constexpr int kRows = 128;           // rows of a tile (TMEM lanes)
 constexpr int kUnit = 128;           // tokens of a unit
-constexpr int kPages = kUnit / kBlock;
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kMaxScale = 0x1p127f;  // times log2 e still finite
 constexpr float kSlack = 8.f;          // log2
 constexpr int kWarps = 12;            // (the last one only fills its warpgroup)
 constexpr int kProducer = 8, kMma = 9, kCleaner = 10;
@@ -133,99 +124,11 @@ struct __align__(16) Meta {
   uint32_t odd[4];          // tokens whose V held infinities or NaN
 };
 
-// ------------------------------------------------------------ PTX wrappers
-__device__ __forceinline__ void tma_load_4d(uint32_t smem_dst,
-                                            const void* tmap, int32_t x,
-                                            int32_t y, int32_t z, int32_t w,
-                                            uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_"
-      "tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_dst),
-      "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
-      : "memory");
-}
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]),
-      "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]),
-      "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
-}
-__device__ __forceinline__ uint32_t tmem_ld1(uint32_t taddr) {
-  uint32_t r;
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];"
-               : "=r"(r)
-               : "r"(taddr));
-  return r;
-}
-__device__ __forceinline__ float exp2_fast(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-__device__ __forceinline__ float rcp_fast(float x) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-// Two fp32 operations in one instruction.
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  uint64_t d, x = *reinterpret_cast<uint64_t*>(&a),
-              y = *reinterpret_cast<uint64_t*>(&b),
-              z = *reinterpret_cast<uint64_t*>(&c);
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(x), "l"(y), "l"(z));
-  return *reinterpret_cast<float2*>(&d);
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  uint64_t d, x = *reinterpret_cast<uint64_t*>(&a),
-              y = *reinterpret_cast<uint64_t*>(&b);
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(x), "l"(y));
-  return *reinterpret_cast<float2*>(&d);
-}
 // A V tile as the B operand: channels contiguous (64 of them in the swizzle's
 // 128 bytes, the next 64 a slab further on), eight tokens an atom.
 __device__ __forceinline__ uint64_t v_desc(uint32_t smem_addr) {
   return (sw128_desc(smem_addr) & ~((uint64_t)0x3FFF << 16)) |
          ((uint64_t)(kUnit * 128 >> 4) << 16);
-}
-
-template <class T>
-struct Elem;
-template <>
-struct Elem<__nv_bfloat16> {
-  static constexpr uint32_t kFormat = 1;
-  static constexpr float kShift = 0.f;
-  static constexpr uint32_t kExp = 0x7F807F80u, kOne = 0x00800080u;
-  static __device__ __forceinline__ uint32_t pack(float a, float b) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&v);
-  }
-  static __device__ __forceinline__ float2 unpack(uint32_t x) {
-    return make_float2(__uint_as_float(x << 16),
-                       __uint_as_float(x & 0xFFFF0000u));
-  }
-};
-// fp16 holds numbers from 2^-24 to 2^16: weights are formed 2^7 times as
-// large, up to 2^15, and what is lost lies 2^-32 below the largest.
-template <>
-struct Elem<__half> {
-  static constexpr uint32_t kFormat = 0;
-  static constexpr float kShift = 7.f;
-  static constexpr uint32_t kExp = 0x7C007C00u, kOne = 0x04000400u;
-  static __device__ __forceinline__ uint32_t pack(float a, float b) {
-    const __half2 v = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&v);
-  }
-  static __device__ __forceinline__ float2 unpack(uint32_t x) {
-    return __half22float2(*reinterpret_cast<const __half2*>(&x));
-  }
-};
-// Halves of a word that are infinite or NaN, as bits 15 and 31.
-template <class T>
-__device__ __forceinline__ uint32_t odd_of(uint32_t w) {
-  return ((w & Elem<T>::kExp) + Elem<T>::kOne) & 0x80008000u;
 }
 
 // ------------------------------------------------------------------- spans
@@ -249,23 +152,9 @@ struct Span {
     units = max(all - gap, 1);
   }
 };
-// A request's rows and length.
-struct Request {
-  int64_t c0;
-  int32_t n, len;
-  __device__ __forceinline__ Request(const ChunkParams& p, int r) {
-    c0 = 0;
-    n = len = 0;
-    if (r < p.R) {
-      c0 = min(max(p.cu[r], (int64_t)0), p.N);
-      n = (int32_t)max(min(max(p.cu[r + 1], (int64_t)0), p.N) - c0,
-                       (int64_t)0);
-      len = min(max(p.lens[r], 0), p.max_blocks * kBlock);
-    }
-  }
-  __device__ __forceinline__ Request(int64_t c0, int32_t n, int32_t len)
-      : c0(c0), n(n), len(len) {}
-};
+__device__ __forceinline__ Request request(const ChunkParams& p, int r) {
+  return Request(p.cu, p.lens, p.N, p.R, p.max_blocks, r);
+}
 // Cost of item i of a request (per KV head), in units: one more than it has,
 // for the begin and the end.
 __device__ __forceinline__ int64_t item_cost(const ChunkParams& p,
@@ -273,27 +162,6 @@ __device__ __forceinline__ int64_t item_cost(const ChunkParams& p,
                                              int32_t per) {
   const int32_t first = i * per, last = min(first + per, n) - 1;
   return Span(p, len - n + first, len - n + last).units + 1;
-}
-// `total` costs in equal runs over the first `ctas` blocks.
-struct Deal {
-  int64_t least;
-  int32_t more, ctas;
-  __device__ __forceinline__ explicit Deal(int64_t total) {
-    ctas = (int32_t)min((int64_t)kCtas, max(total / 3, (int64_t)1));
-    least = total / ctas;
-    more = (int32_t)(total - least * ctas);
-  }
-  __device__ __forceinline__ int64_t begin(int c) const {
-    return c >= ctas ? least * ctas + more : c * least + min(c, more);
-  }
-  __device__ __forceinline__ int cta_of(int64_t x) const {
-    const int64_t wide = more * (least + 1);
-    return (int)(x < wide ? x / (least + 1) : more + (x - wide) / least);
-  }
-};
-
-__device__ __forceinline__ uint32_t low_bits(int64_t n) {
-  return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << (int)n) - 1u;
 }
 // Which of the tokens t0 + 32 w .. + 31 the row at `pos` attends to.
 __device__ __forceinline__ uint32_t seen_bits(const ChunkParams& p,
@@ -306,19 +174,6 @@ __device__ __forceinline__ uint32_t seen_bits(const ChunkParams& p,
   const uint32_t pages = m.pages >> (2 * w);
   return bits & ((pages & 1 ? 0xFFFFu : 0u) | (pages & 2 ? 0xFFFF0000u : 0u));
 }
-
-// A phase of a ring of N barriers.
-template <int N>
-struct Turn {
-  int at = 0;
-  uint32_t phase = 0;
-  __device__ __forceinline__ void next() {
-    if (++at == N) {
-      at = 0;
-      phase ^= 1;
-    }
-  }
-};
 
 struct Bars {
   uint64_t full[8], empty[8];      // stages
@@ -339,12 +194,6 @@ struct Smem {
 };
 static_assert(sizeof(Smem) <= 1536, "the kernels' shared variables");
 
-// A wait that all lanes leave with the same answer.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity,
-                                          const volatile int* stop) {
-  return __all_sync(~0u, mbar_wait(bar, parity, stop));
-}
-
 // --------------------------------------------------------------- producer
 template <class T, class C>
 __device__ __forceinline__ bool produce(const ChunkParams& p, Smem& sm,
@@ -359,7 +208,7 @@ __device__ __forceinline__ bool produce(const ChunkParams& p, Smem& sm,
   uint32_t q_phase = 0;
   int fills = 0;                       // times that the ring went round
   const int64_t total = pre[p.R];
-  const Deal deal(total);
+  const Deal deal(total, 3);
   int64_t x = deal.begin(blockIdx.x);
   const int64_t end = deal.begin(blockIdx.x + 1);
   const int32_t per = C::QT * p.tq;
@@ -373,7 +222,7 @@ __device__ __forceinline__ bool produce(const ChunkParams& p, Smem& sm,
       if (pre[mid] <= x) lo = mid; else hi = mid;
     }
     r = lo;
-    const Request q(p, r);
+    const Request q = request(p, r);
     const int64_t head = (pre[r + 1] - pre[r]) / p.kv_heads;
     y = x - pre[r];
     j = (int)(y / head);
@@ -405,11 +254,11 @@ __device__ __forceinline__ bool produce(const ChunkParams& p, Smem& sm,
   asm volatile("fence.proxy.async;" ::: "memory");
   bool ok = true, left_desc = false;
   int base = r;                        // requests base .. base + 31
-  Request batch(p, base + lane);
+  Request batch = request(p, base + lane);
   while (x < end && ok) {
     if (r >= base + 32) {
       base = r;
-      batch = Request(p, base + lane);
+      batch = request(p, base + lane);
     }
     const Request q(__shfl_sync(~0u, batch.c0, r - base),
                     __shfl_sync(~0u, batch.n, r - base),
@@ -1119,7 +968,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int64_t* pre = reinterpret_cast<int64_t*>(smem + C::kRing);
   const int32_t per = C::QT * p.tq;
   for (int r0 = warp * 32; r0 < p.R; r0 += kThreads) {
-    const Request q(p, r0 + lane);
+    const Request q = request(p, r0 + lane);
     const int items = (q.n + per - 1) / per;
     int64_t cost = 0;
     constexpr int kOwn = 4;             // items that a lane sums itself
@@ -1273,10 +1122,6 @@ __global__ void __launch_bounds__(kRows)
                  : (m + (log2f(l) - Elem<T>::kShift)) * kLn2;
 }
 
-inline bool misaligned(const void* p, unsigned bytes) {
-  return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0;
-}
-
 template <class T, int HD>
 cudaError_t launch_as(const ChunkParams& p, int device, cudaStream_t st) {
   using C = Cfg<HD>;
@@ -1299,37 +1144,6 @@ cudaError_t launch(const ChunkParams& p, int head_dim, int device,
   return head_dim == 64    ? launch_as<T, 64>(p, device, st)
          : head_dim == 128 ? launch_as<T, 128>(p, device, st)
                            : launch_as<T, 256>(p, device, st);
-}
-
-// A pool [num_blocks][16][D] as {64 channels, 16 tokens, D / 64, num_blocks}.
-bool encode_pages(CUtensorMap* m, const void* base, uint64_t D,
-                  uint64_t num_blocks) {
-  auto enc = tensor_map_encoder();
-  if (!enc) return false;
-  cuuint64_t dims[4] = {64, kBlock, D / 64, num_blocks};
-  cuuint64_t strides[3] = {D * 2, 128, D * 2 * kBlock};
-  cuuint32_t box[4] = {64u, (cuuint32_t)kBlock, 1u, 1u};
-  cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base),
-             dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-// Rows [N][ld] of `heads` heads as {64 channels, head_dim / 64, heads, N}: a
-// box is 64 channels of the `group` heads of `tokens` rows.
-bool encode_rows(CUtensorMap* m, const void* base, uint64_t head_dim,
-                 uint64_t heads, uint64_t N, uint64_t ld, uint32_t group,
-                 uint32_t tokens) {
-  auto enc = tensor_map_encoder();
-  if (!enc) return false;
-  cuuint64_t dims[4] = {64, head_dim / 64, heads, N};
-  cuuint64_t strides[3] = {128, head_dim * 2, ld * 2};
-  cuuint32_t box[4] = {64u, 1u, group, tokens};
-  cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base),
-             dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 constexpr int64_t kDescBytes =

@@ -1,24 +1,14 @@
-// The attention weight that cached tokens receive, and eviction by it.
-//
-// kvtc_paged_weigh: acc[t] = decay acc[t] + sum over rows i and heads h of
-//     e^(scale q_ih . k_t - lse_ih),
-// with the log-sum-exp that the attention of the same rows returned, so K is
-// read once and nothing but the sums is written.
-//
-// kvtc_paged_evict: of a request longer than `keep`, the first `sink`, the
-// last `window` and, of the others, those of the greatest weight stay, in
-// their order.
+// Eviction from paged pools by weights per token: of a request longer than
+// `keep`, the first `sink`, the last `window` and, of the others, those of the
+// greatest weight stay, in their order.
 //   select_kernel  a block per request finds the smallest weight that stays
 //     by its bits, eight at a time (histograms), then lists the tokens in
 //     order by sums over the block, and moves their weights.
 //   move_kernel    rows of all pools by that list.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
 #include <climits>
-#include <cmath>
 #include <cstdint>
 
 #include "../../include/kvtc.h"
@@ -31,83 +21,7 @@ namespace {
 constexpr int kBlock = 16;           // tokens per pool block
 constexpr int kMaxReq = 4096;        // requests per call
 constexpr int kMaxTable = INT32_MAX / kBlock - 1;
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kMaxScale = 0x1p127f;
 
-__device__ __forceinline__ float to_float(__nv_bfloat16 x) {
-  return __bfloat162float(x);
-}
-__device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
-
-// ------------------------------------------------------------------- weigh
-struct WeighParams {
-  const void* q;
-  const void* k;
-  const int32_t* table;
-  const int64_t* cu;
-  const int32_t* lens;
-  const float* lse;
-  const float* acc;
-  float* acc_out;
-  unsigned* flags;
-  int64_t N, q_ld, num_blocks, acc_ld;
-  float scale, decay;
-  int32_t R, heads, kv_heads, max_blocks, sink, window, hd;
-};
-
-// A warp per token: each row and head's product over the warp's lanes.
-template <class T>
-__global__ void __launch_bounds__(256)
-    weigh_simple_kernel(const __grid_constant__ WeighParams p) {
-  const int lane = threadIdx.x & 31;
-  const int r = blockIdx.y;
-  const int64_t most = (int64_t)p.max_blocks * kBlock;
-  const int32_t asked = p.lens[r];
-  const int64_t len = min(max((int64_t)asked, (int64_t)0), most);
-  const int64_t c0 = min(max(p.cu[r], (int64_t)0), p.N);
-  const int64_t c1 = min(max(p.cu[r + 1], (int64_t)0), p.N);
-  if (blockIdx.x == 0 && threadIdx.x == 0 && p.flags &&
-      (asked > most || p.cu[r + 1] > p.N))
-    atomicOr(p.flags, KVTC_FLAG_SPACE);
-  const int64_t n = max(c1 - c0, (int64_t)0);
-  const int group = p.heads / p.kv_heads;
-  const int64_t warp = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-  const int64_t warps = ((int64_t)gridDim.x * blockDim.x) >> 5;
-  for (int64_t t = warp; t < len; t += warps) {
-    const int64_t id = p.table[(int64_t)r * p.max_blocks + t / kBlock];
-    float sum = 0.f;
-    const bool ok = id >= 0 && id < p.num_blocks;
-    bool any = false;
-    for (int64_t i = 0; i < n; ++i) {
-      const int64_t pos = len - n + i;
-      if (t > pos || (p.window && t >= p.sink && t <= pos - p.window))
-        continue;
-      any = true;
-      if (!ok) break;
-      const T* q = static_cast<const T*>(p.q) + (c0 + i) * p.q_ld;
-      const T* k = static_cast<const T*>(p.k) +
-                   (id * kBlock + t % kBlock) * p.kv_heads * p.hd;
-      for (int h = 0; h < p.heads; ++h) {
-        float s = 0.f;
-        for (int c = lane; c < p.hd; c += 32)
-          s = fmaf(to_float(q[h * p.hd + c]),
-                   to_float(k[h / group * p.hd + c]), s);
-#pragma unroll
-        for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(~0u, s, d);
-        const float l = p.lse[(c0 + i) * p.heads + h];
-        if (l != -INFINITY) sum += expf(s * p.scale - l);
-      }
-    }
-    if (lane == 0) {
-      if (any && !ok && p.flags) atomicOr(p.flags, KVTC_FLAG_BLOCK);
-      const int64_t at = r * p.acc_ld + t;
-      p.acc_out[at] =
-          p.decay == 0.f ? sum : fmaf(p.decay, p.acc[at], sum);
-    }
-  }
-}
-
-// ------------------------------------------------------------------- evict
 constexpr int kSelThreads = 1024;
 constexpr int kMaxStreams = 64;      // pools per launch
 
@@ -311,87 +225,6 @@ inline bool misaligned(const void* p, unsigned bytes) {
 using namespace kvtc;
 
 extern "C" {
-
-int64_t kvtc_paged_weigh_workspace_bytes(int cuda_device, int R, int64_t N,
-                                         int heads, int kv_heads,
-                                         int head_dim) {
-  if (cuda_device < 0 || R < 0 || R > kMaxReq || N < 0 || N > INT32_MAX ||
-      heads <= 0 || kv_heads <= 0 || heads % kv_heads || head_dim <= 0)
-    return KVTC_EINVAL;
-  if ((head_dim != 64 && head_dim != 128 && head_dim != 256) ||
-      (int64_t)kv_heads * head_dim > kMaxD || heads / kv_heads > 128)
-    return KVTC_ENOTSUP;
-  return 256;
-}
-
-int kvtc_paged_weigh(int cuda_device, int R, int64_t N, int heads,
-                     int kv_heads, int head_dim, int dtype, const void* q,
-                     int64_t q_ld, const void* k_cache, int64_t num_blocks,
-                     int block_size, const int32_t* block_table,
-                     int max_blocks, const int64_t* cu, const int32_t* lens,
-                     int sink, int window, float scale, const float* lse,
-                     float decay, const float* acc, float* acc_out,
-                     int64_t acc_ld, void* workspace, int64_t workspace_bytes,
-                     uint32_t* flags, void* cuda_stream) {
-  const int64_t need = kvtc_paged_weigh_workspace_bytes(
-      cuda_device, R, N, heads, kv_heads, head_dim);
-  if (need < 0) return (int)need;
-  if ((dtype != KVTC_DTYPE_BF16 && dtype != KVTC_DTYPE_FP16) || !k_cache ||
-      num_blocks <= 0 || num_blocks > INT32_MAX || max_blocks <= 0 ||
-      sink < 0 || window < 0 || !(std::fabs(scale) <= kMaxScale) ||
-      !std::isfinite(decay) || !workspace ||
-      (R && (!block_table || !cu || !lens || !acc_out ||
-             (decay != 0.f && !acc))) ||
-      (R && N && (!q || !lse)))
-    return KVTC_EINVAL;
-  if (block_size != kBlock || max_blocks > kMaxTable) return KVTC_ENOTSUP;
-  if (q_ld < (int64_t)heads * head_dim ||
-      acc_ld < (int64_t)max_blocks * kBlock || workspace_bytes < need)
-    return KVTC_ESIZE;
-  if (q_ld % 8 || acc_ld % 4 || !aligned16(q) || !aligned16(k_cache) ||
-      !aligned16(acc) || !aligned16(acc_out) || !aligned16(workspace) ||
-      misaligned(block_table, 4) || misaligned(cu, 8) ||
-      misaligned(lens, 4) || misaligned(lse, 4) || misaligned(flags, 4))
-    return KVTC_EALIGN;
-  if (R == 0) return KVTC_OK;
-  DeviceGuard guard(cuda_device);
-  if (!guard.ok) return KVTC_ECUDA;
-  WeighParams p;
-  p.q = q;
-  p.k = k_cache;
-  p.table = block_table;
-  p.cu = cu;
-  p.lens = lens;
-  p.lse = lse;
-  p.acc = acc;
-  p.acc_out = acc_out;
-  p.flags = flags;
-  p.N = N;
-  p.q_ld = q_ld;
-  p.num_blocks = num_blocks;
-  p.acc_ld = acc_ld;
-  p.scale = scale;
-  p.decay = decay;
-  p.R = R;
-  p.heads = heads;
-  p.kv_heads = kv_heads;
-  p.max_blocks = max_blocks;
-  p.sink = sink;
-  p.window = window;
-  p.hd = head_dim;
-  const dim3 grid((unsigned)std::min<int64_t>(2 * (int64_t)max_blocks, 512),
-                  R);
-  cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
-  const cudaError_t e =
-      dtype == KVTC_DTYPE_BF16
-          ? launch_kernel(weigh_simple_kernel<__nv_bfloat16>, grid, 256, 0,
-                          st, false, 0, p)
-          : launch_kernel(weigh_simple_kernel<__half>, grid, 256, 0, st,
-                          false, 0, p);
-  if (e != cudaSuccess) return KVTC_ECUDA;
-  count_launch();
-  return KVTC_OK;
-}
 
 int64_t kvtc_paged_evict_workspace_bytes(int R, int max_blocks) {
   if (R < 0 || R > kMaxReq || max_blocks <= 0) return KVTC_EINVAL;
