@@ -20,7 +20,6 @@ constexpr int kMaxGroup = 128;       // query heads per KV head
 constexpr int kMaxTable = INT32_MAX / kBlock - 1;
 constexpr int kCtas = 152;           // one block per SM
 constexpr int kRows = 128;           // rows of a tile (TMEM lanes)
-constexpr int kPages = 128 / kBlock;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kMaxScale = 0x1p127f;  // times log2 e still finite
@@ -166,21 +165,82 @@ struct Turn {
   }
 };
 
-// A wait that all lanes leave with the same answer.
+// The MMA warp runs as one: all lanes compute the same, one of them, the same
+// each time, issues.  Where the operands lie in uniform registers a product of
+// 64 cycles is issued in fewer; out of others each takes 90 to 100.
+template <class I>
+__device__ __forceinline__ I uniform(I x) {
+  return (I)__reduce_max_sync(~0u, (unsigned)x);
+}
+// Shared-memory matrix descriptors as in sw128_desc: the low word of one, with
+// a leading byte offset (of operands whose rows are contiguous), and the high
+// word of all.
+__device__ __forceinline__ uint32_t desc_base(uint32_t smem_addr,
+                                              uint32_t lead = 1) {
+  return uniform(((smem_addr & 0x3FFFFu) >> 4) | lead << 16);
+}
+constexpr uint32_t kDescHigh = (1024u >> 4) | 1u << 14 | 2u << 29;
+__device__ __forceinline__ void mma_ss_one(uint32_t d_tmem, uint32_t a_desc,
+                                           uint32_t b_desc, uint32_t idesc,
+                                           uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\t"
+      "elect.sync _|q, 0xFFFFFFFF;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 a, {%1, %5};\n\t"
+      "mov.b64 b, {%2, %5};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(
+          d_tmem),
+      "r"(a_desc), "r"(b_desc), "r"(idesc), "r"(accumulate), "n"(kDescHigh)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts_one(uint32_t d_tmem, uint32_t a_tmem,
+                                           uint32_t b_desc, uint32_t idesc,
+                                           uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 b;\n\t"
+      "elect.sync _|q, 0xFFFFFFFF;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 b, {%2, %5};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(
+          d_tmem),
+      "r"(a_tmem), "r"(b_desc), "r"(idesc), "r"(accumulate), "n"(kDescHigh)
+      : "memory");
+}
+__device__ __forceinline__ void tc_commit_one(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "elect.sync _|q, 0xFFFFFFFF;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 "
+      "[%0];\n\t}" ::"r"(smem_u32(bar))
+      : "memory");
+}
+
+// A bounded wait (mbar_wait's limit) that the warp goes through as one: every
+// branch is on a vote, so that no lane falls behind the others.  (Lanes that
+// leave a loop one by one stay apart after it, and each product that the MMA
+// warp issues then gathers them again: 330 cycles.)  The lanes may ask for
+// barriers of their own.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity,
                                           const volatile int* stop) {
-  return __all_sync(~0u, mbar_wait(bar, parity, stop));
+  if (__all_sync(~0u, mbar_test_wait(bar, parity))) return true;
+  const uint64_t t0 = globaltimer_ns();
+  for (;;) {
+    if (__all_sync(~0u, mbar_try_wait_sleep(bar, parity, 20000u))) return true;
+    if (__any_sync(~0u, *stop || globaltimer_ns() - t0 > kWaitNs)) return false;
+  }
 }
 
 // ---------------------------------------------------------------- host
-// A pool [num_blocks][16][D] as {64 channels, 16 tokens, D / 64, num_blocks}.
+// A pool [num_blocks][16][D] as {64 channels, 16 tokens, D / 64, num_blocks}:
+// a box is `slabs` times 64 channels of a block.
 bool encode_pages(CUtensorMap* m, const void* base, uint64_t D,
-                  uint64_t num_blocks) {
+                  uint64_t num_blocks, uint32_t slabs) {
   auto enc = tensor_map_encoder();
   if (!enc) return false;
   cuuint64_t dims[4] = {64, kBlock, D / 64, num_blocks};
   cuuint64_t strides[3] = {D * 2, 128, D * 2 * kBlock};
-  cuuint32_t box[4] = {64u, (cuuint32_t)kBlock, 1u, 1u};
+  cuuint32_t box[4] = {64u, (cuuint32_t)kBlock, slabs, 1u};
   cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base),
              dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,

@@ -20,12 +20,9 @@
 //   producer   goes through the run: item descriptors, Q, and the pages of K
 //              and V by TMA into a ring of stages (128 tokens x up to 128
 //              channels each);
-//   MMA        one thread issues S = Q K^T and O += P V (tcgen05, S, P and O
-//              in TMEM, P over the S that it came from);
-//   softmax    two warpgroups, a thread per row.  With two row tiles each has
-//              one, and the tensor cores work on one while the other's
-//              exponentials are formed; with one (few rows, head_dim 256) the
-//              first takes all units, S in two buffers;
+//   MMA        a thread issues S = Q K^T and O += P V (tcgen05, S, P and O in
+//              TMEM, P over the S that it came from);
+//   softmax    two warpgroups, a thread per row;
 //   cleaner    rows of V in units that not every row attends to whole: those
 //              that none attends to are zeroed, and infinities and NaN taken
 //              out of the others (a weight of zero times them would be NaN);
@@ -52,9 +49,8 @@
 namespace kvtc {
 namespace {
 
-constexpr int kUnit = 128;           // tokens of a unit
 constexpr float kSlack = 8.f;          // log2
-constexpr int kWarps = 12;            // (the last one only fills its warpgroup)
+constexpr int kWarps = 12;             // (the last one fills its warpgroup)
 constexpr int kProducer = 8, kMma = 9, kCleaner = 10;
 constexpr int kThreads = kWarps * 32;
 constexpr int kItems = 4, kMetas = 8;  // entries of the rings
@@ -68,7 +64,7 @@ struct __align__(16) JoinDesc {
 
 struct ChunkParams {
   CUtensorMap tm_q;         // {64, HD / 64, heads, N}, box {64, 1, group, tq}
-  CUtensorMap tm_k, tm_v;   // {64, 16, D / 64, num_blocks}, box {64, 16, 1, 1}
+  CUtensorMap tm_k, tm_v;   // {64, 16, D / 64, num_blocks}, box {64, 16, x, 1}
   const int32_t* table;
   const int64_t* cu;
   const int32_t* lens;
@@ -91,16 +87,19 @@ template <int HD_>
 struct Cfg {
   static constexpr int HD = HD_;
   static constexpr int QT = HD == 256 ? 1 : 2;        // row tiles per item
+  static constexpr int kChains = QT;
+  static constexpr int U = HD == 256 ? 64 : 128;      // tokens of a unit
+  static constexpr int kPages = U / kBlock;
   static constexpr int SC = HD < 128 ? HD : 128;      // channels per stage
   static constexpr int NS = HD / SC;                  // stages per K or V tile
   static constexpr int kSlabs = SC / 64;              // per stage
-  static constexpr int kStage = kUnit * SC * 2;
-  static constexpr int S = HD == 64 ? 8 : 5;
+  static constexpr int kStage = U * SC * 2;
+  static constexpr int S = HD == 64 ? 8 : HD == 128 ? 5 : 10;
   static constexpr int kQ = QT * kRows * HD * 2;
   static constexpr int kRing = kQ;
   static constexpr int kMisc = kRing + S * kStage;
-  static constexpr int kBytes = kMisc + 1536 + 1024;  // + alignment slack
-  static_assert(kBytes <= 232448, "shared memory of a block");
+  static constexpr int kBytes = kMisc + 3072;
+  static_assert(kBytes <= 232448 && kMisc % 1024 == 0, "shared memory of a block");
   static_assert(S * kStage >= 8 * (kMaxReq + 1), "prefix of the requests");
   // TMEM columns
   static constexpr int kO = 256;                      // O of tile t: + 128 t
@@ -124,28 +123,22 @@ struct __align__(16) Meta {
   uint32_t odd[4];          // tokens whose V held infinities or NaN
 };
 
-// A V tile as the B operand: channels contiguous (64 of them in the swizzle's
-// 128 bytes, the next 64 a slab further on), eight tokens an atom.
-__device__ __forceinline__ uint64_t v_desc(uint32_t smem_addr) {
-  return (sw128_desc(smem_addr) & ~((uint64_t)0x3FFF << 16)) |
-         ((uint64_t)(kUnit * 128 >> 4) << 16);
-}
-
 // ------------------------------------------------------------------- spans
 // Units of an item whose rows are at positions pf .. pl: `units` of them, the
 // first `front` at their own place, the others `gap` further on.  An item
 // whose rows attend to nothing still has one, which is empty.
+template <int U>
 struct Span {
   int32_t units, front, gap;
   __device__ __forceinline__ Span(const ChunkParams& p, int32_t pf,
                                   int32_t pl) {
-    const int32_t all = pl >= 0 ? pl / kUnit + 1 : 0;
+    const int32_t all = pl >= 0 ? pl / U + 1 : 0;
     front = all;
     gap = 0;
     if (p.window) {
       const int64_t lo = (int64_t)pf - p.window + 1;
-      const int32_t back = lo > 0 ? (int32_t)(lo / kUnit) : 0;
-      front = (int32_t)min(((int64_t)p.sink + kUnit - 1) / kUnit,
+      const int32_t back = lo > 0 ? (int32_t)(lo / U) : 0;
+      front = (int32_t)min(((int64_t)p.sink + U - 1) / U,
                            (int64_t)all);
       gap = max(back - front, 0);
     }
@@ -157,11 +150,12 @@ __device__ __forceinline__ Request request(const ChunkParams& p, int r) {
 }
 // Cost of item i of a request (per KV head), in units: one more than it has,
 // for the begin and the end.
+template <int U>
 __device__ __forceinline__ int64_t item_cost(const ChunkParams& p,
                                              int32_t n, int32_t len, int32_t i,
                                              int32_t per) {
   const int32_t first = i * per, last = min(first + per, n) - 1;
-  return Span(p, len - n + first, len - n + last).units + 1;
+  return Span<U>(p, len - n + first, len - n + last).units + 1;
 }
 // Which of the tokens t0 + 32 w .. + 31 the row at `pos` attends to.
 __device__ __forceinline__ uint32_t seen_bits(const ChunkParams& p,
@@ -176,12 +170,13 @@ __device__ __forceinline__ uint32_t seen_bits(const ChunkParams& p,
 }
 
 struct Bars {
-  uint64_t full[8], empty[8];      // stages
+  uint64_t full[10], empty[10];    // stages
   uint64_t q_full, q_empty;
   uint64_t item_full[kItems], item_empty[kItems];
   uint64_t meta[kMetas], clean[kMetas];       // units
-  uint64_t s_full[4], p_full[4];   // tiles 0, 1; buffers 0, 1 of a lone tile
-  uint64_t pv_done[2], fin;
+  uint64_t s_full[2], p_full[2];              // buffers of S
+  uint64_t pv_done[2], fin;                   // chains
+  uint64_t ready, taken;                      // chain 1's part of a lone tile
 };
 
 struct Smem {
@@ -189,16 +184,18 @@ struct Smem {
   Item items[kItems];
   Meta metas[kMetas];
   int64_t sums[kWarps];
+  float2 lone[kRows];       // m and l of chain 1's part of a lone tile
   uint32_t tmem;
   int abort_flag;
 };
-static_assert(sizeof(Smem) <= 1536, "the kernels' shared variables");
+static_assert(sizeof(Smem) <= 3072, "the kernels' shared variables");
 
 // --------------------------------------------------------------- producer
 template <class T, class C>
 __device__ __forceinline__ bool produce(const ChunkParams& p, Smem& sm,
                                         uint32_t smem, const int64_t* pre) {
-  constexpr int HD = C::HD, NS = C::NS, S = C::S;
+  constexpr int HD = C::HD, NS = C::NS, S = C::S, U = C::U;
+  constexpr int kPages = C::kPages;
   const int lane = (int)lane_id();
   Bars& b = sm.bars;
   volatile int* stop = &sm.abort_flag;
@@ -231,7 +228,7 @@ __device__ __forceinline__ bool produce(const ChunkParams& p, Smem& sm,
     const int items = (q.n + per - 1) / per;
     for (;;) {
       const int64_t cost =
-          i + lane < items ? item_cost(p, q.n, q.len, i + lane, per) : 0;
+          i + lane < items ? item_cost<C::U>(p, q.n, q.len, i + lane, per) : 0;
       int64_t upto = cost;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
@@ -270,7 +267,7 @@ __device__ __forceinline__ bool produce(const ChunkParams& p, Smem& sm,
     }
     const int32_t first = i * per, ntok = min(per, q.n - first);
     const int32_t pf = q.len - q.n + first, pl = pf + ntok - 1;
-    const Span span(p, pf, pl);
+    const Span<U> span(p, pf, pl);
     const int64_t k0 = max(y - 1, (int64_t)0);
     const int64_t k1 = min((int64_t)span.units, y + (end - x) - 1);
     const bool dual = ntok > p.tq;
@@ -309,7 +306,7 @@ __device__ __forceinline__ bool produce(const ChunkParams& p, Smem& sm,
       const int slab_all = j * (HD / 64) + slab;
       auto id_at = [&](int64_t k) -> int32_t {
         const int32_t t0 =
-            (int32_t)(k < span.front ? k : k + span.gap) * kUnit;
+            (int32_t)(k < span.front ? k : k + span.gap) * U;
         const int32_t tp = t0 + page * kBlock;
         const bool need =
             pl >= 0 && tp <= pl &&
@@ -321,7 +318,7 @@ __device__ __forceinline__ bool produce(const ChunkParams& p, Smem& sm,
       for (int64_t k = k0; k < k1 && ok; ++k) {
         const int32_t next_id = k + 1 < k1 ? id_at(k + 1) : 0;
         const int32_t t0 =
-            (int32_t)(k < span.front ? k : k + span.gap) * kUnit;
+            (int32_t)(k < span.front ? k : k + span.gap) * U;
         const bool fine = id >= 0 && id < p.num_blocks;
         const int32_t tp = t0 + page * kBlock;
         // (ids that are not asked for are -2^31; one in the table is bad too)
@@ -329,13 +326,14 @@ __device__ __forceinline__ bool produce(const ChunkParams& p, Smem& sm,
             (!p.window || tp < p.sink ||
              (int64_t)tp + kBlock - 1 > (int64_t)pf - p.window))
           atomicOr(p.flags, KVTC_FLAG_BLOCK);
-        const uint32_t pages = __ballot_sync(~0u, fine) & 0xFFu;
+        const uint32_t pages =
+            __ballot_sync(~0u, fine) & ((1u << kPages) - 1);
         if (lane == 0) {
           Meta m;
           m.t0 = t0;
           m.pages = pages;
-          const int64_t tl = (int64_t)t0 + kUnit - 1;
-          m.mixed = !(pages == 0xFF && tl <= pf &&
+          const int64_t tl = (int64_t)t0 + U - 1;
+          m.mixed = !(pages == (1u << kPages) - 1 && tl <= pf &&
                       (!p.window || tl < p.sink ||
                        (int64_t)t0 > (int64_t)pl - p.window));
           sm.metas[mt.at].t0 = m.t0;
@@ -347,7 +345,6 @@ __device__ __forceinline__ bool produce(const ChunkParams& p, Smem& sm,
         const uint32_t bytes = __popc(pages) * C::kSlabs * 2048;
 #pragma unroll
         for (int kv = 0; kv < 2 && ok; ++kv) {
-          const void* map = kv ? &p.tm_v : &p.tm_k;
 #pragma unroll
           for (int s = 0; s < NS; ++s) {
             if (!warp_wait(&b.empty[st.at], st.phase ^ 1, stop)) {
@@ -356,11 +353,13 @@ __device__ __forceinline__ bool produce(const ChunkParams& p, Smem& sm,
             }
             if (lane == 0) mbar_arrive_expect_tx(&b.full[st.at], bytes);
             __syncwarp();
-            if (fine && slab >= s * C::kSlabs && slab < (s + 1) * C::kSlabs)
-              tma_load_4d(smem + C::kRing + st.at * C::kStage +
-                              (slab - s * C::kSlabs) * (kUnit * 128) +
-                              page * 2048,
-                          map, 0, 0, slab_all, id, &b.full[st.at]);
+            const uint32_t to = smem + C::kRing + st.at * C::kStage;
+            if (kv == 0 && fine && slab / C::kSlabs == s && slab < HD / 64)
+              tma_load_4d(to + slab % C::kSlabs * (U * 128) + page * 2048,
+                          &p.tm_k, 0, 0, slab_all, id, &b.full[st.at]);
+            if (kv == 1 && fine && slab == 0)
+              tma_load_4d(to + page * (C::kSlabs * 2048), &p.tm_v, 0, 0,
+                          slab_all + s * C::kSlabs, id, &b.full[st.at]);
             st.next();
             ++fills;
           }
@@ -427,8 +426,8 @@ __device__ __forceinline__ bool produce(const ChunkParams& p, Smem& sm,
 template <class T, class C>
 __device__ __forceinline__ bool multiply(const ChunkParams& p, Smem& sm,
                                          uint32_t smem, uint32_t tmem) {
-  constexpr int HD = C::HD, NS = C::NS, S = C::S, SC = C::SC;
-  constexpr uint32_t kIdS = make_idesc(kRows, kUnit, Elem<T>::kFormat);
+  constexpr int HD = C::HD, NS = C::NS, S = C::S, SC = C::SC, U = C::U;
+  constexpr uint32_t kIdS = make_idesc(kRows, U, Elem<T>::kFormat);
   // (bit 16: B's rows are contiguous)
   constexpr uint32_t kIdO =
       make_idesc(kRows, SC, Elem<T>::kFormat) | (1u << 16);
@@ -443,56 +442,41 @@ __device__ __forceinline__ bool multiply(const ChunkParams& p, Smem& sm,
 
   // S of tile t into buffer `to`, from the K tile that begins at stage k
   auto qk = [&](int t, int to, Turn<S> k) {
-    const uint32_t d = tmem + to * kUnit;
+    const uint32_t d = tmem + to * 128;
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
-      const uint64_t bd = sw128_desc(ring + k.at * C::kStage);
-      const uint64_t ad = sw128_desc(smem + t * (kRows * HD * 2) +
-                                     s * C::kSlabs * (kRows * 128));
+      const uint32_t bd = desc_base(ring + k.at * C::kStage);
+      const uint32_t ad = desc_base(smem + t * (kRows * HD * 2) +
+                                    s * C::kSlabs * (kRows * 128));
 #pragma unroll
-      for (int e = 0; e < SC / 16; ++e) {
-        const uint32_t off = (e / 4) * (kUnit * 128 >> 4) + (e % 4) * 2;
-        mma_ss(d, ad + off, bd + off, kIdS, (s | e) > 0);
-      }
+      for (int e = 0; e < SC / 16; ++e)
+        mma_ss_one(d, ad + (e / 4) * (kRows * 128 >> 4) + (e % 4) * 2,
+                   bd + (e / 4) * (U * 128 >> 4) + (e % 4) * 2, kIdS,
+                   (s | e) > 0);
       k.next();
     }
+    tc_commit_one(&b.s_full[to]);
   };
-  // O of tile t, from P in buffer `from` and the V tile that begins at v
-  auto pv = [&](int t, int from, Turn<S> v, bool more) {
+  // O of chain c, from P in buffer `from` and the V tile that begins at v
+  auto pv = [&](int c, int from, Turn<S> v, bool more) {
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
-      const uint64_t bd = v_desc(ring + v.at * C::kStage);
-      const uint32_t d = tmem + C::kO + t * 128 + s * SC;
+      // (the next 64 channels lie a slab further on)
+      const uint32_t bd =
+          desc_base(ring + v.at * C::kStage, (uint32_t)(2048 >> 4));
+      const uint32_t d = tmem + C::kO + c * 128 + s * SC;
 #pragma unroll
-      for (int e = 0; e < kUnit / 16; ++e)
-        mma_ts(d, tmem + from * kUnit + e * 8, bd + e * (2048 >> 4), kIdO,
-               more || e > 0);
+      for (int e = 0; e < U / 16; ++e)
+        mma_ts_one(d, tmem + from * 128 + e * 8, bd + e * (C::kSlabs * 2048 >> 4), kIdO,
+                   more || e > 0);
       v.next();
     }
-  };
-  auto wait_k = [&](Turn<S> k) {
-#pragma unroll
-    for (int s = 0; s < NS; ++s) {
-      if (!mbar_wait(&b.full[k.at], k.phase, stop)) return false;
-      k.next();
-    }
-    return true;
-  };
-  auto wait_v = [&] {
-    const bool ok = mbar_wait(&b.clean[mt.at], mt.phase, stop);
-    mt.next();
-    return ok;
-  };
-  auto wait_p = [&](int i) {
-    const bool ok = mbar_wait(&b.p_full[i], (p_phase >> i) & 1, stop);
-    p_phase ^= 1u << i;
-    tc_fence_after();
-    return ok;
+    tc_commit_one(&b.pv_done[c]);
   };
   auto release = [&](Turn<S> k) {
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
-      tc_commit(&b.empty[k.at]);
+      tc_commit_one(&b.empty[k.at]);
       k.next();
     }
   };
@@ -500,71 +484,98 @@ __device__ __forceinline__ bool multiply(const ChunkParams& p, Smem& sm,
     for (int s = 0; s < stages; ++s) k.next();
     return k;
   };
-  for (;;) {
-    if (!mbar_wait(&b.item_full[it.at], it.phase, stop)) return false;
-    const int units = sm.items[it.at].units;
-    const bool dual = sm.items[it.at].flags & kDual;
-    if (units == 0) return true;
-    if (!mbar_wait(&b.q_full, q_phase, stop)) return false;
-    q_phase ^= 1;
-    // stages of unit k: K at st + 2 NS k, V NS further on
-    if (!wait_k(st)) return false;
+  // A barrier's wait costs 60 cycles even where nothing is waited for: lanes
+  // ask for different ones at once.
+  const int lane = (int)lane_id();
+  auto wait_k = [&](Turn<S> k) {
+    for (int s = 0; s < lane % NS; ++s) k.next();
+    const bool ok = warp_wait(&b.full[k.at], k.phase, stop);
     tc_fence_after();
+    return ok;
+  };
+  auto wait_p = [&](int i) {
+    const bool ok = warp_wait(&b.p_full[i], (p_phase >> i) & 1, stop);
+    p_phase ^= 1u << i;
+    tc_fence_after();
+    __syncwarp();
+    return ok;
+  };
+  // P in buffer i, the unit's V and, where `more`, K at `next`
+  auto wait_pvk = [&](int i, bool more, Turn<S> next) {
+    for (int s = 0; s < lane / 4 % NS; ++s) next.next();
+    bool ok = warp_wait(&b.clean[mt.at], mt.phase, stop);
+    if (more) ok = ok && warp_wait(&b.full[next.at], next.phase, stop);
+    ok = ok && warp_wait(&b.p_full[i], (p_phase >> i) & 1, stop);
+    p_phase ^= 1u << i;
+    mt.next();
+    tc_fence_after();
+    __syncwarp();
+    return ok;
+  };
+  for (;;) {
+    if (!warp_wait(&b.item_full[it.at], it.phase, stop)) return false;
+    const int units = uniform(sm.items[it.at].units);
+    const bool dual = uniform(sm.items[it.at].flags) & kDual;
+    if (units == 0) return true;
+    if (!warp_wait(&b.q_full, q_phase, stop)) return false;
+    q_phase ^= 1;
+    // Stages of a unit: K at st, V NS further on.  The S of a step is formed
+    // as soon as the product with the P that lay in its buffer has been issued.
+    if (!wait_k(st)) return false;
     if (dual) {
       qk(0, 0, st);
-      tc_commit(&b.s_full[0]);
       qk(1, 1, st);
-      tc_commit(&b.s_full[1]);
       release(st);
-      if (units == 1) tc_commit(&b.q_empty);
+      if (units == 1) tc_commit_one(&b.q_empty);
+#pragma unroll 1
       for (int k = 0; k < units; ++k) {
-        const Turn<S> v = ahead(st, NS), next = ahead(st, 2 * NS);
+        const Turn<S> v = ahead(st, NS), next = ahead(v, NS);
         const bool more = k + 1 < units;
-        if (!wait_v() || !wait_p(0)) return false;
+        if (!wait_pvk(0, more, next)) return false;
         pv(0, 0, v, k > 0);
-        tc_commit(&b.pv_done[0]);
-        if (more) {
-          if (!wait_k(next)) return false;
-          tc_fence_after();
-          qk(0, 0, next);
-          tc_commit(&b.s_full[0]);
-        }
+        if (more) qk(0, 0, next);
         if (!wait_p(1)) return false;
         pv(1, 1, v, k > 0);
-        tc_commit(&b.pv_done[1]);
         release(v);
         if (more) {
           qk(1, 1, next);
-          tc_commit(&b.s_full[1]);
           release(next);
-          if (k + 2 == units) tc_commit(&b.q_empty);
+          if (k + 2 == units) tc_commit_one(&b.q_empty);
         }
         st = next;
       }
     } else {
+      // a lone tile: units in the two buffers (and with two chains to the two
+      // O) in turn
       qk(0, 0, st);
-      tc_commit(&b.s_full[2]);
       release(st);
-      if (units == 1) tc_commit(&b.q_empty);
+      if (units == 1) tc_commit_one(&b.q_empty);
+      if (units > 1) {
+        const Turn<S> next = ahead(st, 2 * NS);
+        if (!wait_k(next)) return false;
+        qk(0, 1, next);
+        release(next);
+        if (units == 2) tc_commit_one(&b.q_empty);
+      }
+#pragma unroll 1
       for (int k = 0; k < units; ++k) {
-        const Turn<S> v = ahead(st, NS), next = ahead(st, 2 * NS);
-        if (k + 1 < units) {
-          // the other buffer's P went into its product before this one's S
-          if (!wait_k(next)) return false;
-          tc_fence_after();
-          qk(0, (k + 1) & 1, next);
-          tc_commit(&b.s_full[2 + ((k + 1) & 1)]);
-          release(next);
-          if (k + 2 == units) tc_commit(&b.q_empty);
-        }
-        if (!wait_v() || !wait_p(2 + (k & 1))) return false;
-        pv(0, k & 1, v, k > 0);
-        tc_commit(&b.pv_done[0]);
+        const int buf = k & 1;
+        const Turn<S> v = ahead(st, NS);
+        if (!wait_pvk(buf, false, v)) return false;
+        pv(C::kChains == 2 ? buf : 0, buf, v, k >= C::kChains);
         release(v);
-        st = next;
+        if (k + 2 < units) {
+          const Turn<S> next = ahead(st, 4 * NS);
+          if (!wait_k(next)) return false;
+          qk(0, buf, next);
+          release(next);
+          if (k + 3 == units) tc_commit_one(&b.q_empty);
+        }
+        st = ahead(st, 2 * NS);
       }
     }
-    mbar_arrive(&b.item_empty[it.at]);
+    __syncwarp();
+    if (lane_id() == 0) mbar_arrive(&b.item_empty[it.at]);
     it.next();
   }
 }
@@ -573,7 +584,7 @@ __device__ __forceinline__ bool multiply(const ChunkParams& p, Smem& sm,
 template <class T, class C>
 __device__ __forceinline__ bool clean(const ChunkParams& p, Smem& sm,
                                       uint8_t* smem) {
-  constexpr int NS = C::NS, S = C::S;
+  constexpr int NS = C::NS, S = C::S, U = C::U;
   const int lane = (int)lane_id();
   Bars& b = sm.bars;
   volatile int* stop = &sm.abort_flag;
@@ -603,7 +614,7 @@ __device__ __forceinline__ bool clean(const ChunkParams& p, Smem& sm,
           uint8_t* tile = smem + C::kRing + st.at * C::kStage;
           // four tokens at a time, eight lanes each
 #pragma unroll 1
-          for (int g = 0; g < kUnit / 4; ++g) {
+          for (int g = 0; g < U / 4; ++g) {
             const int row = g * 4 + lane / 8;
             const int64_t t = (int64_t)t0 + row;
             const bool none =
@@ -616,7 +627,8 @@ __device__ __forceinline__ bool clean(const ChunkParams& p, Smem& sm,
 #pragma unroll
             for (int sl = 0; sl < C::kSlabs; ++sl) {
               uint4* at = reinterpret_cast<uint4*>(
-                  tile + sl * (kUnit * 128) + row * 128 + (lane % 8) * 16);
+                  tile + (row / kBlock * C::kSlabs + sl) * 2048 +
+                  row % kBlock * 128 + (lane % 8) * 16);
               if (none) {
                 *at = make_uint4(0, 0, 0, 0);
               } else if (!every) {
@@ -707,7 +719,7 @@ __device__ __noinline__ void add_odd(const ChunkParams& p, const Item& item,
 template <class T, class C>
 __device__ __forceinline__ bool soften(const ChunkParams& p, Smem& sm,
                                        uint32_t tmem, int warp) {
-  constexpr int HD = C::HD;
+  constexpr int HD = C::HD, U = C::U;
   const int lane = (int)lane_id(), wg = warp >> 2;
   const int row = (warp & 3) * 32 + lane;
   const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);
@@ -718,6 +730,7 @@ __device__ __forceinline__ bool soften(const ChunkParams& p, Smem& sm,
   Turn<kMetas> mt;
   uint32_t s_phase = 0;          // a bit per barrier
   uint32_t pv_phase = 0;         // of the next product
+  uint32_t lone_phase = 0;
   const float shift = Elem<T>::kShift;
   const int tok = row / p.group, head = row - tok * p.group;
   for (;;) {
@@ -728,36 +741,35 @@ __device__ __forceinline__ bool soften(const ChunkParams& p, Smem& sm,
     it.next();
     if (item.units == 0) return true;
     const bool dual = item.flags & kDual;
-    if (wg && !dual) {           // not this warpgroup's
-      for (int k = 0; k < item.units; ++k) mt.next();
-      continue;
-    }
-    const int32_t mine = wg * p.tq + tok;         // the row's token
+    // of a lone tile every second unit is this chain's
+    const bool lone = C::kChains == 2 && !dual;
+    const int32_t mine = (dual ? wg * p.tq : 0) + tok;    // the row's token
     const int64_t pos = (int64_t)item.pf + mine;
     const bool valid = tok < p.tq && mine < item.ntok;
     float m = -INFINITY;
     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-    for (int k = 0; k < item.units; ++k) {
-      const int buf = dual ? wg : k & 1;
-      const int bar = dual ? wg : 2 + buf;
-      const uint32_t s_at = lanes + buf * kUnit;
+    bool first = true;
+    for (int k = 0; k < item.units; ++k, mt.next()) {
+      if (lone && (k & 1) != wg) continue;
+      const int bar = C::kChains == 1 ? k & 1 : wg;
+      const uint32_t s_at = lanes + bar * 128;
       if (!warp_wait(&b.meta[mt.at], mt.phase, stop)) return false;
       if (!warp_wait(&b.s_full[bar], (s_phase >> bar) & 1, stop)) return false;
       s_phase ^= 1u << bar;
       tc_fence_after();
       const Meta& meta = sm.metas[mt.at];
       const bool mixed = meta.mixed;
-      float s[kUnit];
+      float s[U];
 #pragma unroll
-      for (int c = 0; c < kUnit; c += 32) tmem_ld32(s_at + c, s + c);
+      for (int c = 0; c < U; c += 32) tmem_ld32(s_at + c, s + c);
       tmem_wait_ld();
       if (p.pre_on) {
 #pragma unroll
-        for (int c = 0; c < kUnit; ++c) s[c] *= p.pre;
+        for (int c = 0; c < U; ++c) s[c] *= p.pre;
       }
       if (mixed) {
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
+        for (int w = 0; w < U / 32; ++w) {
           const uint32_t seen = seen_bits(p, meta, pos, w);
 #pragma unroll
           for (int c = 0; c < 32; ++c)
@@ -766,10 +778,13 @@ __device__ __forceinline__ bool soften(const ChunkParams& p, Smem& sm,
       }
       float top[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-      for (int c = 4; c < kUnit; c += 4) {
+      for (int c = 4; c + 8 <= U; c += 8) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) top[e] = fmaxf(top[e], s[c + e]);
+        for (int e = 0; e < 4; ++e)
+          top[e] = fmaxf(fmaxf(top[e], s[c + 2 * e]), s[c + 2 * e + 1]);
       }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) top[e] = fmaxf(top[e], s[U - 4 + e]);
       const float most =
           fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * p.scale;
       const bool moves = most > m + kSlack;
@@ -781,7 +796,7 @@ __device__ __forceinline__ bool soften(const ChunkParams& p, Smem& sm,
           sum[e].x *= factor;
           sum[e].y *= factor;
         }
-        if (k > 0) {
+        if (!first) {
           if (!warp_wait(&b.pv_done[wg], pv_phase ^ 1, stop)) return false;
           tc_fence_after();
 #pragma unroll 1
@@ -804,7 +819,7 @@ __device__ __forceinline__ bool soften(const ChunkParams& p, Smem& sm,
       const float2 scale2 = make_float2(p.scale, p.scale);
       const float2 base2 = make_float2(shift - base, shift - base);
 #pragma unroll
-      for (int c = 0; c < kUnit; c += 32) {
+      for (int c = 0; c < U; c += 32) {
         uint32_t w[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
@@ -846,11 +861,13 @@ __device__ __forceinline__ bool soften(const ChunkParams& p, Smem& sm,
           }
         }
       }
-      // A lone tile's last product may still be under way (with two tiles it
-      // ended before this S): a second one behind it would make its phase
-      // of the barrier look like the one before.
-      if (!dual && k > 0 && !warp_wait(&b.pv_done[0], pv_phase ^ 1, stop))
+      // With one chain the last product may still be under way (with two it
+      // ended before this S): a second one behind it would make its phase of
+      // the barrier look like the one before.
+      if (C::kChains == 1 && !first &&
+          !warp_wait(&b.pv_done[0], pv_phase ^ 1, stop))
         return false;
+      first = false;
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&b.p_full[bar]);
@@ -860,12 +877,54 @@ __device__ __forceinline__ bool soften(const ChunkParams& p, Smem& sm,
         tc_fence_after();
         add_odd<T, HD>(p, item, t0, odd, has, none, o_at);
       }
-      mt.next();
     }
     // the item's result, or this block's part of it
+    if (first) continue;         // (a lone tile's only unit was chain 0's)
     if (!warp_wait(&b.pv_done[wg], pv_phase ^ 1, stop)) return false;
     tc_fence_after();
-    const float l = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+    float l = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+    const bool joins = lone && item.units > 1;
+    float mine_f = 1.f, their_f = 0.f;
+    if (joins && wg) {
+      sm.lone[row] = make_float2(m, l);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&b.ready);
+      // (O of this chain is read by the other)
+      if (!warp_wait(&b.taken, lone_phase, stop)) return false;
+      lone_phase ^= 1;
+      tc_fence_after();
+      continue;
+    }
+    if (joins) {
+      if (!warp_wait(&b.ready, lone_phase, stop)) return false;
+      lone_phase ^= 1;
+      tc_fence_after();
+      const float2 their = sm.lone[row];
+      const float top = fmaxf(m, their.x);
+      const float base = top == -INFINITY ? 0.f : top;
+      mine_f = exp2_fast(m - base);
+      their_f = exp2_fast(their.x - base);
+      m = top;
+      l = l * mine_f + their.y * their_f;
+    }
+    // 32 channels of O, with the other chain's part of them
+    const auto load_o = [&](int c, float (&o)[32]) {
+      tmem_ld32(o_at + c, o);
+      tmem_wait_ld();
+      if (joins) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          float x[16];
+          tmem_ld16(o_at + 128 + c + 16 * half, x);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            o[16 * half + e] =
+                o[16 * half + e] * mine_f + x[e] * their_f;
+        }
+      }
+    };
     if ((item.flags & (kStarts | kEnds)) == (kStarts | kEnds)) {
       const float inv = l == 0.f ? 0.f : rcp_fast(l);
       const int64_t n = item.row0 + mine;
@@ -874,8 +933,7 @@ __device__ __forceinline__ bool soften(const ChunkParams& p, Smem& sm,
 #pragma unroll 1
       for (int c = 0; c < HD; c += 32) {
         float o[32];
-        tmem_ld32(o_at + c, o);
-        tmem_wait_ld();
+        load_o(c, o);
         if (valid) {
 #pragma unroll
           for (int e = 0; e < 32; e += 8)
@@ -900,8 +958,7 @@ __device__ __forceinline__ bool soften(const ChunkParams& p, Smem& sm,
 #pragma unroll 1
       for (int c = 0; c < HD; c += 32) {
         float o[32];
-        tmem_ld32(o_at + c, o);
-        tmem_wait_ld();
+        load_o(c, o);
         if (valid) {
 #pragma unroll
           for (int e = 0; e < 32; e += 4)
@@ -916,6 +973,10 @@ __device__ __forceinline__ bool soften(const ChunkParams& p, Smem& sm,
     }
     // (the next product into O comes after the next arrival at p_full)
     tc_fence_before();
+    if (joins) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&b.taken);
+    }
   }
 }
 
@@ -924,8 +985,7 @@ template <class T, int HD>
 __global__ void __launch_bounds__(kThreads, 1)
     chunk_kernel(const __grid_constant__ ChunkParams p) {
   using C = Cfg<HD>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  extern __shared__ __align__(1024) uint8_t smem[];
   Smem& sm = *reinterpret_cast<Smem*>(smem + C::kMisc);
   Bars& b = sm.bars;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -938,19 +998,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&b.q_empty, 1);
     for (int i = 0; i < kItems; ++i) {
       mbar_init(&b.item_full[i], 1);
-      mbar_init(&b.item_empty[i], 10);    // softmax warps, MMA, cleaner
+      mbar_init(&b.item_empty[i], 4 * C::kChains + 2);  // (MMA, cleaner)
     }
     for (int i = 0; i < kMetas; ++i) {
       mbar_init(&b.meta[i], 1);
       mbar_init(&b.clean[i], 1);
     }
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2; ++i) {
       mbar_init(&b.s_full[i], 1);
       mbar_init(&b.p_full[i], 4);
+      mbar_init(&b.pv_done[i], 1);
     }
-    mbar_init(&b.pv_done[0], 1);
-    mbar_init(&b.pv_done[1], 1);
     mbar_init(&b.fin, 1);
+    mbar_init(&b.ready, 4);
+    mbar_init(&b.taken, 4);
     sm.abort_flag = 0;
     prefetch_tmap(&p.tm_q);
     prefetch_tmap(&p.tm_k);
@@ -974,14 +1035,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int kOwn = 4;             // items that a lane sums itself
     if (items <= kOwn)
       for (int i = 0; i < items; ++i)
-        cost += item_cost(p, q.n, q.len, i, per);
+        cost += item_cost<C::U>(p, q.n, q.len, i, per);
     for (uint32_t m = __ballot_sync(~0u, items > kOwn); m; m &= m - 1) {
       const int l = __ffs(m) - 1;
       const int32_t n = __shfl_sync(~0u, q.n, l);
       const int32_t len = __shfl_sync(~0u, q.len, l);
       int64_t part = 0;
       for (int i = lane; i < (n + per - 1) / per; i += 32)
-        part += item_cost(p, n, len, i, per);
+        part += item_cost<C::U>(p, n, len, i, per);
 #pragma unroll
       for (int d = 16; d; d >>= 1) part += __shfl_xor_sync(~0u, part, d);
       if (lane == l) cost = part;
@@ -1030,18 +1091,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   // 128: 256 x 208 + 128 x 88 is the same number.
   if (warp < 8) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-    ok = soften<T, C>(p, sm, tmem, warp);
+    if (warp < 4 * C::kChains) ok = soften<T, C>(p, sm, tmem, warp);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == kProducer) {
       ok = produce<T, C>(p, sm, base, pre);
     } else if (warp == kMma) {
-      if (lane == 0) {
-        ok = multiply<T, C>(p, sm, base, tmem);
-        // products under way end before the block's memory is given up
-        tc_commit(&b.fin);
-        mbar_drain(&b.fin, 0);
-      }
+      ok = multiply<T, C>(p, sm, base, uniform(tmem));
+      // products under way end before the block's memory is given up
+      __syncwarp();
+      tc_commit_one(&b.fin);
+      mbar_drain(&b.fin, 0);
       __syncwarp();
     } else if (warp == kCleaner) {
       ok = clean<T, C>(p, sm, smem);
@@ -1208,8 +1268,9 @@ int kvtc_paged_attend_chunks(
   p.group = heads / kv_heads;
   p.tq = kRows / p.group;
   const uint64_t D = (uint64_t)kv_heads * head_dim;
-  if (!encode_pages(&p.tm_k, k_cache, D, num_blocks) ||
-      !encode_pages(&p.tm_v, v_cache, D, num_blocks) ||
+  if (!encode_pages(&p.tm_k, k_cache, D, num_blocks, 1) ||
+      !encode_pages(&p.tm_v, v_cache, D, num_blocks,
+                    head_dim == 64 ? 1 : 2) ||
       !encode_rows(&p.tm_q, q, head_dim, heads, N, q_ld, p.group, p.tq))
     return KVTC_ECUDA;
   p.table = block_table;

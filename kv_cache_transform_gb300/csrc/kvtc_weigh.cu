@@ -779,7 +779,7 @@ int kvtc_paged_weigh(int cuda_device, int R, int64_t N, int heads,
   p.group = heads / kv_heads;
   p.tq = kCols / p.group;
   if (!encode_pages(&p.tm_k, k_cache, (uint64_t)kv_heads * head_dim,
-                    num_blocks))
+                    num_blocks, 1))
     return KVTC_ECUDA;
   // (without rows no box is read: their maps are never made)
   for (int i = 0; N && i < kBoxes; ++i) {
