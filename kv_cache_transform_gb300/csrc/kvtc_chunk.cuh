@@ -221,14 +221,16 @@ __device__ __forceinline__ void tc_commit_one(uint64_t* bar) {
 // leave a loop one by one stay apart after it, and each product that the MMA
 // warp issues then gathers them again: 330 cycles.)  The lanes may ask for
 // barriers of their own.
+// (Kept short: the kernels' code competes for the instruction cache.)
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity,
                                           const volatile int* stop) {
-  if (__all_sync(~0u, mbar_test_wait(bar, parity))) return true;
-  const uint64_t t0 = globaltimer_ns();
-  for (;;) {
-    if (__all_sync(~0u, mbar_try_wait_sleep(bar, parity, 20000u))) return true;
-    if (__any_sync(~0u, *stop || globaltimer_ns() - t0 > kWaitNs)) return false;
-  }
+  const uint32_t t0 = (uint32_t)globaltimer_ns();
+#pragma unroll 1
+  while (!__all_sync(~0u, mbar_try_wait_sleep(bar, parity, 20000u)))
+    if (__any_sync(~0u, *stop ||
+                            (uint32_t)globaltimer_ns() - t0 > kWaitNs))
+      return false;
+  return true;
 }
 
 // ---------------------------------------------------------------- host

@@ -50,6 +50,11 @@ namespace kvtc {
 namespace {
 
 constexpr float kSlack = 8.f;          // log2
+// What an item's begin and end cost, in units: the first S, the last P V, O, and
+// units that are attended in part.  (With 1, 2, 4 and 8 a prompt of 8192 tokens
+// takes 505, 475, 424 and 439 us, 64 chunks up to 256 tokens 266, 238, 219 and
+// 230.)
+constexpr int kItemCost = 4;
 constexpr int kWarps = 12;             // (the last one fills its warpgroup)
 constexpr int kProducer = 8, kMma = 9, kCleaner = 10;
 constexpr int kThreads = kWarps * 32;
@@ -76,9 +81,8 @@ struct ChunkParams {
   float* slots;             // [kCtas][2] parts: 0 of an item begun in an
                             // earlier block, 1 of one begun in this block
   int64_t N, out_ld, num_blocks;
-  float scale;              // times log2 e; positive, else as pre
-  float pre;                // where pre_on: scores are multiplied by it first
-  int32_t pre_on;
+  float scale;              // its magnitude, times log2 e; never 0
+  int32_t negate;           // a negative scale: S is formed with -Q
   int32_t R, heads, kv_heads, max_blocks, sink, window;
   int32_t group, tq;        // query heads a KV head; tokens per row tile
 };
@@ -148,14 +152,13 @@ struct Span {
 __device__ __forceinline__ Request request(const ChunkParams& p, int r) {
   return Request(p.cu, p.lens, p.N, p.R, p.max_blocks, r);
 }
-// Cost of item i of a request (per KV head), in units: one more than it has,
-// for the begin and the end.
+// Cost of item i of a request (per KV head), in units.
 template <int U>
-__device__ __forceinline__ int64_t item_cost(const ChunkParams& p,
+__device__ __noinline__ int64_t item_cost(const ChunkParams& p,
                                              int32_t n, int32_t len, int32_t i,
                                              int32_t per) {
   const int32_t first = i * per, last = min(first + per, n) - 1;
-  return Span<U>(p, len - n + first, len - n + last).units + 1;
+  return Span<U>(p, len - n + first, len - n + last).units + kItemCost;
 }
 // Which of the tokens t0 + 32 w .. + 31 the row at `pos` attends to.
 __device__ __forceinline__ uint32_t seen_bits(const ChunkParams& p,
@@ -205,7 +208,7 @@ __device__ __forceinline__ bool produce(const ChunkParams& p, Smem& sm,
   uint32_t q_phase = 0;
   int fills = 0;                       // times that the ring went round
   const int64_t total = pre[p.R];
-  const Deal deal(total, 3);
+  const Deal deal(total, kItemCost + 2);
   int64_t x = deal.begin(blockIdx.x);
   const int64_t end = deal.begin(blockIdx.x + 1);
   const int32_t per = C::QT * p.tq;
@@ -268,8 +271,8 @@ __device__ __forceinline__ bool produce(const ChunkParams& p, Smem& sm,
     const int32_t first = i * per, ntok = min(per, q.n - first);
     const int32_t pf = q.len - q.n + first, pl = pf + ntok - 1;
     const Span<U> span(p, pf, pl);
-    const int64_t k0 = max(y - 1, (int64_t)0);
-    const int64_t k1 = min((int64_t)span.units, y + (end - x) - 1);
+    const int64_t k0 = max(y - kItemCost, (int64_t)0);
+    const int64_t k1 = min((int64_t)span.units, y + (end - x) - kItemCost);
     const bool dual = ntok > p.tq;
     if (k1 > k0) {
       if (!warp_wait(&b.item_empty[it.at], it.phase ^ 1, stop)) {
@@ -294,7 +297,7 @@ __device__ __forceinline__ bool produce(const ChunkParams& p, Smem& sm,
           jd.r = r;
           jd.j = j;
           jd.ntok = ntok;
-          jd.last = deal.cta_of(x - y + span.units);
+          jd.last = deal.cta_of(x - y + kItemCost + span.units - 1);
           p.desc[blockIdx.x] = jd;
           left_desc = true;
         }
@@ -386,7 +389,7 @@ __device__ __forceinline__ bool produce(const ChunkParams& p, Smem& sm,
         }
       }
     }
-    const int64_t step = min((int64_t)span.units + 1 - y, end - x);
+    const int64_t step = min((int64_t)span.units + kItemCost - y, end - x);
     x += step;
     y = 0;
     if (++i == items) {
@@ -427,91 +430,22 @@ template <class T, class C>
 __device__ __forceinline__ bool multiply(const ChunkParams& p, Smem& sm,
                                          uint32_t smem, uint32_t tmem) {
   constexpr int HD = C::HD, NS = C::NS, S = C::S, SC = C::SC, U = C::U;
-  constexpr uint32_t kIdS = make_idesc(kRows, U, Elem<T>::kFormat);
+  // (bit 13: A is negated)
+  const uint32_t id_s =
+      make_idesc(kRows, U, Elem<T>::kFormat) | (p.negate ? 1u << 13 : 0u);
   // (bit 16: B's rows are contiguous)
   constexpr uint32_t kIdO =
       make_idesc(kRows, SC, Elem<T>::kFormat) | (1u << 16);
   Bars& b = sm.bars;
   volatile int* stop = &sm.abort_flag;
-  Turn<S> st;                    // the unit's first stage
+  Turn<S> kt, vt;                // the next tile's first stage
   Turn<kItems> it;
   Turn<kMetas> mt;
   uint32_t q_phase = 0;
   uint32_t p_phase = 0;          // a bit per barrier
   const uint32_t ring = smem + C::kRing;
+  for (int s = 0; s < NS; ++s) vt.next();
 
-  // S of tile t into buffer `to`, from the K tile that begins at stage k
-  auto qk = [&](int t, int to, Turn<S> k) {
-    const uint32_t d = tmem + to * 128;
-#pragma unroll
-    for (int s = 0; s < NS; ++s) {
-      const uint32_t bd = desc_base(ring + k.at * C::kStage);
-      const uint32_t ad = desc_base(smem + t * (kRows * HD * 2) +
-                                    s * C::kSlabs * (kRows * 128));
-#pragma unroll
-      for (int e = 0; e < SC / 16; ++e)
-        mma_ss_one(d, ad + (e / 4) * (kRows * 128 >> 4) + (e % 4) * 2,
-                   bd + (e / 4) * (U * 128 >> 4) + (e % 4) * 2, kIdS,
-                   (s | e) > 0);
-      k.next();
-    }
-    tc_commit_one(&b.s_full[to]);
-  };
-  // O of chain c, from P in buffer `from` and the V tile that begins at v
-  auto pv = [&](int c, int from, Turn<S> v, bool more) {
-#pragma unroll
-    for (int s = 0; s < NS; ++s) {
-      // (the next 64 channels lie a slab further on)
-      const uint32_t bd =
-          desc_base(ring + v.at * C::kStage, (uint32_t)(2048 >> 4));
-      const uint32_t d = tmem + C::kO + c * 128 + s * SC;
-#pragma unroll
-      for (int e = 0; e < U / 16; ++e)
-        mma_ts_one(d, tmem + from * 128 + e * 8, bd + e * (C::kSlabs * 2048 >> 4), kIdO,
-                   more || e > 0);
-      v.next();
-    }
-    tc_commit_one(&b.pv_done[c]);
-  };
-  auto release = [&](Turn<S> k) {
-#pragma unroll
-    for (int s = 0; s < NS; ++s) {
-      tc_commit_one(&b.empty[k.at]);
-      k.next();
-    }
-  };
-  auto ahead = [&](Turn<S> k, int stages) {
-    for (int s = 0; s < stages; ++s) k.next();
-    return k;
-  };
-  // A barrier's wait costs 60 cycles even where nothing is waited for: lanes
-  // ask for different ones at once.
-  const int lane = (int)lane_id();
-  auto wait_k = [&](Turn<S> k) {
-    for (int s = 0; s < lane % NS; ++s) k.next();
-    const bool ok = warp_wait(&b.full[k.at], k.phase, stop);
-    tc_fence_after();
-    return ok;
-  };
-  auto wait_p = [&](int i) {
-    const bool ok = warp_wait(&b.p_full[i], (p_phase >> i) & 1, stop);
-    p_phase ^= 1u << i;
-    tc_fence_after();
-    __syncwarp();
-    return ok;
-  };
-  // P in buffer i, the unit's V and, where `more`, K at `next`
-  auto wait_pvk = [&](int i, bool more, Turn<S> next) {
-    for (int s = 0; s < lane / 4 % NS; ++s) next.next();
-    bool ok = warp_wait(&b.clean[mt.at], mt.phase, stop);
-    if (more) ok = ok && warp_wait(&b.full[next.at], next.phase, stop);
-    ok = ok && warp_wait(&b.p_full[i], (p_phase >> i) & 1, stop);
-    p_phase ^= 1u << i;
-    mt.next();
-    tc_fence_after();
-    __syncwarp();
-    return ok;
-  };
   for (;;) {
     if (!warp_wait(&b.item_full[it.at], it.phase, stop)) return false;
     const int units = uniform(sm.items[it.at].units);
@@ -519,59 +453,77 @@ __device__ __forceinline__ bool multiply(const ChunkParams& p, Smem& sm,
     if (units == 0) return true;
     if (!warp_wait(&b.q_full, q_phase, stop)) return false;
     q_phase ^= 1;
-    // Stages of a unit: K at st, V NS further on.  The S of a step is formed
-    // as soon as the product with the P that lay in its buffer has been issued.
-    if (!wait_k(st)) return false;
-    if (dual) {
-      qk(0, 0, st);
-      qk(1, 1, st);
-      release(st);
-      if (units == 1) tc_commit_one(&b.q_empty);
+    // Steps: a unit for each row tile in turn, or one unit after the other for
+    // a lone tile; S, P (and with two chains O) of step n in buffer n & 1.  The
+    // S of a step is formed as soon as the product with the P that lay in its
+    // buffer has been issued.  (One place for each product, and loops that are
+    // not unrolled: the code has to stay in the instruction cache.)
+    const int steps = dual ? 2 * units : units;
 #pragma unroll 1
-      for (int k = 0; k < units; ++k) {
-        const Turn<S> v = ahead(st, NS), next = ahead(v, NS);
-        const bool more = k + 1 < units;
-        if (!wait_pvk(0, more, next)) return false;
-        pv(0, 0, v, k > 0);
-        if (more) qk(0, 0, next);
-        if (!wait_p(1)) return false;
-        pv(1, 1, v, k > 0);
-        release(v);
-        if (more) {
-          qk(1, 1, next);
-          release(next);
-          if (k + 2 == units) tc_commit_one(&b.q_empty);
+    for (int n = 0; n < steps + 2; ++n) {
+      const int buf = n & 1;
+      const bool begins = !dual || buf == 0, ends = !dual || buf == 1;
+      if (n >= 2) {
+        // O += P V of step n - 2
+        if (begins) {
+          if (!warp_wait(&b.clean[mt.at], mt.phase, stop)) return false;
+          mt.next();
         }
-        st = next;
-      }
-    } else {
-      // a lone tile: units in the two buffers (and with two chains to the two
-      // O) in turn
-      qk(0, 0, st);
-      release(st);
-      if (units == 1) tc_commit_one(&b.q_empty);
-      if (units > 1) {
-        const Turn<S> next = ahead(st, 2 * NS);
-        if (!wait_k(next)) return false;
-        qk(0, 1, next);
-        release(next);
-        if (units == 2) tc_commit_one(&b.q_empty);
-      }
+        if (!warp_wait(&b.p_full[buf], p_phase >> buf & 1, stop)) return false;
+        p_phase ^= 1u << buf;
+        tc_fence_after();
+        const int chain = C::kChains == 2 ? buf : 0;
+        Turn<S> v = vt;
 #pragma unroll 1
-      for (int k = 0; k < units; ++k) {
-        const int buf = k & 1;
-        const Turn<S> v = ahead(st, NS);
-        if (!wait_pvk(buf, false, v)) return false;
-        pv(C::kChains == 2 ? buf : 0, buf, v, k >= C::kChains);
-        release(v);
-        if (k + 2 < units) {
-          const Turn<S> next = ahead(st, 4 * NS);
-          if (!wait_k(next)) return false;
-          qk(0, buf, next);
-          release(next);
-          if (k + 3 == units) tc_commit_one(&b.q_empty);
+        for (int s = 0; s < NS; ++s) {
+          // (the next 64 channels lie a slab further on)
+          const uint32_t bd =
+              desc_base(ring + v.at * C::kStage, (uint32_t)(2048 >> 4));
+          const uint32_t d = tmem + C::kO + chain * 128 + s * SC;
+          const uint32_t a = tmem + buf * 128;
+#pragma unroll
+          for (int e = 0; e < U / 16; ++e)
+            mma_ts_one(d, a + e * 8, bd + e * (C::kSlabs * 2048 >> 4), kIdO,
+                       n - 2 >= C::kChains || e > 0);
+          v.next();
         }
-        st = ahead(st, 2 * NS);
+        tc_commit_one(&b.pv_done[chain]);
+        if (ends) {
+          for (int s = 0; s < NS; ++s) {
+            tc_commit_one(&b.empty[vt.at]);
+            vt.next();
+          }
+          for (int s = 0; s < NS; ++s) vt.next();     // (K's stages)
+        }
+      }
+      if (n < steps) {
+        // S of step n
+        Turn<S> k = kt;
+#pragma unroll 1
+        for (int s = 0; s < NS; ++s) {
+          if (begins && !warp_wait(&b.full[k.at], k.phase, stop)) return false;
+          tc_fence_after();
+          const uint32_t bd = desc_base(ring + k.at * C::kStage);
+          const uint32_t ad = desc_base(smem + (dual ? buf : 0) *
+                                                   (kRows * HD * 2) +
+                                        s * C::kSlabs * (kRows * 128));
+          const uint32_t d = tmem + buf * 128;
+#pragma unroll
+          for (int e = 0; e < SC / 16; ++e)
+            mma_ss_one(d, ad + (e / 4) * (kRows * 128 >> 4) + (e % 4) * 2,
+                       bd + (e / 4) * (U * 128 >> 4) + (e % 4) * 2, id_s,
+                       (s | e) > 0);
+          k.next();
+        }
+        tc_commit_one(&b.s_full[buf]);
+        if (ends) {
+          for (int s = 0; s < NS; ++s) {
+            tc_commit_one(&b.empty[kt.at]);
+            kt.next();
+          }
+          for (int s = 0; s < NS; ++s) kt.next();     // (V's stages)
+        }
+        if (n + 1 == steps) tc_commit_one(&b.q_empty);
       }
     }
     __syncwarp();
@@ -674,6 +626,28 @@ __device__ __forceinline__ bool clean(const ChunkParams& p, Smem& sm,
 }
 
 // ---------------------------------------------------------------- softmax
+// Of a unit's tokens whose V held infinities or NaN, those that this row
+// attends to with a weight above 0 and with one of 0.
+__device__ __noinline__ void find_odd(const ChunkParams& p, const Meta& meta,
+                                      int64_t pos, uint32_t s_at,
+                                      uint32_t (&has)[4],
+                                      uint32_t (&none)[4]) {
+#pragma unroll 1
+  for (int w = 0; w < 4; ++w) {
+    const uint32_t seen = seen_bits(p, meta, pos, w);
+    has[w] = none[w] = 0;
+#pragma unroll 1
+    for (uint32_t x = meta.odd[w]; x; x &= x - 1) {
+      const int bit = __ffs(x) - 1;
+      const uint32_t word = tmem_ld1(s_at + w * 16 + bit / 2);
+      tmem_wait_ld();
+      const uint32_t half = bit & 1 ? word >> 16 : word & 0xFFFFu;
+      if ((seen >> bit) & 1) {
+        if (half) has[w] |= 1u << bit; else none[w] |= 1u << bit;
+      }
+    }
+  }
+}
 // Infinities and NaN that the cleaner took out of V, for the rows that attend
 // to them: v times the row's weight, added to O behind the unit's product.
 // `has`: tokens of the unit that this row attends to with a weight above 0,
@@ -712,6 +686,38 @@ __device__ __noinline__ void add_odd(const ChunkParams& p, const Item& item,
         tmem_st16(o + c, r);
         tmem_wait_st();
       }
+    }
+  }
+}
+
+template <int N>
+__device__ __forceinline__ float row_max(const float (&s)[N]) {
+  float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+  for (int c = 0; c < N; c += 8) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      top[e] = fmaxf(fmaxf(top[e], s[c + 2 * e]), s[c + 2 * e + 1]);
+  }
+  return fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+}
+// Four rows' 64 bytes each, a row a lane, to four pieces of 16 bytes a lane:
+// piece lane % 4 of the four rows, so that a store covers 64 bytes of a row.
+__device__ __forceinline__ void transpose4(uint4 (&v)[4], int lane) {
+#pragma unroll
+  for (int d = 1; d <= 2; d <<= 1) {
+    const bool up = lane & d;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      uint4& a = v[d == 1 ? 2 * k : k];
+      uint4& z = v[d == 1 ? 2 * k + 1 : k + 2];
+      const uint4 give = up ? a : z;
+      uint4 get;
+      get.x = __shfl_xor_sync(~0u, give.x, d);
+      get.y = __shfl_xor_sync(~0u, give.y, d);
+      get.z = __shfl_xor_sync(~0u, give.z, d);
+      get.w = __shfl_xor_sync(~0u, give.w, d);
+      if (up) a = get; else z = get;
     }
   }
 }
@@ -763,32 +769,48 @@ __device__ __forceinline__ bool soften(const ChunkParams& p, Smem& sm,
 #pragma unroll
       for (int c = 0; c < U; c += 32) tmem_ld32(s_at + c, s + c);
       tmem_wait_ld();
-      if (p.pre_on) {
-#pragma unroll
-        for (int c = 0; c < U; ++c) s[c] *= p.pre;
-      }
       if (mixed) {
 #pragma unroll
         for (int w = 0; w < U / 32; ++w) {
           const uint32_t seen = seen_bits(p, meta, pos, w);
+          if (__all_sync(~0u, seen == ~0u)) continue;
 #pragma unroll
           for (int c = 0; c < 32; ++c)
             if (!((seen >> c) & 1)) s[w * 32 + c] = -INFINITY;
         }
       }
-      float top[4] = {s[0], s[1], s[2], s[3]};
+      // A unit's weights are formed with the reference as it stands, beside
+      // its maximum; the rare unit that moves the reference is gone through
+      // again.  (The maximum first: 250 cycles more from S to P.)
+      if (first) m = row_max(s) * p.scale;
+      float2 part[2];
+#pragma unroll 1
+      for (;;) {
+        // 0 where no score is finite; a score of +inf gives NaN
+        const float base = m == -INFINITY  ? 0.f
+                           : m == INFINITY ? __int_as_float(0x7FC00000)
+                                           : m;
+        const float2 scale2 = make_float2(p.scale, p.scale);
+        const float2 base2 = make_float2(shift - base, shift - base);
+        part[0] = part[1] = make_float2(0.f, 0.f);
+        float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-      for (int c = 4; c + 8 <= U; c += 8) {
+        for (int c = 0; c < U; c += 32) {
+          uint32_t w[16];
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          top[e] = fmaxf(fmaxf(top[e], s[c + 2 * e]), s[c + 2 * e + 1]);
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) top[e] = fmaxf(top[e], s[U - 4 + e]);
-      const float most =
-          fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * p.scale;
-      const bool moves = most > m + kSlack;
-      if (__any_sync(~0u, moves)) {
+          for (int e = 0; e < 16; ++e) {
+            const float a = s[c + 2 * e], z = s[c + 2 * e + 1];
+            const float2 x = fma2(make_float2(a, z), scale2, base2);
+            const float2 y = make_float2(exp2_fast(x.x), exp2_fast(x.y));
+            top[e & 1] = fmaxf(fmaxf(top[e & 1], a), z);
+            part[e & 1] = add2(part[e & 1], y);
+            w[e] = Elem<T>::pack(y.x, y.y);
+          }
+          tmem_st16(s_at + c / 2, w);
+        }
+        const float most = fmaxf(top[0], top[1]) * p.scale;
+        const bool moves = most > m + kSlack;
+        if (!__any_sync(~0u, moves)) break;
         const float factor = moves ? exp2_fast(m - most) : 1.f;
         if (moves) m = most;
 #pragma unroll
@@ -800,37 +822,19 @@ __device__ __forceinline__ bool soften(const ChunkParams& p, Smem& sm,
           if (!warp_wait(&b.pv_done[wg], pv_phase ^ 1, stop)) return false;
           tc_fence_after();
 #pragma unroll 1
-          for (int c = 0; c < HD; c += 32) {
-            float o[32];
-            tmem_ld32(o_at + c, o);
+          for (int c = 0; c < HD; c += 16) {
+            float o[16];
+            tmem_ld16(o_at + c, o);
             tmem_wait_ld();
-            uint32_t r[32];
+            uint32_t r[16];
 #pragma unroll
-            for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(o[e] * factor);
+            for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(o[e] * factor);
             tmem_st16(o_at + c, r);
-            tmem_st16(o_at + c + 16, r + 16);
           }
         }
       }
-      // 0 where no score is finite; a score of +inf gives NaN
-      const float base = m == -INFINITY  ? 0.f
-                         : m == INFINITY ? __int_as_float(0x7FC00000)
-                                         : m;
-      const float2 scale2 = make_float2(p.scale, p.scale);
-      const float2 base2 = make_float2(shift - base, shift - base);
-#pragma unroll
-      for (int c = 0; c < U; c += 32) {
-        uint32_t w[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const float2 x =
-              fma2(make_float2(s[c + 2 * e], s[c + 2 * e + 1]), scale2, base2);
-          const float2 y = make_float2(exp2_fast(x.x), exp2_fast(x.y));
-          sum[e & 1] = add2(sum[e & 1], y);
-          w[e] = Elem<T>::pack(y.x, y.y);
-        }
-        tmem_st16(s_at + c / 2, w);
-      }
+      sum[0] = add2(sum[0], part[0]);
+      sum[1] = add2(sum[1], part[1]);
       tmem_wait_st();
       // infinities and NaN of V, rarely
       uint32_t odd[4] = {0, 0, 0, 0}, has[4], none[4];
@@ -845,20 +849,7 @@ __device__ __forceinline__ bool soften(const ChunkParams& p, Smem& sm,
         }
         if (any_odd) {
           t0 = meta.t0;
-#pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            const uint32_t seen = seen_bits(p, meta, pos, w);
-            has[w] = none[w] = 0;
-            for (uint32_t x = odd[w]; x; x &= x - 1) {
-              const int bit = __ffs(x) - 1;
-              const uint32_t word = tmem_ld1(s_at + w * 16 + bit / 2);
-              tmem_wait_ld();
-              const uint32_t half = bit & 1 ? word >> 16 : word & 0xFFFFu;
-              if ((seen >> bit) & 1) {
-                if (half) has[w] |= 1u << bit; else none[w] |= 1u << bit;
-              }
-            }
-          }
+          find_odd(p, meta, pos, s_at, has, none);
         }
       }
       // With one chain the last product may still be under way (with two it
@@ -908,68 +899,61 @@ __device__ __forceinline__ bool soften(const ChunkParams& p, Smem& sm,
       m = top;
       l = l * mine_f + their.y * their_f;
     }
-    // 32 channels of O, with the other chain's part of them
-    const auto load_o = [&](int c, float (&o)[32]) {
+    const bool whole =
+        (item.flags & (kStarts | kEnds)) == (kStarts | kEnds);
+    const float inv = l == 0.f ? 0.f : rcp_fast(l);
+    const int64_t n = item.row0 + mine;
+    const int h = item.j * p.group + head;
+    T* out = static_cast<T*>(p.out) + lane % 4 * 8;
+    // where the rows of this lane's four go
+    const int64_t to = valid ? n * p.out_ld + (int64_t)h * HD : -1;
+    int64_t at[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) at[e] = __shfl_sync(~0u, to, (lane & ~3) + e);
+    float* part = p.slots + ((int64_t)(blockIdx.x * 2 +
+                                       (item.flags & kStarts ? 1 : 0)) *
+                                 C::QT + wg) * C::kPart;
+#pragma unroll 1
+    for (int c = 0; c < HD; c += 32) {
+      float o[32];
       tmem_ld32(o_at + c, o);
       tmem_wait_ld();
-      if (joins) {
+      if (joins) {             // with the other chain's part
+        float x[32];
+        tmem_ld32(o_at + 128 + c, x);
+        tmem_wait_ld();
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          float x[16];
-          tmem_ld16(o_at + 128 + c + 16 * half, x);
-          tmem_wait_ld();
+        for (int e = 0; e < 32; ++e) o[e] = o[e] * mine_f + x[e] * their_f;
+      }
+      if (whole) {
+        uint4 v[4];
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
-            o[16 * half + e] =
-                o[16 * half + e] * mine_f + x[e] * their_f;
+        for (int e = 0; e < 4; ++e) {
+          uint32_t w[4];
+#pragma unroll
+          for (int f = 0; f < 4; ++f)
+            w[f] = Elem<T>::pack(
+                l == 0.f ? 0.f : o[8 * e + 2 * f] * inv,
+                l == 0.f ? 0.f : o[8 * e + 2 * f + 1] * inv);
+          v[e] = make_uint4(w[0], w[1], w[2], w[3]);
         }
-      }
-    };
-    if ((item.flags & (kStarts | kEnds)) == (kStarts | kEnds)) {
-      const float inv = l == 0.f ? 0.f : rcp_fast(l);
-      const int64_t n = item.row0 + mine;
-      const int h = item.j * p.group + head;
-      T* out = static_cast<T*>(p.out) + n * p.out_ld + (int64_t)h * HD;
-#pragma unroll 1
-      for (int c = 0; c < HD; c += 32) {
-        float o[32];
-        load_o(c, o);
-        if (valid) {
+        transpose4(v, lane);
 #pragma unroll
-          for (int e = 0; e < 32; e += 8)
-            *reinterpret_cast<uint4*>(out + c + e) = make_uint4(
-                Elem<T>::pack(l == 0.f ? 0.f : o[e] * inv,
-                              l == 0.f ? 0.f : o[e + 1] * inv),
-                Elem<T>::pack(l == 0.f ? 0.f : o[e + 2] * inv,
-                              l == 0.f ? 0.f : o[e + 3] * inv),
-                Elem<T>::pack(l == 0.f ? 0.f : o[e + 4] * inv,
-                              l == 0.f ? 0.f : o[e + 5] * inv),
-                Elem<T>::pack(l == 0.f ? 0.f : o[e + 6] * inv,
-                              l == 0.f ? 0.f : o[e + 7] * inv));
-        }
-      }
-      if (valid && p.lse)
-        p.lse[n * p.heads + h] =
-            l == 0.f ? -INFINITY : (m + (log2f(l) - shift)) * kLn2;
-    } else {
-      float* part = p.slots + ((int64_t)(blockIdx.x * 2 +
-                                         (item.flags & kStarts ? 1 : 0)) *
-                                   C::QT + wg) * C::kPart;
-#pragma unroll 1
-      for (int c = 0; c < HD; c += 32) {
-        float o[32];
-        load_o(c, o);
-        if (valid) {
+        for (int e = 0; e < 4; ++e)
+          if (at[e] >= 0) *reinterpret_cast<uint4*>(out + at[e] + c) = v[e];
+      } else if (valid) {
 #pragma unroll
-          for (int e = 0; e < 32; e += 4)
-            reinterpret_cast<float4*>(part)[(c + e) / 4 * kRows + row] =
-                make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-        }
+        for (int e = 0; e < 32; e += 4)
+          reinterpret_cast<float4*>(part)[(c + e) / 4 * kRows + row] =
+              make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
       }
-      if (valid) {
-        part[HD * kRows + row] = m;
-        part[HD * kRows + kRows + row] = l;
-      }
+    }
+    if (valid && whole && p.lse)
+      p.lse[n * p.heads + h] =
+          l == 0.f ? -INFINITY : (m + (log2f(l) - shift)) * kLn2;
+    if (valid && !whole) {
+      part[HD * kRows + row] = m;
+      part[HD * kRows + kRows + row] = l;
     }
     // (the next product into O comes after the next arrival at p_full)
     tc_fence_before();
@@ -1286,10 +1270,10 @@ int kvtc_paged_attend_chunks(
   p.N = N;
   p.out_ld = out_ld;
   p.num_blocks = num_blocks;
-  // (the maximum is taken of the products, before the scale)
-  p.pre_on = !(scale > 0.f);
-  p.pre = scale * kLog2e;
-  p.scale = p.pre_on ? 1.f : scale * kLog2e;
+  // (the maximum is taken of the products, before the scale; that of 0 is the
+  // smallest number, so that -inf stays what it is for tokens left out)
+  p.negate = scale < 0.f;
+  p.scale = std::max(std::fabs(scale) * kLog2e, 0x1p-149f);
   p.R = R;
   p.heads = heads;
   p.kv_heads = kv_heads;
