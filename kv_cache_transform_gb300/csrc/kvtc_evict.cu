@@ -24,6 +24,7 @@ constexpr int kMaxTable = INT32_MAX / kBlock - 1;
 
 constexpr int kSelThreads = 1024;
 constexpr int kMaxStreams = 64;      // pools per launch
+constexpr int kBins = 2048;          // weights are told apart 11 bits at a time
 
 struct EvictParams {
   const float* acc;
@@ -50,42 +51,40 @@ __device__ __forceinline__ uint32_t key_of(float x) {
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-// Exclusive sums of a and b over the block's threads; totals in ta and tb.
-__device__ __forceinline__ void block_sums2(int& a, int& b, int* ta, int* tb,
-                                            int2* sums) {
+// Exclusive sums of a over the block's threads (a may hold two counts, of 32
+// bits each); the total in *all.
+__device__ __forceinline__ uint64_t block_sums(uint64_t a, uint64_t* all,
+                                               uint64_t* sums) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int a0 = a, b0 = b;
+  uint64_t upto = a;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const int x = __shfl_up_sync(~0u, a, d), y = __shfl_up_sync(~0u, b, d);
-    if (lane >= d) {
-      a += x;
-      b += y;
-    }
+    const uint64_t x = __shfl_up_sync(~0u, upto, d);
+    if (lane >= d) upto += x;
   }
+  if (lane == 31) sums[warp] = upto;
   __syncthreads();
-  if (lane == 31) sums[warp] = make_int2(a, b);
-  __syncthreads();
-  const int2 w = sums[lane];          // (32 warps)
-  int xa = lane < warp ? w.x : 0, xb = lane < warp ? w.y : 0;
-  int sa = w.x, sb = w.y;
+  const uint64_t w = sums[lane];              // (32 warps)
+  uint64_t before = lane < warp ? w : 0, total = w;
 #pragma unroll
   for (int d = 16; d; d >>= 1) {
-    xa += __shfl_xor_sync(~0u, xa, d);
-    xb += __shfl_xor_sync(~0u, xb, d);
-    sa += __shfl_xor_sync(~0u, sa, d);
-    sb += __shfl_xor_sync(~0u, sb, d);
+    before += __shfl_xor_sync(~0u, before, d);
+    total += __shfl_xor_sync(~0u, total, d);
   }
-  a += xa - a0;
-  b += xb - b0;
-  *ta = sa;
-  *tb = sb;
+  __syncthreads();
+  *all = total;
+  return upto - a + before;
 }
 
+// A block per request.  The smallest key that stays is found from the top, 11
+// bits a round: a histogram of those that agree so far, and its sums from above.
+// Then the tokens that stay are listed in order, four tokens a thread at a time.
+// (One thread that goes through the bins, 8 bits a round, and one token a
+// thread: 27 us where 64 requests up to 4K go to 1K, 70 for one of 32K.)
 __global__ void __launch_bounds__(kSelThreads)
     select_kernel(const __grid_constant__ EvictParams p) {
-  __shared__ int hist[256];
-  __shared__ int2 sums[32];
+  __shared__ int hist[kBins];
+  __shared__ uint64_t sums[32];
   __shared__ int pick[2];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -104,23 +103,40 @@ __global__ void __launch_bounds__(kSelThreads)
   const int32_t hi = len > p.keep ? len - p.window : len;
   const int32_t want = len > p.keep ? p.keep - p.sink - p.window : 0;
   // the smallest key that stays, and how many of those equal to it
-  uint32_t least = 0;
+  uint32_t least = want ? 0u : ~0u;
   int equal = want;
-  if (len > p.keep) {
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      if (tid < 256) hist[tid] = 0;
+  if (want) {
+    for (int round = 0; round < 3; ++round) {
+      const int shift = round == 0 ? 21 : round == 1 ? 10 : 0;
+      const int bits = round == 2 ? 10 : 11;
+      const uint32_t known = round == 0 ? 0u : ~0u << (shift + bits);
+      for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
       __syncthreads();
-      const uint32_t above = shift == 24 ? 0u : ~0u << (shift + 8);
-      for (int32_t t = lo + tid; t < hi; t += kSelThreads) {
-        const uint32_t key = key_of(acc[t]);
-        if ((key & above) == least) atomicAdd(&hist[(key >> shift) & 255], 1);
+      constexpr int kAhead = 8;
+      for (int32_t t0 = lo + tid; t0 < hi; t0 += kAhead * kSelThreads) {
+        float w[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+          w[i] = t0 + i * kSelThreads < hi ? acc[t0 + i * kSelThreads] : 0.f;
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          const uint32_t key = key_of(w[i]);
+          if (t0 + i * kSelThreads < hi && (key & known) == least)
+            atomicAdd(&hist[(key >> shift) & ((1u << bits) - 1)], 1);
+        }
       }
       __syncthreads();
-      if (tid == 0) {
-        int left = equal, b = 255;
-        while (b > 0 && hist[b] < left) left -= hist[b--];
-        pick[0] = b;
-        pick[1] = left;
+      // thread t: bins 2047 - 2 t and 2046 - 2 t; sums from the largest
+      const int b1 = kBins - 1 - 2 * tid, b0 = b1 - 1;
+      const int n1 = hist[b1], n0 = hist[b0];
+      uint64_t all;
+      const int above = (int)block_sums((uint64_t)(n0 + n1), &all, sums);
+      if (above < equal && above + n1 >= equal) {
+        pick[0] = b1;
+        pick[1] = equal - above;
+      } else if (above + n1 < equal && above + n1 + n0 >= equal) {
+        pick[0] = b0;
+        pick[1] = equal - above - n1;
       }
       __syncthreads();
       least |= (uint32_t)pick[0] << shift;
@@ -128,43 +144,57 @@ __global__ void __launch_bounds__(kSelThreads)
       __syncthreads();
     }
   }
-  // the list, a stretch of tokens at a time
-  int above = 0, same = 0;      // before this stretch
+  // the list: of a thread's four tokens those above `least`, and of those equal
+  // to it the first ones
+  uint32_t gone_above = 0, gone_same = 0;      // before this stretch
   int32_t* kept = p.kept + r * (int64_t)p.keep;
   int32_t* ids = p.ids + r * (int64_t)most;
   float* acc_out = p.acc_out + r * p.acc_ld;
   bool bad = false;
-  for (int32_t t0 = 0; t0 < len; t0 += kSelThreads) {
-    const int32_t t = t0 + tid;
-    float w = 0.f;
-    int is_above = 0, is_same = 0, stays = 0;
-    if (t < len) {
-      w = acc[t];
-      if (t >= lo && t < hi) {
-        const uint32_t key = key_of(w);
-        is_above = key > least;
-        is_same = key == least;
+  for (int32_t t0 = 0; t0 < len; t0 += 4 * kSelThreads) {
+    const int32_t t = t0 + 4 * tid;
+    // (rows of acc are as long as the table, a multiple of 16)
+    const float4 w4 = t < len ? *reinterpret_cast<const float4*>(acc + t)
+                              : make_float4(0.f, 0.f, 0.f, 0.f);
+    const float w[4] = {w4.x, w4.y, w4.z, w4.w};
+    uint64_t count = 0;
+    uint32_t what = 0;             // 2 bits a token: 1 above, 2 equal, 3 stays
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (t + i >= len) continue;
+      uint32_t x;
+      if (t + i >= lo && t + i < hi) {
+        const uint32_t key = key_of(w[i]);
+        x = key > least ? 1u : key == least && equal ? 2u : 0u;
       } else {
-        stays = 1;
+        x = 3;
       }
+      what |= x << (2 * i);
+      count += x == 1 ? 1ull : x == 2 ? 1ull << 32 : 0ull;
     }
-    int a = is_above, s = is_same, ta, ts;
-    block_sums2(a, s, &ta, &ts, sums);
-    int32_t to = -1;
-    if (stays) {
-      to = t < lo ? t : t - (hi - lo) + want;
-    } else if (is_above || (is_same && same + s < equal)) {
-      to = lo + above + a + min(same + s, equal);
-    }
-    above += ta;
-    same += ts;
-    if (to >= 0) {
-      const int32_t id = row[t / kBlock];
-      const bool ok = id >= 0 && id < p.num_blocks;
+    const int32_t id = what ? row[t / kBlock] : 0;
+    uint64_t all;
+    const uint64_t before = block_sums(count, &all, sums);
+    uint32_t above = gone_above + (uint32_t)before;
+    uint32_t same = gone_same + (uint32_t)(before >> 32);
+    gone_above += (uint32_t)all;
+    gone_same += (uint32_t)(all >> 32);
+    const bool ok = id >= 0 && id < p.num_blocks;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t x = (what >> (2 * i)) & 3;
+      int32_t to = -1;
+      if (x == 3)
+        to = t + i < lo ? t + i : t + i - (hi - lo) + want;
+      else if (x == 1 || (x == 2 && same < (uint32_t)equal))
+        to = lo + (int32_t)(above + min(same, (uint32_t)equal));
+      above += x == 1;
+      same += x == 2;
+      if (to < 0) continue;
       bad |= !ok;
-      kept[to] = t;
+      kept[to] = t + i;
       ids[to] = ok ? id : -1;
-      acc_out[to] = w;
+      acc_out[to] = w[i];
     }
   }
   __syncthreads();
@@ -174,12 +204,13 @@ __global__ void __launch_bounds__(kSelThreads)
   if (bad && p.flags) atomicOr(p.flags, KVTC_FLAG_BLOCK);
 }
 
-// A block takes `slice` pieces of the rows of one request in one pool.  Where
-// kept rows go into the blocks that they come from, it goes through them in
-// order: row j's place is at or before the one it comes from, so that what is
-// still to be read is never written, once all reads of a step are done.
-// Otherwise several blocks share the rows of a slice.
+// A block takes `slice` pieces of the rows of one request in one pool, four
+// rows a thread under way.  Where kept rows go into the blocks that they come
+// from, it goes through them in order: row j's place is at or before the one it
+// comes from, so that what is still to be read is never written, once all reads
+// of a step are done.  Otherwise several blocks share the rows of a slice.
 constexpr int kMoveThreads = 256;
+constexpr int kMoveRows = 4;         // per thread and step
 __global__ void __launch_bounds__(kMoveThreads)
     move_kernel(const __grid_constant__ EvictParams p) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -188,7 +219,8 @@ __global__ void __launch_bounds__(kMoveThreads)
   const int64_t r = blockIdx.z;
   const int part = blockIdx.x / slices, parts = gridDim.x / slices;
   const int c = (blockIdx.x % slices) * p.slice + threadIdx.x % p.slice;
-  const int step = kMoveThreads / p.slice;
+  const int rows = kMoveThreads / p.slice, mine = threadIdx.x / p.slice;
+  const bool in = mine < rows && c < p.pieces;
   const int32_t most = p.max_blocks * kBlock;
   const int32_t n = p.lens_out[r];
   const int32_t* kept = p.kept + r * (int64_t)p.keep;
@@ -196,21 +228,32 @@ __global__ void __launch_bounds__(kMoveThreads)
   const int32_t* to_row = p.out_table + r * p.max_blocks;
   uint4* pool = p.cache[blockIdx.y];
   bool bad = false;
-  for (int32_t j0 = part * step; j0 < n; j0 += parts * step) {
-    const int32_t j = j0 + (int32_t)threadIdx.x / p.slice;
-    uint4 v;
-    int64_t to = -1;
-    if (j < n && threadIdx.x / p.slice < step && c < p.pieces) {
-      const int32_t t = kept[j], id = ids[j], oid = to_row[j / kBlock];
-      const bool ok = oid >= 0 && oid < p.num_blocks;
-      bad |= !ok;
-      if (ok && id >= 0 && !(p.in_place && t == j)) {
-        to = (int64_t)oid * kBlock + j % kBlock;
-        v = pool[((int64_t)id * kBlock + t % kBlock) * p.pieces + c];
-      }
+  const int64_t step = (int64_t)rows * kMoveRows;
+  for (int64_t j0 = part * step; j0 < n; j0 += parts * step) {
+    uint4 v[kMoveRows];
+    int64_t to[kMoveRows];
+    int32_t t[kMoveRows], id[kMoveRows], oid[kMoveRows];
+#pragma unroll
+    for (int i = 0; i < kMoveRows; ++i) {
+      const int64_t j = j0 + i * rows + mine;
+      const bool has = in && j < n;
+      t[i] = has ? kept[j] : 0;
+      id[i] = has ? ids[j] : -1;
+      oid[i] = has ? to_row[j / kBlock] : -1;
+      const bool ok = oid[i] >= 0 && oid[i] < p.num_blocks;
+      bad |= has && !ok;
+      to[i] = ok && id[i] >= 0 && !(p.in_place && t[i] == j)
+                  ? (int64_t)oid[i] * kBlock + j % kBlock
+                  : -1;
     }
+#pragma unroll
+    for (int i = 0; i < kMoveRows; ++i)
+      if (to[i] >= 0)
+        v[i] = pool[((int64_t)id[i] * kBlock + t[i] % kBlock) * p.pieces + c];
     if (p.in_place) __syncthreads();
-    if (to >= 0) pool[to * p.pieces + c] = v;
+#pragma unroll
+    for (int i = 0; i < kMoveRows; ++i)
+      if (to[i] >= 0) pool[to[i] * p.pieces + c] = v[i];
   }
   if (bad && p.flags) atomicOr(p.flags, KVTC_FLAG_BLOCK);
 }
@@ -282,19 +325,32 @@ int kvtc_paged_evict(int cuda_device, int R, const float* acc, int64_t acc_ld,
   p.max_blocks = max_blocks;
   p.in_place = out_table == block_table;
   p.pieces = D / 8;
-  p.slice = std::min(8, p.pieces);
   cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
   if (launch_kernel(select_kernel, R, kSelThreads, 0, st, true, 0, p) !=
       cudaSuccess)
     return KVTC_ECUDA;
   count_launch();
-  const int slices = (p.pieces + p.slice - 1) / p.slice;
   for (int j0 = 0; j0 < nstreams; j0 += kMaxStreams) {
     const int n = std::min(kMaxStreams, nstreams - j0);
     for (int j = 0; j < n; ++j) p.cache[j] = static_cast<uint4*>(cache[j0 + j]);
-    const int parts = p.in_place ? 1 : 4;
-    if (launch_kernel(move_kernel, dim3(slices * parts, n, R), kMoveThreads,
-                      0, st, true, 0, p) != cudaSuccess)
+    // 512 bytes of a row, or in place, where a slice is one block's, as little
+    // as 64 while there are fewer blocks than the GPU holds
+    const int64_t pools = (int64_t)R * n;
+    p.slice = std::min(32, p.pieces);
+    while (p.in_place && p.slice > 4 &&
+           pools * ((p.pieces + p.slice - 1) / p.slice) < 8 * 152)
+      p.slice = (p.slice + 1) / 2;
+    const int64_t slices = (p.pieces + p.slice - 1) / p.slice;
+    const int64_t step = kMoveThreads / p.slice * kMoveRows;
+    const int64_t steps =
+        (std::min<int64_t>(keep, (int64_t)max_blocks * kBlock) + step - 1) /
+        step;
+    const int64_t parts =
+        p.in_place ? 1
+                   : std::max<int64_t>(
+                         1, std::min(steps, 16 * 152 / (pools * slices)));
+    if (launch_kernel(move_kernel, dim3((unsigned)(slices * parts), n, R),
+                      kMoveThreads, 0, st, true, 0, p) != cudaSuccess)
       return KVTC_ECUDA;
     count_launch();
   }

@@ -111,17 +111,34 @@ struct Place {
   }
 };
 
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t d, x = *reinterpret_cast<uint64_t*>(&a),
+              y = *reinterpret_cast<uint64_t*>(&b);
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(x), "l"(y));
+  return *reinterpret_cast<float2*>(&d);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t d, x = *reinterpret_cast<uint64_t*>(&a),
+              y = *reinterpret_cast<uint64_t*>(&b),
+              z = *reinterpret_cast<uint64_t*>(&c);
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(x), "l"(y), "l"(z));
+  return *reinterpret_cast<float2*>(&d);
+}
+
 template <class T, int HD, bool kNeighbours>
 __global__ void __launch_bounds__(kThreads)
     rotate_kernel(const __grid_constant__ RotateParams p) {
   constexpr int kLanes = HD / 8;                  // per head
   constexpr int kHeads = kThreads / kLanes;       // heads at once
-  __shared__ float2 turn[kMaxTile * HD / 2];      // cos and sin
+  __shared__ __align__(16) float cosines[kMaxTile * HD / 2];
+  __shared__ __align__(16) float sines[kMaxTile * HD / 2];
   __shared__ int64_t slot[kMaxTile];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x, c = tid % kLanes;
   const Place<HD, kNeighbours> place(c, p.pairs);
   const bool turned = 4 * c < p.pairs;
+  const bool normed = p.norm[0] || p.norm[1];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   // this thread's angle: pair and token of a tile
   const int pair = tid % (HD / 2);
@@ -145,7 +162,8 @@ __global__ void __launch_bounds__(kThreads)
       const uint64_t at = (uint64_t)(int64_t)p.positions[n0 + i] * step;
       float s, co;
       sincospif((float)(int32_t)(at >> 32) * 0x1p-31f, &s, &co);
-      turn[i * (HD / 2) + pair] = make_float2(co * p.scale, s * p.scale);
+      cosines[i * (HD / 2) + pair] = co * p.scale;
+      sines[i * (HD / 2) + pair] = s * p.scale;
     }
     if (tid < tokens) {
       int64_t to = p.slots[n0 + tid];
@@ -195,44 +213,59 @@ __global__ void __launch_bounds__(kThreads)
         const int g = hi[k] - p.heads;
         const int what = g < 0 ? 0 : g < p.kv_heads ? 1 : 2;
         uint4 out = x[k];
-        const float2 v0 = unpack2<T>(x[k].x), v1 = unpack2<T>(x[k].y);
-        const float2 v2 = unpack2<T>(x[k].z), v3 = unpack2<T>(x[k].w);
-        float v[8] = {v0.x, v0.y, v1.x, v1.y, v2.x, v2.y, v3.x, v3.y};
-        if (p.norm[0] || p.norm[1]) {
-          float sum = 0.f;
+        // halves: a0 a1, a2 a3, b0 b1, b2 b3; neighbours: a0 b0, a1 b1, ...
+        float2 v[4] = {unpack2<T>(x[k].x), unpack2<T>(x[k].y),
+                       unpack2<T>(x[k].z), unpack2<T>(x[k].w)};
+        if (normed) {
+          float2 sum2 = mul2(v[0], v[0]);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) sum = fmaf(v[e], v[e], sum);
+          for (int e = 1; e < 4; ++e) sum2 = fma2(v[e], v[e], sum2);
+          float sum = sum2.x + sum2.y;
 #pragma unroll
           for (int d = 1; d < kLanes; d <<= 1)
             sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
           if (what < 2 && p.norm[what]) {
             // (to 2^-22, far below the output's step)
             const float inv = rsqrtf(fmaf(sum, 1.f / HD, p.eps));
-            const uint4 ww = w[what];
-            const float2 w0 = unpack2<T>(ww.x), w1 = unpack2<T>(ww.y);
-            const float2 w2 = unpack2<T>(ww.z), w3 = unpack2<T>(ww.w);
-            const float f[8] = {w0.x, w0.y, w1.x, w1.y,
-                                w2.x, w2.y, w3.x, w3.y};
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = v[e] * inv * f[e];
+            const float2 inv2 = make_float2(inv, inv);
+            const uint4 ww = what ? w[1] : w[0];
+            v[0] = mul2(mul2(v[0], inv2), unpack2<T>(ww.x));
+            v[1] = mul2(mul2(v[1], inv2), unpack2<T>(ww.y));
+            v[2] = mul2(mul2(v[2], inv2), unpack2<T>(ww.z));
+            v[3] = mul2(mul2(v[3], inv2), unpack2<T>(ww.w));
           }
         }
         if (ti[k] >= tokens) continue;
         if (what < 2) {
           if (turned) {
-            const float2* at = turn + ti[k] * (HD / 2) + c * 4;
+            const int at = ti[k] * (HD / 2) + c * 4;
+            const float4 co = *reinterpret_cast<const float4*>(cosines + at);
+            const float4 si = *reinterpret_cast<const float4*>(sines + at);
+            if (kNeighbours) {
+              const float cc[4] = {co.x, co.y, co.z, co.w};
+              const float ss[4] = {si.x, si.y, si.z, si.w};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float2 cs = at[e];
-              float& a = v[kNeighbours ? 2 * e : e];
-              float& b = v[kNeighbours ? 2 * e + 1 : e + 4];
-              const float u = a * cs.x - b * cs.y;
-              b = b * cs.x + a * cs.y;
-              a = u;
+              for (int e = 0; e < 4; ++e)
+                v[e] = fma2(v[e], make_float2(cc[e], cc[e]),
+                            mul2(make_float2(v[e].y, v[e].x),
+                                 make_float2(-ss[e], ss[e])));
+            } else {
+              const float2 c01 = make_float2(co.x, co.y);
+              const float2 c23 = make_float2(co.z, co.w);
+              const float2 s01 = make_float2(si.x, si.y);
+              const float2 s23 = make_float2(si.z, si.w);
+              const float2 m01 = make_float2(-si.x, -si.y);
+              const float2 m23 = make_float2(-si.z, -si.w);
+              const float2 a01 = fma2(v[0], c01, mul2(v[2], m01));
+              const float2 a23 = fma2(v[1], c23, mul2(v[3], m23));
+              v[2] = fma2(v[2], c01, mul2(v[0], s01));
+              v[3] = fma2(v[3], c23, mul2(v[1], s23));
+              v[0] = a01;
+              v[1] = a23;
             }
           }
-          out = make_uint4(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]),
-                           pack2<T>(v[4], v[5]), pack2<T>(v[6], v[7]));
+          out = make_uint4(pack2<T>(v[0].x, v[0].y), pack2<T>(v[1].x, v[1].y),
+                           pack2<T>(v[2].x, v[2].y), pack2<T>(v[3].x, v[3].y));
         }
         char* to;
         if (what == 0) {
