@@ -47,7 +47,8 @@ struct RotateParams {
   unsigned* flags;
   int64_t N, ld, q_out_ld, pool_rows;
   float scale, eps;
-  int32_t heads, kv_heads, all;      // all: heads of q, k and v together
+  int32_t heads, kv_heads;
+  uint32_t inv[2];                   // 2^32 / heads (and kv_heads), up; 0: one
   int32_t pairs;                     // rotary_dim / 2
   int32_t tile;                      // tokens per tile
 };
@@ -127,7 +128,7 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
 }
 
 template <class T, int HD, bool kNeighbours>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 4)
     rotate_kernel(const __grid_constant__ RotateParams p) {
   constexpr int kLanes = HD / 8;                  // per head
   constexpr int kHeads = kThreads / kLanes;       // heads at once
@@ -138,7 +139,6 @@ __global__ void __launch_bounds__(kThreads)
   const int tid = threadIdx.x, c = tid % kLanes;
   const Place<HD, kNeighbours> place(c, p.pairs);
   const bool turned = 4 * c < p.pairs;
-  const bool normed = p.norm[0] || p.norm[1];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   // this thread's angle: pair and token of a tile
   const int pair = tid % (HD / 2);
@@ -147,11 +147,16 @@ __global__ void __launch_bounds__(kThreads)
     const double f = p.inv_freq[pair] * 0.15915494309189533577;   // 1 / 2 pi
     step = __double2ull_rn((f - floor(f)) * 18446744073709551616.0);
   }
-  uint4 w[2];
+  float2 w[2][4];                    // weights of the norms
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
-    w[i] = p.norm[i] ? place.load(static_cast<const char*>(p.norm[i]))
-                     : make_uint4(0, 0, 0, 0);
+  for (int i = 0; i < 2; ++i) {
+    const uint4 x = p.norm[i] ? place.load(static_cast<const char*>(p.norm[i]))
+                              : make_uint4(0, 0, 0, 0);
+    w[i][0] = unpack2<T>(x.x);
+    w[i][1] = unpack2<T>(x.y);
+    w[i][2] = unpack2<T>(x.z);
+    w[i][3] = unpack2<T>(x.w);
+  }
   const int64_t tiles = (p.N + p.tile - 1) / p.tile;
   for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
     const int64_t n0 = t * p.tile;
@@ -173,34 +178,32 @@ __global__ void __launch_bounds__(kThreads)
       }
       slot[tid] = to;
     }
-    // heads of the tile, kHeads at a time; q's first, then k's, then v's
-    int i = 0, h = tid / kLanes;
-    while (h >= p.all) {
-      h -= p.all;
-      ++i;
-    }
-    const int rounds = (tokens * p.all + kHeads - 1) / kHeads;
+    // Rounds of kHeads heads of the tile, of one kind each: q, then k, then v.
+    const int of_q = (tokens * p.heads + kHeads - 1) / kHeads;
+    const int of_k = (tokens * p.kv_heads + kHeads - 1) / kHeads;
+    const int rounds = of_q + (p.src[2] ? 2 : 1) * of_k;
     bool first = true;
+#pragma unroll 1
     for (int r0 = 0; r0 < rounds; r0 += kAhead) {
       uint4 x[kAhead];
-      int ti[kAhead], hi[kAhead];
+      int ti[kAhead], hi[kAhead];     // token, or -1; head
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
-        ti[k] = i;
-        hi[k] = h;
-        if (i < tokens) {
-          const int g = h - p.heads;
-          const char* from = p.src[g < 0 ? 0 : g < p.kv_heads ? 1 : 2] +
-                             (n0 + i) * p.ld * 2;
-          from += (g < 0 ? h : g < p.kv_heads ? g : g - p.kv_heads) * (HD * 2);
-          x[k] = place.load(from);
-        } else {
+        const int r = r0 + k;
+        const int what = r < of_q ? 0 : r < of_q + of_k ? 1 : 2;
+        const int head0 = what == 0 ? r : what == 1 ? r - of_q
+                                                    : r - of_q - of_k;
+        const int n = what ? p.kv_heads : p.heads;
+        const uint32_t at = head0 * kHeads + tid / kLanes;
+        const uint32_t inv = p.inv[what ? 1 : 0];
+        ti[k] = inv ? __umulhi(at, inv) : at;
+        hi[k] = at - ti[k] * n;
+        if (r >= rounds || ti[k] >= tokens) {
+          ti[k] = -1;
           x[k] = make_uint4(0, 0, 0, 0);
-        }
-        h += kHeads;
-        while (h >= p.all) {
-          h -= p.all;
-          ++i;
+        } else {
+          x[k] = place.load(p.src[what] + (n0 + ti[k]) * p.ld * 2 +
+                            hi[k] * (HD * 2));
         }
       }
       if (first) {
@@ -209,14 +212,20 @@ __global__ void __launch_bounds__(kThreads)
       }
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
-        if (r0 + k >= rounds) break;
-        const int g = hi[k] - p.heads;
-        const int what = g < 0 ? 0 : g < p.kv_heads ? 1 : 2;
-        uint4 out = x[k];
+        const int r = r0 + k;
+        if (r >= rounds) break;
+        if (r >= of_q + of_k) {
+          if (ti[k] >= 0 && slot[ti[k]] >= 0)
+            place.store(p.pool[1] + (slot[ti[k]] * p.kv_heads + hi[k]) *
+                                        (HD * 2),
+                        x[k]);
+          continue;
+        }
+        const bool is_k = r >= of_q;
         // halves: a0 a1, a2 a3, b0 b1, b2 b3; neighbours: a0 b0, a1 b1, ...
         float2 v[4] = {unpack2<T>(x[k].x), unpack2<T>(x[k].y),
                        unpack2<T>(x[k].z), unpack2<T>(x[k].w)};
-        if (normed) {
+        if (p.norm[is_k]) {
           float2 sum2 = mul2(v[0], v[0]);
 #pragma unroll
           for (int e = 1; e < 4; ++e) sum2 = fma2(v[e], v[e], sum2);
@@ -224,59 +233,53 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
           for (int d = 1; d < kLanes; d <<= 1)
             sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-          if (what < 2 && p.norm[what]) {
-            // (to 2^-22, far below the output's step)
-            const float inv = rsqrtf(fmaf(sum, 1.f / HD, p.eps));
-            const float2 inv2 = make_float2(inv, inv);
-            const uint4 ww = what ? w[1] : w[0];
-            v[0] = mul2(mul2(v[0], inv2), unpack2<T>(ww.x));
-            v[1] = mul2(mul2(v[1], inv2), unpack2<T>(ww.y));
-            v[2] = mul2(mul2(v[2], inv2), unpack2<T>(ww.z));
-            v[3] = mul2(mul2(v[3], inv2), unpack2<T>(ww.w));
-          }
-        }
-        if (ti[k] >= tokens) continue;
-        if (what < 2) {
-          if (turned) {
-            const int at = ti[k] * (HD / 2) + c * 4;
-            const float4 co = *reinterpret_cast<const float4*>(cosines + at);
-            const float4 si = *reinterpret_cast<const float4*>(sines + at);
-            if (kNeighbours) {
-              const float cc[4] = {co.x, co.y, co.z, co.w};
-              const float ss[4] = {si.x, si.y, si.z, si.w};
+          // (to 2^-22, far below the output's step)
+          const float inv = rsqrtf(fmaf(sum, 1.f / HD, p.eps));
+          const float2 inv2 = make_float2(inv, inv);
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                v[e] = fma2(v[e], make_float2(cc[e], cc[e]),
-                            mul2(make_float2(v[e].y, v[e].x),
-                                 make_float2(-ss[e], ss[e])));
-            } else {
-              const float2 c01 = make_float2(co.x, co.y);
-              const float2 c23 = make_float2(co.z, co.w);
-              const float2 s01 = make_float2(si.x, si.y);
-              const float2 s23 = make_float2(si.z, si.w);
-              const float2 m01 = make_float2(-si.x, -si.y);
-              const float2 m23 = make_float2(-si.z, -si.w);
-              const float2 a01 = fma2(v[0], c01, mul2(v[2], m01));
-              const float2 a23 = fma2(v[1], c23, mul2(v[3], m23));
-              v[2] = fma2(v[2], c01, mul2(v[0], s01));
-              v[3] = fma2(v[3], c23, mul2(v[1], s23));
-              v[0] = a01;
-              v[1] = a23;
-            }
+          for (int e = 0; e < 4; ++e)
+            v[e] = mul2(mul2(v[e], inv2), is_k ? w[1][e] : w[0][e]);
+        }
+        if (ti[k] < 0) continue;
+        if (turned) {
+          const int at = ti[k] * (HD / 2) + c * 4;
+          const float4 co = *reinterpret_cast<const float4*>(cosines + at);
+          const float4 si = *reinterpret_cast<const float4*>(sines + at);
+          if (kNeighbours) {
+            const float cc[4] = {co.x, co.y, co.z, co.w};
+            const float ss[4] = {si.x, si.y, si.z, si.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              v[e] = fma2(v[e], make_float2(cc[e], cc[e]),
+                          mul2(make_float2(v[e].y, v[e].x),
+                               make_float2(-ss[e], ss[e])));
+          } else {
+            const float2 c01 = make_float2(co.x, co.y);
+            const float2 c23 = make_float2(co.z, co.w);
+            const float2 s01 = make_float2(si.x, si.y);
+            const float2 s23 = make_float2(si.z, si.w);
+            const float2 m01 = make_float2(-si.x, -si.y);
+            const float2 m23 = make_float2(-si.z, -si.w);
+            const float2 a01 = fma2(v[0], c01, mul2(v[2], m01));
+            const float2 a23 = fma2(v[1], c23, mul2(v[3], m23));
+            v[2] = fma2(v[2], c01, mul2(v[0], s01));
+            v[3] = fma2(v[3], c23, mul2(v[1], s23));
+            v[0] = a01;
+            v[1] = a23;
           }
-          out = make_uint4(pack2<T>(v[0].x, v[0].y), pack2<T>(v[1].x, v[1].y),
-                           pack2<T>(v[2].x, v[2].y), pack2<T>(v[3].x, v[3].y));
         }
-        char* to;
-        if (what == 0) {
-          to = p.q_out + ((n0 + ti[k]) * p.q_out_ld + (int64_t)hi[k] * HD) * 2;
-        } else {
-          const int64_t s = slot[ti[k]];
-          if (s < 0) continue;
-          to = p.pool[what - 1] +
-               (s * p.kv_heads + (g - (what - 1) * p.kv_heads)) * (HD * 2);
+        const uint4 out =
+            make_uint4(pack2<T>(v[0].x, v[0].y), pack2<T>(v[1].x, v[1].y),
+                       pack2<T>(v[2].x, v[2].y), pack2<T>(v[3].x, v[3].y));
+        if (!is_k) {
+          place.store(p.q_out + (n0 + ti[k]) * p.q_out_ld * 2 +
+                          hi[k] * (HD * 2),
+                      out);
+        } else if (slot[ti[k]] >= 0) {
+          place.store(p.pool[0] + (slot[ti[k]] * p.kv_heads + hi[k]) *
+                                      (HD * 2),
+                      out);
         }
-        place.store(to, out);
       }
     }
   }
@@ -392,7 +395,9 @@ int kvtc_paged_rotate(int cuda_device, int64_t N, int heads, int kv_heads,
   p.eps = eps;
   p.heads = heads;
   p.kv_heads = kv_heads;
-  p.all = heads + kv_heads * (v ? 2 : 1);
+  // (exact for the up to 8 x 2048 heads of a tile)
+  p.inv[0] = heads > 1 ? (uint32_t)((1ull << 32) / heads + 1) : 0;
+  p.inv[1] = kv_heads > 1 ? (uint32_t)((1ull << 32) / kv_heads + 1) : 0;
   p.pairs = rotary_dim / 2;
   // as many tokens as a block has angles to form, or one where that leaves
   // blocks without any
