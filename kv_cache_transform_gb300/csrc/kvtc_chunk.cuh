@@ -174,12 +174,15 @@ __device__ __forceinline__ I uniform(I x) {
 }
 // Shared-memory matrix descriptors as in sw128_desc: the low word of one, with
 // a leading byte offset (of operands whose rows are contiguous), and the high
-// word of all.
+// word, with the bytes from one group of eight rows to the next.
 __device__ __forceinline__ uint32_t desc_base(uint32_t smem_addr,
                                               uint32_t lead = 1) {
   return uniform(((smem_addr & 0x3FFFFu) >> 4) | lead << 16);
 }
-constexpr uint32_t kDescHigh = (1024u >> 4) | 1u << 14 | 2u << 29;
+__host__ __device__ constexpr uint32_t desc_high(uint32_t stride) {
+  return (stride >> 4) | 1u << 14 | 2u << 29;
+}
+template <uint32_t kHighA = desc_high(1024)>
 __device__ __forceinline__ void mma_ss_one(uint32_t d_tmem, uint32_t a_desc,
                                            uint32_t b_desc, uint32_t idesc,
                                            uint32_t accumulate) {
@@ -188,10 +191,11 @@ __device__ __forceinline__ void mma_ss_one(uint32_t d_tmem, uint32_t a_desc,
       "elect.sync _|q, 0xFFFFFFFF;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
       "mov.b64 a, {%1, %5};\n\t"
-      "mov.b64 b, {%2, %5};\n\t"
+      "mov.b64 b, {%2, %6};\n\t"
       "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(
           d_tmem),
-      "r"(a_desc), "r"(b_desc), "r"(idesc), "r"(accumulate), "n"(kDescHigh)
+      "r"(a_desc), "r"(b_desc), "r"(idesc), "r"(accumulate), "n"(kHighA),
+      "n"(desc_high(1024))
       : "memory");
 }
 __device__ __forceinline__ void mma_ts_one(uint32_t d_tmem, uint32_t a_tmem,
@@ -204,7 +208,8 @@ __device__ __forceinline__ void mma_ts_one(uint32_t d_tmem, uint32_t a_tmem,
       "mov.b64 b, {%2, %5};\n\t"
       "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(
           d_tmem),
-      "r"(a_tmem), "r"(b_desc), "r"(idesc), "r"(accumulate), "n"(kDescHigh)
+      "r"(a_tmem), "r"(b_desc), "r"(idesc), "r"(accumulate),
+      "n"(desc_high(1024))
       : "memory");
 }
 __device__ __forceinline__ void tc_commit_one(uint64_t* bar) {

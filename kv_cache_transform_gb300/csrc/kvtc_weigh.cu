@@ -4,9 +4,9 @@
 // with the log-sum-exp that the attention of the same rows returned, so K is
 // read once and nothing but the sums is written.
 //
-// The products are formed transposed, S^T = K Q^T: 128 tokens fill the 128
-// lanes of TMEM and the (row, head) pairs of a KV head the columns, so that a
-// thread owns a token, adds up its columns in a register, and nothing is
+// The products are formed transposed, S^T = K Q^T: 128 tokens (eight of each of
+// 16 pages) fill the 128 lanes of TMEM and the (row, head) pairs of a KV head
+// the columns, so that a thread owns a token, adds up its columns in a register, and nothing is
 // summed across threads.  Few pairs (a decode step: the heads of one row) make
 // a narrow product, down to 16 columns.
 //
@@ -35,8 +35,9 @@ namespace {
 constexpr int kThreads = 384;
 constexpr int kProducer = 8, kMma = 9, kFetch = 10;   // (and 11)
 constexpr int kTile = 256;           // tokens of an item
+constexpr int kPages = kTile / kBlock;
 constexpr int kCols = 128;           // columns of a product
-constexpr int kItems = 4, kSteps = 2;
+constexpr int kItems = 4;
 constexpr int kBoxes = 8;            // tokens of Q at once: 1, 2, ... 128
 
 struct __align__(16) JoinDesc {
@@ -68,14 +69,16 @@ struct Cfg {
   static constexpr int SC = HD < 128 ? HD : 128;      // channels per stage
   static constexpr int NS = HD / SC;                  // stages per tile
   static constexpr int kSlabs = SC / 64;
-  static constexpr int kStage = kRows * SC * 2;
-  static constexpr int SK = HD == 64 ? 8 : 4;         // stages of K
+  static constexpr int kPage = kSlabs * 2048;         // bytes of a page
+  static constexpr int kStageK = kPages * kPage;      // both token tiles'
+  static constexpr int kStage = kRows * SC * 2;       // of Q
+  static constexpr int SK = HD == 64 ? 4 : 2;         // stages of K
   static constexpr int SQ = HD == 64 ? 4 : 3;         // stages of Q
-  static constexpr int kQ = SK * kStage;
+  static constexpr int kQ = SK * kStageK;
   static constexpr int kMisc = kQ + SQ * kStage;
   static constexpr int kBytes = kMisc + 2048 + 1024;  // + alignment slack
   static_assert(kBytes <= 232448, "shared memory of a block");
-  static_assert(SK * kStage >= 8 * (kMaxReq + 1), "prefix of the requests");
+  static_assert(SK * kStageK >= 8 * (kMaxReq + 1), "prefix of the requests");
 };
 
 struct __align__(16) Item {
@@ -90,10 +93,10 @@ struct __align__(16) Item {
 constexpr int kStarts = 1, kEnds = 2, kStop = 4;
 
 struct Bars {
-  uint64_t k_full[8], k_empty[8], q_full[4], q_empty[4];
+  uint64_t k_full[4], k_empty[4], q_full[4], q_empty[4];
   uint64_t item_full[kItems], item_empty[kItems];
-  uint64_t l_full[kSteps], l_empty[kSteps];
-  uint64_t s_full[2][2], s_empty[2][2];     // buffer, token tile
+  // buffer, token tile: products and log-sum-exps are there; are done with
+  uint64_t s_full[2][2], s_empty[2][2];
   uint64_t fin;
 };
 struct Smem {
@@ -102,8 +105,8 @@ struct Smem {
   int64_t sums[kThreads / 32];
   uint32_t tmem;
   int abort_flag;
-  uint32_t dead[kSteps];     // columns without weight, a bit per 32
-  __align__(16) float lse[kSteps][kCols];   // minus log-sum-exp, in log2
+  uint32_t dead[2];     // columns without weight, a bit per 32
+  __align__(16) float lse[2][kCols];   // minus log-sum-exp, in log2
 };
 static_assert(sizeof(Smem) <= 2048, "the kernel's shared variables");
 
@@ -143,7 +146,6 @@ template <class T, class C>
 __device__ __forceinline__ bool produce(const WeighParams& p, Smem& sm,
                                         uint32_t smem, const int64_t* pre) {
   constexpr int HD = C::HD, NS = C::NS;
-  constexpr int kRounds = HD == 256 ? 2 : 1;    // of 32 lanes per K tile pair
   const int lane = (int)lane_id();
   Bars& b = sm.bars;
   volatile int* stop = &sm.abort_flag;
@@ -202,8 +204,7 @@ __device__ __forceinline__ bool produce(const WeighParams& p, Smem& sm,
     if (j1 > j0) {
       const int32_t t0 = tiles.tile(i) * kTile;
       const int64_t pf = (int64_t)q.len - q.n, pl = (int64_t)q.len - 1;
-      // lane l: page l % 16, slab l / 16 (and 2 further on)
-      const int page = lane % 16, slab = lane / 16;
+      const int page = lane % kPages;
       const int64_t tp = (int64_t)t0 + page * kBlock;
       const bool need = live && tp <= pl &&
                         (!p.window || tp < p.sink ||
@@ -211,7 +212,7 @@ __device__ __forceinline__ bool produce(const WeighParams& p, Smem& sm,
       const int32_t id =
           need ? p.table[(int64_t)r * p.max_blocks + tp / kBlock] : -1;
       const bool fine = id >= 0 && id < p.num_blocks;
-      if (need && !fine && slab == 0 && p.flags)
+      if (need && !fine && lane < kPages && p.flags)
         atomicOr(p.flags, KVTC_FLAG_BLOCK);
       const uint32_t pages = __ballot_sync(~0u, fine) & 0xFFFFu;
       if (!warp_wait(&b.item_empty[it.at], it.phase ^ 1, stop)) {
@@ -247,31 +248,19 @@ __device__ __forceinline__ bool produce(const WeighParams& p, Smem& sm,
       }
       it.next();
       for (int j = j0; j < j1 && ok && steps; ++j) {
-        // K: two token tiles, NS stages each
 #pragma unroll
-        for (int s = 0; s < 2 * NS; ++s) {
-          const int tile = s / NS, sub = s % NS;
+        for (int s = 0; s < NS; ++s) {
           if (!warp_wait(&b.k_empty[kt.at], kt.phase ^ 1, stop)) {
             ok = false;
             break;
           }
           if (lane == 0)
-            mbar_arrive_expect_tx(&b.k_full[kt.at],
-                                  __popc(pages >> (8 * tile) & 0xFF) *
-                                      C::kSlabs * 2048);
+            mbar_arrive_expect_tx(&b.k_full[kt.at], __popc(pages) * C::kPage);
           __syncwarp();
-          if (fine && page / 8 == tile) {
-#pragma unroll
-            for (int f = 0; f < kRounds; ++f) {
-              const int sl = slab + 2 * f;
-              if (sl < HD / 64 && sl / C::kSlabs == sub)
-                tma_load_4d(smem + kt.at * C::kStage +
-                                (sl % C::kSlabs) * (kRows * 128) +
-                                (page % 8) * 2048,
-                            &p.tm_k, 0, 0, j * (HD / 64) + sl, id,
-                            &b.k_full[kt.at]);
-            }
-          }
+          if (fine && lane < kPages)
+            tma_load_4d(smem + kt.at * C::kStageK + page * C::kPage, &p.tm_k,
+                        0, 0, j * (HD / 64) + s * C::kSlabs, id,
+                        &b.k_full[kt.at]);
           kt.next();
           ++k_fills;
         }
@@ -353,52 +342,61 @@ __device__ __forceinline__ bool multiply(const WeighParams& p, Smem& sm,
   Turn<kItems> it;
   uint32_t step = 0;                  // over all items
   for (;;) {
-    if (!mbar_wait(&b.item_full[it.at], it.phase, stop)) return false;
-    const Item item = sm.items[it.at];
-    mbar_arrive(&b.item_empty[it.at]);
+    if (!warp_wait(&b.item_full[it.at], it.phase, stop)) return false;
+    const Item& item = sm.items[it.at];
+    const int flags = uniform(item.flags), steps = uniform(item.steps);
+    const int heads = uniform(item.j1 - item.j0), n = uniform(item.n);
+    __syncwarp();
+    if (lane_id() == 0) mbar_arrive(&b.item_empty[it.at]);
     it.next();
-    if (item.flags & kStop) return true;
-    if (item.steps == 0) continue;
-    for (int j = item.j0; j < item.j1; ++j) {
-      for (int st = 0; st < item.steps; ++st, ++step) {
+    if (flags & kStop) return true;
+    if (steps == 0) continue;
+#pragma unroll 1
+    for (int j = 0; j < heads; ++j) {
+#pragma unroll 1
+      for (int st = 0; st < steps; ++st, ++step) {
         const uint32_t buf = step & 1, phase = (step >> 1) & 1;
         const uint32_t idesc =
-            make_idesc(kRows, columns(p, item.n, st), Elem<T>::kFormat);
+            make_idesc(kRows, columns(p, n, st), Elem<T>::kFormat);
         Turn<C::SQ> q0 = qt;
 #pragma unroll
         for (int s = 0; s < NS; ++s) {
-          if (!mbar_wait(&b.q_full[qt.at], qt.phase, stop)) return false;
+          if (!warp_wait(&b.q_full[qt.at], qt.phase, stop)) return false;
           qt.next();
         }
         Turn<C::SK> k = kt;
-#pragma unroll
-        for (int tile = 0; tile < 2; ++tile) {
-          if (!mbar_wait(&b.s_empty[buf][tile], phase ^ 1, stop)) return false;
-          Turn<C::SQ> q = q0;
-#pragma unroll
-          for (int s = 0; s < NS; ++s) {
-            if (st == 0 && !mbar_wait(&b.k_full[k.at], k.phase, stop))
+        Turn<C::SQ> q = q0;
+#pragma unroll 1
+        for (int s = 0; s < NS; ++s) {
+          if (st == 0 && !warp_wait(&b.k_full[k.at], k.phase, stop))
+            return false;
+          const uint32_t bd = desc_base(smem + C::kQ + q.at * C::kStage);
+#pragma unroll 1
+          for (int tile = 0; tile < 2; ++tile) {
+            if (s == 0 && !warp_wait(&b.s_empty[buf][tile], phase ^ 1, stop))
               return false;
+            // (rows 0 .. 7 of the 16 pages, or 8 .. 15)
             tc_fence_after();
-            const uint64_t ad = sw128_desc(smem + k.at * C::kStage);
-            const uint64_t bd = sw128_desc(smem + C::kQ + q.at * C::kStage);
+            const uint32_t ad =
+                desc_base(smem + k.at * C::kStageK + tile * 1024);
+            const uint32_t d = tmem + (buf * 2 + tile) * kCols;
 #pragma unroll
-            for (int e = 0; e < SC / 16; ++e) {
-              const uint32_t off = (e / 4) * (kRows * 128 >> 4) + (e % 4) * 2;
-              mma_ss(tmem + (buf * 2 + tile) * kCols, ad + off, bd + off,
-                     idesc, (s | e) > 0);
-            }
-            if (st + 1 == item.steps) tc_commit(&b.k_empty[k.at]);
-            k.next();
-            q.next();
+            for (int e = 0; e < SC / 16; ++e)
+              mma_ss_one<desc_high(C::kPage)>(
+                  d, ad + (e / 4) * (2048 >> 4) + (e % 4) * 2,
+                  bd + (e / 4) * (kRows * 128 >> 4) + (e % 4) * 2, idesc,
+                  (s | e) > 0);
+            if (s == NS - 1) tc_commit_one(&b.s_full[buf][tile]);
           }
-          tc_commit(&b.s_full[buf][tile]);
+          if (st + 1 == steps) tc_commit_one(&b.k_empty[k.at]);
+          k.next();
+          q.next();
         }
         for (int s = 0; s < NS; ++s) {
-          tc_commit(&b.q_empty[q0.at]);
+          tc_commit_one(&b.q_empty[q0.at]);
           q0.next();
         }
-        if (st + 1 == item.steps) kt = k;
+        if (st + 1 == steps) kt = k;
       }
     }
   }
@@ -433,7 +431,7 @@ __device__ __forceinline__ bool fetch(const WeighParams& p, Smem& sm,
     for (int j = item.j0; j < item.j1; ++j) {
       for (int st = 0; st < item.steps; ++st, ++step) {
         if ((int)(step & 1) != which) continue;
-        const int slot = step % kSteps;
+        const int slot = step & 1;
         const int cols = min(p.tq, item.n - st * p.tq) * p.group;
         const float* lse = p.lse + (item.row0 + st * p.tq) * p.heads +
                            (int64_t)j * p.group;
@@ -441,7 +439,9 @@ __device__ __forceinline__ bool fetch(const WeighParams& p, Smem& sm,
 #pragma unroll
         for (int i = 0; i < kCols / 32; ++i)
           v[i] = lane + 32 * i < cols ? lse[at[i]] : -INFINITY;
-        if (!warp_wait(&b.l_empty[slot], ((step / kSteps) & 1) ^ 1, stop))
+        const uint32_t phase = (step >> 1) & 1;
+        if (!warp_wait(&b.s_empty[slot][0], phase ^ 1, stop) ||
+            !warp_wait(&b.s_empty[slot][1], phase ^ 1, stop))
           return false;
         uint32_t dead = 0;
 #pragma unroll
@@ -452,7 +452,7 @@ __device__ __forceinline__ bool fetch(const WeighParams& p, Smem& sm,
         }
         if (lane == 0) sm.dead[slot] = dead;
         __syncwarp();
-        if (lane == 0) mbar_arrive(&b.l_full[slot]);
+        if (lane < 2) mbar_arrive(&b.s_full[slot][lane]);
       }
     }
   }
@@ -508,8 +508,10 @@ __device__ __forceinline__ bool weigh(const WeighParams& p, Smem& sm,
     if (lane == 0) mbar_arrive(&b.item_empty[it.at]);
     it.next();
     if (item.flags & kStop) return true;
-    const int64_t t = (int64_t)item.t0 + tile * kRows + row;
-    const bool here = (item.pages >> (tile * 8 + row / kBlock)) & 1;
+    // (eight rows of each page to a tile: the pages lie one behind the other)
+    const int in_item = row / 8 * kBlock + tile * 8 + row % 8;
+    const int64_t t = (int64_t)item.t0 + in_item;
+    const bool here = (item.pages >> (row / 8)) & 1;
     // rows that attend to this token: from, ..., upto - 1
     const int64_t from = max(t - item.pf, (int64_t)0);
     int64_t upto = item.n;
@@ -520,18 +522,15 @@ __device__ __forceinline__ bool weigh(const WeighParams& p, Smem& sm,
     for (int j = item.j0; item.steps && j < item.j1; ++j) {
       for (int st = 0; st < item.steps; ++st, ++step) {
         const uint32_t buf = step & 1, phase = (step >> 1) & 1;
-        const int slot = step % kSteps;
         const int64_t first = (int64_t)st * p.tq;
         const int lo = (int)min(max(from - first, (int64_t)0),
                                 (int64_t)kCols) * p.group;
         const int hi = (int)min(max(upto - first, (int64_t)0),
                                 (int64_t)p.tq) * p.group;
         const int n = columns(p, item.n, st);
-        if (!warp_wait(&b.l_full[slot], (step / kSteps) & 1, stop))
-          return false;
-        const uint32_t dead = sm.dead[slot];
         if (!warp_wait(&b.s_full[buf][tile], phase, stop)) return false;
         tc_fence_after();
+        const uint32_t dead = sm.dead[buf];
         const uint32_t at = lanes + buf * 2 * kCols;
         int c = 0;
         float part = 0.f;
@@ -541,23 +540,20 @@ __device__ __forceinline__ bool weigh(const WeighParams& p, Smem& sm,
           tmem_wait_ld();
           const bool whole = __all_sync(~0u, lo <= c && hi >= c + 32) &&
                              !((dead >> (c / 32)) & 1);
-          part += add_columns(s, &sm.lse[slot][c], p.scale, whole, lo - c,
+          part += add_columns(s, &sm.lse[buf][c], p.scale, whole, lo - c,
                               hi - c);
         }
         if (c < n) {
           float s[16];
           tmem_ld16(at + c, s);
           tmem_wait_ld();
-          part += add_columns(s, &sm.lse[slot][c], p.scale, false, lo - c,
+          part += add_columns(s, &sm.lse[buf][c], p.scale, false, lo - c,
                               hi - c);
         }
         sum += part;
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&b.s_empty[buf][tile]);
-          mbar_arrive(&b.l_empty[slot]);
-        }
+        if (lane == 0) mbar_arrive(&b.s_empty[buf][tile]);
       }
     }
     if ((item.flags & (kStarts | kEnds)) == (kStarts | kEnds)) {
@@ -568,7 +564,7 @@ __device__ __forceinline__ bool weigh(const WeighParams& p, Smem& sm,
       }
     } else {
       p.slots[(blockIdx.x * 2 + (item.flags & kStarts ? 1 : 0)) * kTile +
-              tile * kRows + row] = sum;
+              in_item] = sum;
     }
   }
 }
@@ -596,12 +592,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&b.item_full[i], 1);
       mbar_init(&b.item_empty[i], 11);    // eight warps, MMA, two fetchers
     }
-    for (int i = 0; i < kSteps; ++i) {
-      mbar_init(&b.l_full[i], 1);
-      mbar_init(&b.l_empty[i], 8);
-    }
     for (int i = 0; i < 4; ++i) {
-      mbar_init(&b.s_full[i / 2][i % 2], 1);
+      mbar_init(&b.s_full[i / 2][i % 2], 2);    // MMA, fetcher
       mbar_init(&b.s_empty[i / 2][i % 2], 4);
     }
     mbar_init(&b.fin, 1);
@@ -660,13 +652,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == kProducer) {
     ok = produce<T, C>(p, sm, base, pre);
   } else if (warp == kMma) {
-    if (lane == 0) {
-      ok = multiply<T, C>(p, sm, base, tmem);
-      // products under way end before the block's memory is given up
-      tc_commit(&b.fin);
-      mbar_drain(&b.fin, 0);
-    }
+    ok = multiply<T, C>(p, sm, base, uniform(tmem));
+    // products under way end before the block's memory is given up
     __syncwarp();
+    tc_commit_one(&b.fin);
+    mbar_drain(&b.fin, 0);
   } else {
     ok = fetch(p, sm, warp - kFetch);
   }
@@ -779,7 +769,7 @@ int kvtc_paged_weigh(int cuda_device, int R, int64_t N, int heads,
   p.group = heads / kv_heads;
   p.tq = kCols / p.group;
   if (!encode_pages(&p.tm_k, k_cache, (uint64_t)kv_heads * head_dim,
-                    num_blocks, 1))
+                    num_blocks, head_dim == 64 ? 1 : 2))
     return KVTC_ECUDA;
   // (without rows no box is read: their maps are never made)
   for (int i = 0; N && i < kBoxes; ++i) {
