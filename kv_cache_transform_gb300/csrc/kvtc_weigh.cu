@@ -95,8 +95,9 @@ constexpr int kStarts = 1, kEnds = 2, kStop = 4;
 struct Bars {
   uint64_t k_full[4], k_empty[4], q_full[4], q_empty[4];
   uint64_t item_full[kItems], item_empty[kItems];
-  // buffer, token tile: products and log-sum-exps are there; are done with
-  uint64_t s_full[2][2], s_empty[2][2];
+  // buffer, token tile: products and log-sum-exps are there; products have
+  // been read; log-sum-exps too
+  uint64_t s_full[2][2], s_empty[2][2], l_empty[2];
   uint64_t fin;
 };
 struct Smem {
@@ -440,9 +441,7 @@ __device__ __forceinline__ bool fetch(const WeighParams& p, Smem& sm,
         for (int i = 0; i < kCols / 32; ++i)
           v[i] = lane + 32 * i < cols ? lse[at[i]] : -INFINITY;
         const uint32_t phase = (step >> 1) & 1;
-        if (!warp_wait(&b.s_empty[slot][0], phase ^ 1, stop) ||
-            !warp_wait(&b.s_empty[slot][1], phase ^ 1, stop))
-          return false;
+        if (!warp_wait(&b.l_empty[slot], phase ^ 1, stop)) return false;
         uint32_t dead = 0;
 #pragma unroll
         for (int i = 0; i < kCols / 32; ++i) {
@@ -532,28 +531,43 @@ __device__ __forceinline__ bool weigh(const WeighParams& p, Smem& sm,
         tc_fence_after();
         const uint32_t dead = sm.dead[buf];
         const uint32_t at = lanes + buf * 2 * kCols;
-        int c = 0;
         float part = 0.f;
-        for (; c + 32 <= n; c += 32) {
-          float s[32];
-          tmem_ld32(at + c, s);
+        if (n == kCols && dead == 0 && __all_sync(~0u, lo <= 0 && hi >= n)) {
+          // (read at once: the next product may go into the buffer)
+          float s[kCols];
+#pragma unroll
+          for (int c = 0; c < kCols; c += 32) tmem_ld32(at + c, s + c);
           tmem_wait_ld();
-          const bool whole = __all_sync(~0u, lo <= c && hi >= c + 32) &&
-                             !((dead >> (c / 32)) & 1);
-          part += add_columns(s, &sm.lse[buf][c], p.scale, whole, lo - c,
-                              hi - c);
-        }
-        if (c < n) {
-          float s[16];
-          tmem_ld16(at + c, s);
-          tmem_wait_ld();
-          part += add_columns(s, &sm.lse[buf][c], p.scale, false, lo - c,
-                              hi - c);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&b.s_empty[buf][tile]);
+          part = add_columns(s, sm.lse[buf], p.scale, true, 0, 0);
+        } else {
+          int c = 0;
+#pragma unroll 1
+          for (; c + 32 <= n; c += 32) {
+            float s[32];
+            tmem_ld32(at + c, s);
+            tmem_wait_ld();
+            const bool whole = __all_sync(~0u, lo <= c && hi >= c + 32) &&
+                               !((dead >> (c / 32)) & 1);
+            part += add_columns(s, &sm.lse[buf][c], p.scale, whole, lo - c,
+                                hi - c);
+          }
+          if (c < n) {
+            float s[16];
+            tmem_ld16(at + c, s);
+            tmem_wait_ld();
+            part += add_columns(s, &sm.lse[buf][c], p.scale, false, lo - c,
+                                hi - c);
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&b.s_empty[buf][tile]);
         }
         sum += part;
-        tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&b.s_empty[buf][tile]);
+        if (lane == 0) mbar_arrive(&b.l_empty[buf]);
       }
     }
     if ((item.flags & (kStarts | kEnds)) == (kStarts | kEnds)) {
@@ -595,6 +609,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 4; ++i) {
       mbar_init(&b.s_full[i / 2][i % 2], 2);    // MMA, fetcher
       mbar_init(&b.s_empty[i / 2][i % 2], 4);
+      if (i < 2) mbar_init(&b.l_empty[i], 8);
     }
     mbar_init(&b.fin, 1);
     sm.abort_flag = 0;
