@@ -14,6 +14,7 @@
 #include "../../include/kvtc.h"
 #include "kvtc_hostutil.cuh"
 #include "kvtc_internal.cuh"
+#include "ptx.cuh"
 
 namespace kvtc {
 namespace {
@@ -35,6 +36,7 @@ struct EvictParams {
   float* acc_out;
   int32_t* lens_out;
   int32_t* ids;        // [R][max_blocks * 16]: the block of a kept token
+  float* weights;      // [R][max_blocks * 16]: its weight
   unsigned* flags;
   int64_t acc_ld, num_blocks;
   int32_t R, keep, sink, window, max_blocks, in_place;
@@ -76,32 +78,64 @@ __device__ __forceinline__ uint64_t block_sums(uint64_t a, uint64_t* all,
   return upto - a + before;
 }
 
-// A block per request.  The smallest key that stays is found from the top, 11
-// bits a round: a histogram of those that agree so far, and its sums from above.
-// Then the tokens that stay are listed in order, four tokens a thread at a time.
-// (One thread that goes through the bins, 8 bits a round, and one token a
-// thread: 27 us where 64 requests up to 4K go to 1K, 70 for one of 32K.)
+// A cluster of blocks per request, each with a stretch of its tokens.  The
+// smallest key that stays is found from the top, 11 bits a round: histograms of
+// those that agree so far, added up through distributed shared memory, and their
+// sums from above.  Then the tokens that stay are listed in order, four tokens a
+// thread at a time.  (One request of 32K cut to 4K: 34 us in one block, 70 with
+// 8 bits a round, a thread that goes through the bins and one token a thread.)
+struct __align__(16) SelectShared {
+  int hist[kBins];
+  uint64_t sums[32];
+  uint64_t counts;          // of the block's tokens: above, equal
+  int pick[2];
+};
+__device__ __forceinline__ uint32_t cluster_blocks() {
+  uint32_t n;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(n));
+  return n;
+}
+// 64 bits at the same place in another block's shared memory.
+constexpr int kMaxBlocks = 8;
+__device__ __forceinline__ uint2 load2_from(const void* at, uint32_t rank) {
+  uint2 v;
+  asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];"
+               : "=r"(v.x), "=r"(v.y)
+               : "r"(mapa_shared(smem_u32(at), rank))
+               : "memory");
+  return v;
+}
+// kMany: more than one block per request.
+template <bool kMany>
 __global__ void __launch_bounds__(kSelThreads)
     select_kernel(const __grid_constant__ EvictParams p) {
-  __shared__ int hist[kBins];
-  __shared__ uint64_t sums[32];
-  __shared__ int pick[2];
+  __shared__ SelectShared sm;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int tid = threadIdx.x;
-  const int64_t r = blockIdx.x;
+  const int blocks = kMany ? (int)cluster_blocks() : 1;
+  const int rank = kMany ? (int)cluster_ctarank() : 0;
+  const auto sync = [] {
+    if (kMany) cluster_sync(); else __syncthreads();
+  };
+  const int64_t r = blockIdx.y;
   const int32_t most = p.max_blocks * kBlock;
   const int32_t asked = p.lens[r];
   const int32_t len = min(max(asked, 0), most);
   const int32_t after = min(len, p.keep);
   const float* acc = p.acc + r * p.acc_ld;
   const int32_t* row = p.table + r * p.max_blocks;
-  if (tid == 0 && asked > most && p.flags)
+  if (tid == 0 && rank == 0 && asked > most && p.flags)
     atomicOr(p.flags, KVTC_FLAG_SPACE);
   // of tokens lo .. hi - 1, `want` stay
   const int32_t lo = len > p.keep ? p.sink : len;
   const int32_t hi = len > p.keep ? len - p.window : len;
   const int32_t want = len > p.keep ? p.keep - p.sink - p.window : 0;
+  // this block's tokens
+  const int32_t each = (len / (int32_t)blocks / 16 + 1) * 16;
+  const int32_t from = (int32_t)min((int64_t)rank * each, (int64_t)len);
+  const int32_t upto = min(from + each, len);
+  const int32_t from_mid = max(from, lo), upto_mid = min(upto, hi);
   // the smallest key that stays, and how many of those equal to it
   uint32_t least = want ? 0u : ~0u;
   int equal = want;
@@ -110,71 +144,119 @@ __global__ void __launch_bounds__(kSelThreads)
       const int shift = round == 0 ? 21 : round == 1 ? 10 : 0;
       const int bits = round == 2 ? 10 : 11;
       const uint32_t known = round == 0 ? 0u : ~0u << (shift + bits);
-      for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
+      for (int i = tid; i < kBins; i += kSelThreads) sm.hist[i] = 0;
       __syncthreads();
-      constexpr int kAhead = 8;
-      for (int32_t t0 = lo + tid; t0 < hi; t0 += kAhead * kSelThreads) {
+      constexpr int kAhead = 4;
+      for (int32_t t0 = from_mid + tid; t0 < upto_mid;
+           t0 += kAhead * kSelThreads) {
         float w[kAhead];
 #pragma unroll
         for (int i = 0; i < kAhead; ++i)
-          w[i] = t0 + i * kSelThreads < hi ? acc[t0 + i * kSelThreads] : 0.f;
+          w[i] = t0 + i * kSelThreads < upto_mid ? acc[t0 + i * kSelThreads]
+                                                 : 0.f;
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
           const uint32_t key = key_of(w[i]);
-          if (t0 + i * kSelThreads < hi && (key & known) == least)
-            atomicAdd(&hist[(key >> shift) & ((1u << bits) - 1)], 1);
+          if (t0 + i * kSelThreads < upto_mid && (key & known) == least)
+            atomicAdd(&sm.hist[(key >> shift) & ((1u << bits) - 1)], 1);
         }
       }
-      __syncthreads();
+      sync();
       // thread t: bins 2047 - 2 t and 2046 - 2 t; sums from the largest
       const int b1 = kBins - 1 - 2 * tid, b0 = b1 - 1;
-      const int n1 = hist[b1], n0 = hist[b0];
-      uint64_t all;
-      const int above = (int)block_sums((uint64_t)(n0 + n1), &all, sums);
-      if (above < equal && above + n1 >= equal) {
-        pick[0] = b1;
-        pick[1] = equal - above;
-      } else if (above + n1 < equal && above + n1 + n0 >= equal) {
-        pick[0] = b0;
-        pick[1] = equal - above - n1;
+      int n1 = 0, n0 = 0;
+      {
+        // (all asked for at once)
+        uint2 v[kMaxBlocks] = {};
+        if (!kMany) v[0] = *reinterpret_cast<const uint2*>(&sm.hist[b0]);
+#pragma unroll
+        for (int k = 0; kMany && k < kMaxBlocks; ++k)
+          v[k] = k < blocks ? load2_from(&sm.hist[b0], k) : make_uint2(0, 0);
+#pragma unroll
+        for (int k = 0; k < kMaxBlocks; ++k) {
+          n0 += (int)v[k].x;
+          n1 += (int)v[k].y;
+        }
       }
-      __syncthreads();
-      least |= (uint32_t)pick[0] << shift;
-      equal = pick[1];
-      __syncthreads();
+      uint64_t all;
+      const int above = (int)block_sums((uint64_t)(n0 + n1), &all, sm.sums);
+      if (above < equal && above + n1 >= equal) {
+        sm.pick[0] = b1;
+        sm.pick[1] = equal - above;
+      } else if (above + n1 < equal && above + n1 + n0 >= equal) {
+        sm.pick[0] = b0;
+        sm.pick[1] = equal - above - n1;
+      }
+      // (all blocks have read all histograms)
+      sync();
+      least |= (uint32_t)sm.pick[0] << shift;
+      equal = sm.pick[1];
     }
   }
-  // the list: of a thread's four tokens those above `least`, and of those equal
-  // to it the first ones
-  uint32_t gone_above = 0, gone_same = 0;      // before this stretch
-  int32_t* kept = p.kept + r * (int64_t)p.keep;
-  int32_t* ids = p.ids + r * (int64_t)most;
-  float* acc_out = p.acc_out + r * p.acc_ld;
-  bool bad = false;
-  for (int32_t t0 = 0; t0 < len; t0 += 4 * kSelThreads) {
-    const int32_t t = t0 + 4 * tid;
-    // (rows of acc are as long as the table, a multiple of 16)
-    const float4 w4 = t < len ? *reinterpret_cast<const float4*>(acc + t)
-                              : make_float4(0.f, 0.f, 0.f, 0.f);
-    const float w[4] = {w4.x, w4.y, w4.z, w4.w};
-    uint64_t count = 0;
-    uint32_t what = 0;             // 2 bits a token: 1 above, 2 equal, 3 stays
+  // 2 bits a token: 1 above, 2 equal, 3 stays in any case; four from t on
+  const auto classify = [&](int32_t t, const float (&w)[4], uint64_t* count) {
+    uint32_t what = 0;
+    *count = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if (t + i >= len) continue;
-      uint32_t x;
+      if (t + i >= upto) continue;
+      uint32_t x = 3;
       if (t + i >= lo && t + i < hi) {
         const uint32_t key = key_of(w[i]);
         x = key > least ? 1u : key == least && equal ? 2u : 0u;
-      } else {
-        x = 3;
       }
       what |= x << (2 * i);
-      count += x == 1 ? 1ull : x == 2 ? 1ull << 32 : 0ull;
+      *count += x == 1 ? 1ull : x == 2 ? 1ull << 32 : 0ull;
     }
+    return what;
+  };
+  // (rows of acc are as long as the table, a multiple of 16)
+  const auto load = [&](int32_t t, float (&w)[4]) {
+    const float4 x = t < upto ? *reinterpret_cast<const float4*>(acc + t)
+                              : make_float4(0.f, 0.f, 0.f, 0.f);
+    w[0] = x.x;
+    w[1] = x.y;
+    w[2] = x.z;
+    w[3] = x.w;
+  };
+  // counts of the blocks before this one
+  uint32_t gone_above = 0, gone_same = 0;
+  if (kMany && want) {
+    uint64_t mine = 0, all;
+    for (int32_t t0 = from; t0 < upto; t0 += 4 * kSelThreads) {
+      float w[4];
+      uint64_t count;
+      load(t0 + 4 * tid, w);
+      classify(t0 + 4 * tid, w, &count);
+      mine += count;
+    }
+    block_sums(mine, &all, sm.sums);
+    if (tid == 0) sm.counts = all;
+    sync();
+    uint2 v[kMaxBlocks];
+#pragma unroll
+    for (int k = 0; k < kMaxBlocks; ++k)
+      v[k] = k < rank ? load2_from(&sm.counts, k) : make_uint2(0, 0);
+#pragma unroll
+    for (int k = 0; k < kMaxBlocks; ++k) {
+      gone_above += v[k].x;
+      gone_same += v[k].y;
+    }
+  }
+  // the list: tokens above `least`, and of those equal to it the first ones
+  int32_t* kept = p.kept + r * (int64_t)p.keep;
+  int32_t* ids = p.ids + r * (int64_t)most;
+  float* weights = p.weights + r * (int64_t)most;
+  float* acc_out = p.acc_out + r * p.acc_ld;
+  bool bad = false;
+  for (int32_t t0 = from; t0 < upto; t0 += 4 * kSelThreads) {
+    const int32_t t = t0 + 4 * tid;
+    float w[4];
+    uint64_t count, all;
+    load(t, w);
+    const uint32_t what = classify(t, w, &count);
     const int32_t id = what ? row[t / kBlock] : 0;
-    uint64_t all;
-    const uint64_t before = block_sums(count, &all, sums);
+    const uint64_t before = block_sums(count, &all, sm.sums);
     uint32_t above = gone_above + (uint32_t)before;
     uint32_t same = gone_same + (uint32_t)(before >> 32);
     gone_above += (uint32_t)all;
@@ -194,14 +276,32 @@ __global__ void __launch_bounds__(kSelThreads)
       bad |= !ok;
       kept[to] = t + i;
       ids[to] = ok ? id : -1;
-      acc_out[to] = w[i];
+      if (kMany) weights[to] = w[i]; else acc_out[to] = w[i];
     }
   }
-  __syncthreads();
-  for (int32_t t = after + tid; t < len; t += kSelThreads) acc_out[t] = 0.f;
-  for (int64_t j = after + tid; j < p.keep; j += kSelThreads) kept[j] = -1;
-  if (tid == 0) p.lens_out[r] = after;
+  // (acc_out may be acc: a stretch's places lie at or before what it reads, so
+  // one block may write them as it goes; of several, one would overtake another
+  // that still reads, so theirs wait in the workspace)
+  if (kMany) __threadfence();
+  sync();
+  const int32_t step = (int32_t)blocks * kSelThreads;
+  for (int64_t t = (kMany ? 0 : after) + (int64_t)rank * kSelThreads + tid;
+       t < len; t += step)
+    acc_out[t] = t < after ? __ldcg(weights + t) : 0.f;
+  for (int64_t j = (int64_t)after + rank * kSelThreads + tid; j < p.keep;
+       j += step)
+    kept[j] = -1;
+  if (tid == 0 && rank == 0) p.lens_out[r] = after;
   if (bad && p.flags) atomicOr(p.flags, KVTC_FLAG_BLOCK);
+}
+
+// Blocks per request: as many as the GPU holds at once, and as 4096 tokens each
+// can feed.
+int select_blocks(int R, int64_t max_blocks) {
+  int blocks = R <= 19 ? 8 : R <= 38 ? 4 : R <= 76 ? 2 : 1;
+  while (blocks > 1 && max_blocks * kBlock <= 4096ll * (blocks / 2))
+    blocks /= 2;
+  return blocks;
 }
 
 // A block takes `slice` pieces of the rows of one request in one pool, four
@@ -272,7 +372,7 @@ extern "C" {
 int64_t kvtc_paged_evict_workspace_bytes(int R, int max_blocks) {
   if (R < 0 || R > kMaxReq || max_blocks <= 0) return KVTC_EINVAL;
   if (max_blocks > kMaxTable) return KVTC_ENOTSUP;
-  return std::max<int64_t>(256, (int64_t)R * max_blocks * kBlock * 4);
+  return std::max<int64_t>(256, (int64_t)R * max_blocks * kBlock * 8);
 }
 
 int kvtc_paged_evict(int cuda_device, int R, const float* acc, int64_t acc_ld,
@@ -315,6 +415,8 @@ int kvtc_paged_evict(int cuda_device, int R, const float* acc, int64_t acc_ld,
   p.acc_out = acc_out;
   p.lens_out = lens_out;
   p.ids = static_cast<int32_t*>(workspace);
+  p.weights = reinterpret_cast<float*>(p.ids + (int64_t)R * max_blocks *
+                                                   kBlock);
   p.flags = flags;
   p.acc_ld = acc_ld;
   p.num_blocks = num_blocks;
@@ -326,8 +428,12 @@ int kvtc_paged_evict(int cuda_device, int R, const float* acc, int64_t acc_ld,
   p.in_place = out_table == block_table;
   p.pieces = D / 8;
   cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
-  if (launch_kernel(select_kernel, R, kSelThreads, 0, st, true, 0, p) !=
-      cudaSuccess)
+  const int blocks = select_blocks(R, max_blocks);
+  if ((blocks > 1
+           ? launch_kernel(select_kernel<true>, dim3(blocks, R), kSelThreads,
+                           0, st, true, blocks, p)
+           : launch_kernel(select_kernel<false>, dim3(1, R), kSelThreads, 0,
+                           st, true, 0, p)) != cudaSuccess)
     return KVTC_ECUDA;
   count_launch();
   for (int j0 = 0; j0 < nstreams; j0 += kMaxStreams) {
