@@ -1,9 +1,14 @@
 """Plain 64-bit forms of the calls around chunks of new tokens, and their
 error bounds."""
+import fractions
+import functools
+
 import numpy as np
 
 from _paged import BLOCK, UNIT, blocks_of
 
+TWO_PI = fractions.Fraction(
+    "6.283185307179586476925286766559005768394338798750211641949889")
 STEP = 2.0 ** -23           # a step of fp32, relative
 
 
@@ -40,13 +45,19 @@ def rotate(x, weight, eps, positions, inv_freq, rotary_dim, interleaved,
     return y, tol + unit * np.abs(y) * (1 + 1e-6) + 2.0 ** -26
 
 
+@functools.lru_cache(maxsize=None)
+def turns(f):
+    """f / 2 pi in whole numbers of 2^-160 turns."""
+    x = fractions.Fraction(f) / TWO_PI * 2 ** 160
+    return round(x)
+
+
 def turn_of(p, f):
-    """p f modulo 2 pi: f as a fraction of 80 binary places, exactly."""
-    import fractions
-    turns = fractions.Fraction(f) * p / fractions.Fraction(
-        "6.283185307179586476925286766559005768394338798750211641949889")
-    return float((turns - round(turns)) * fractions.Fraction(
-        "6.283185307179586476925286766559005768394338798750211641949889"))
+    """p f modulo 2 pi, to 2^-120 or so."""
+    at = p * turns(f) % 2 ** 160
+    if at >= 2 ** 159:
+        at -= 2 ** 160
+    return at / 2 ** 160 * 6.283185307179586
 
 
 # ----------------------------------------------------------------- chunks
