@@ -123,6 +123,38 @@ def test_head_layouts(kv, heads, kv_heads, hd, dtype):
     run(kv, heads + hd, NEWS, LENS, heads, kv_heads, hd, dtype)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("heads,kv_heads,hd", [
+    (2, 2, 64), (15, 3, 64), (1, 1, 128), (28, 4, 128), (9, 1, 128),
+    (2, 2, 256), (24, 2, 256)])
+def test_runs_over_a_wide_table(kv, heads, kv_heads, hd, dtype):
+    """Under a table of more than 64 columns items are dealt out in runs that
+    begin and end inside them, and joined by a second launch."""
+    case = paged_case(heads, LENS, heads, kv_heads, hd, extra_cols=70)
+    before = kv.kvtc_launch_count()
+    a = run(kv, heads, NEWS, LENS, heads, kv_heads, hd, dtype, case=case)
+    assert kv.kvtc_launch_count() == before + 2
+    # the same call under a narrow one: a block per item
+    narrow = paged_case(heads, LENS, heads, kv_heads, hd)
+    few = sum(-(-n // max(1, 128 // (heads // kv_heads))) for n in NEWS)
+    b = Chunks(kv, heads, NEWS, LENS, heads, kv_heads, hd, dtype,
+               case=narrow)
+    before = kv.kvtc_launch_count()
+    b.call()
+    b.check()
+    count = kv.kvtc_launch_count() - before
+    assert count in (1, 2) and (count == 1 or (few + 13) * kv_heads > 152)
+    assert a.R == b.R
+
+
+@pytest.mark.parametrize("new,held", [(1, 20000), (3, 4000), (200, 3000),
+                                      (64, 64000)])
+@pytest.mark.parametrize("hd", [64, 128, 256])
+def test_few_rows_over_many_blocks(kv, new, held, hd):
+    """One item cut into parts for many blocks, and their join."""
+    run(kv, new + hd, [new], [new + held], 2, 1, hd)
+
+
 @pytest.mark.parametrize("group", [5, 24, 31, 33, 64, 65, 100, 127, 128])
 def test_group_sizes(kv, group):
     run(kv, group, [3, 0, 1, 9], [70, 0, 1, 300], group, 1, 64)

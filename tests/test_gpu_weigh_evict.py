@@ -171,6 +171,25 @@ def test_weigh_sink_and_window(kv, sink, window):
     weigh(kv, 3, news, lens, 6, 2, 128, sink=sink, window=window, case=case)
 
 
+def test_weigh_without_rows(kv):
+    """No rows at all: the sums decay."""
+    import torch
+    acc = torch.rand((3, 64), device="cuda")
+    out = torch.full_like(acc, 77.0)
+    lens = torch.tensor([0, 5, 64], dtype=torch.int32, device="cuda")
+    table = torch.zeros((3, 4), dtype=torch.int32, device="cuda")
+    cu = torch.zeros(4, dtype=torch.int64, device="cuda")
+    pool = torch.zeros((1, 16, 128), dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(kv.kvtc_paged_weigh_workspace_bytes(3, 0, 8, 2, 64),
+                     dtype=torch.uint8, device="cuda")
+    kv.kvtc_paged_weigh(3, 0, 8, 2, 64, 0, None, 512, pool, 1, BLOCK, table,
+                        4, cu, lens, 0, 0, 0.125, None, 0.5, acc, out, 64,
+                        ws, ws.numel())
+    for r, n in enumerate((0, 5, 64)):
+        assert torch.equal(out[r, :n], acc[r, :n] * 0.5)
+        assert (out[r, n:] == 77).all()
+
+
 def test_weigh_odd_values(kv):
     lens = [60, 60, 60]
     case = paged_case(5, lens, 4, 2, 64)
