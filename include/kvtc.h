@@ -564,12 +564,21 @@ int64_t kvtc_paged_attend_chunks_workspace_bytes(int cuda_device, int R,
  * A row whose token is before the first (more rows than lens[r]) and a head
  * whose weights sum to zero get out = 0, lse = -inf; tokens in blocks whose
  * id is out of range are left out and flag KVTC_FLAG_BLOCK.  Infinities and
- * NaN in K, V or q reach the rows that attend to them and no others.
- * Products are summed, and the softmax statistics held, in fp32.
+ * NaN in K, V or q reach the rows that attend to them and no others (an
+ * infinity in V as an infinity, or NaN where its weight is below 2^-20).
+ * Products are summed, and the softmax statistics held, in fp32.  A weight
+ * enters its product with v as one `dtype` number (half a step of it, relative;
+ * in fp16 to 2^-32 of the largest weight at least), the sum of the weights is of
+ * the unrounded ones; exponentials and the reciprocal of their sum are the
+ * hardware's approximate ones (2^-22); out is rounded once.  The error against
+ * 64 bits is that of the output's own rounding, to a tenth.  Equal calls on one
+ * device give equal bits.
  *   head_dim 64, 128 or 256; kv_heads * head_dim <= 8192; at most 128 query
  * heads a KV head.  Alignment and overlap as for kvtc_paged_attend, cu 8.
  * workspace: device scratch of kvtc_paged_attend_chunks_workspace_bytes
- * bytes, used only while the call's work runs on cuda_stream.
+ * bytes (20 to 41 MB), used only while the call's work runs on cuda_stream:
+ * calls that may run at the same time need one each.  Two kernel launches; one
+ * where the table has at most 64 columns and there are few rows.
  * Errors: EINVAL, ESIZE, EALIGN, ENOTSUP, ECUDA.
  */
 int kvtc_paged_attend_chunks(
@@ -601,7 +610,10 @@ int64_t kvtc_paged_weigh_workspace_bytes(int cuda_device, int R, int64_t N,
  * with a cu of their own, if they are the requests' last).  Tokens in blocks
  * whose id is out of range receive nothing and, where attended, flag
  * KVTC_FLAG_BLOCK.  Sums are in fp32, in a fixed order: equal calls on one
- * device give equal bits.  acc, acc_out, q, k_cache and workspace 16-byte
+ * device give equal bits.  Two kernel launches.  workspace: device scratch of
+ * kvtc_paged_weigh_workspace_bytes bytes, used only while the call's work runs
+ * on cuda_stream; calls that may run at the same time need one each.  No output
+ * may overlap an input other than as said.  acc, acc_out, q, k_cache and workspace 16-byte
  * aligned, cu 8, the others 4.
  * Errors: EINVAL, ESIZE, EALIGN, ENOTSUP, ECUDA.
  */
@@ -647,8 +659,11 @@ int64_t kvtc_paged_evict_workspace_bytes(int R, int max_blocks);
  *   lens_out     : DEVICE int32 [R], written: min(lens[r], keep); may be lens
  *                  itself.
  * A token whose old or new block id is out of range stays in the list, its
- * rows are not written, and KVTC_FLAG_BLOCK is set.  cache, acc, acc_out and
- * workspace 16-byte aligned, acc_ld % 4 == 0, the others 4.  Other than as
+ * rows are not written, and KVTC_FLAG_BLOCK is set.  workspace: device scratch
+ * of kvtc_paged_evict_workspace_bytes bytes (8 for each token that the table
+ * has place for), used only while the call's work runs on cuda_stream; calls
+ * that may run at the same time need one each.  One kernel launch, and one per
+ * 64 pools.  cache, acc, acc_out and workspace 16-byte aligned, acc_ld % 4 == 0, the others 4.  Other than as
  * said no output may overlap an input or another output.
  * Errors: EINVAL, ESIZE, EALIGN, ENOTSUP, ECUDA.
  */
