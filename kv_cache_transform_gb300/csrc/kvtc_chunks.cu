@@ -175,7 +175,12 @@ __device__ __forceinline__ uint32_t seen_bits(const ChunkParams& p,
 }
 
 struct Bars {
-  uint64_t full[10], empty[10];    // stages
+  // A stage holds K and V in turn, and K's loads have another reader than V's:
+  // what tells that loads have landed goes by units, so that each barrier has
+  // one reader, which sees all of its phases.  (By stages, a reader of V would
+  // take the phase before K's for its own while K's loads are under way.)
+  uint64_t full[kMetas][2][2];     // K, V; stages of one
+  uint64_t empty[10];              // stages
   uint64_t q_full, q_empty;
   uint64_t item_full[kItems], item_empty[kItems];
   uint64_t meta[kMetas], clean[kMetas];       // units
@@ -208,7 +213,7 @@ __device__ __forceinline__ bool produce(const ChunkParams& p, Smem& sm,
   Turn<kItems> it;
   Turn<kMetas> mt;
   uint32_t q_phase = 0;
-  int fills = 0;                       // times that the ring went round
+  uint32_t fills = 0;                  // stages filled
   const int64_t total = pre[p.R];
   const Deal deal(total, p.whole ? 1 : kItemCost + 2);
   int64_t x = deal.begin(blockIdx.x);
@@ -348,6 +353,7 @@ __device__ __forceinline__ bool produce(const ChunkParams& p, Smem& sm,
           sm.metas[mt.at].mixed = m.mixed;
           mbar_arrive(&b.meta[mt.at]);
         }
+        const int unit = mt.at;
         mt.next();
         const uint32_t bytes = __popc(pages) * C::kSlabs * 2048;
 #pragma unroll
@@ -358,15 +364,16 @@ __device__ __forceinline__ bool produce(const ChunkParams& p, Smem& sm,
               ok = false;
               break;
             }
-            if (lane == 0) mbar_arrive_expect_tx(&b.full[st.at], bytes);
+            uint64_t* full = &b.full[unit][kv][s];
+            if (lane == 0) mbar_arrive_expect_tx(full, bytes);
             __syncwarp();
             const uint32_t to = smem + C::kRing + st.at * C::kStage;
             if (kv == 0 && fine && slab / C::kSlabs == s && slab < HD / 64)
               tma_load_4d(to + slab % C::kSlabs * (U * 128) + page * 2048,
-                          &p.tm_k, 0, 0, slab_all, id, &b.full[st.at]);
+                          &p.tm_k, 0, 0, slab_all, id, full);
             if (kv == 1 && fine && slab == 0)
               tma_load_4d(to + page * (C::kSlabs * 2048), &p.tm_v, 0, 0,
-                          slab_all + s * C::kSlabs, id, &b.full[st.at]);
+                          slab_all + s * C::kSlabs, id, full);
             st.next();
             ++fills;
           }
@@ -418,13 +425,10 @@ __device__ __forceinline__ bool produce(const ChunkParams& p, Smem& sm,
   __syncwarp();
   if (lane == 0) {
     mbar_drain(&b.q_full, q_phase ^ 1);
-    Turn<S> back = st;
-    for (int k = min(fills, S); k > 0; --k) {
-      if (back.at-- == 0) {
-        back.at = S - 1;
-        back.phase ^= 1;
-      }
-      mbar_drain(&b.full[back.at], back.phase);
+    for (uint32_t k = 1; k <= min(fills, (uint32_t)S); ++k) {
+      const uint32_t f = fills - k, unit = f / (2 * NS);
+      mbar_drain(&b.full[unit % kMetas][f / NS % 2][f % NS],
+                 unit / kMetas & 1);
     }
   }
   return ok;
@@ -445,7 +449,7 @@ __device__ __forceinline__ bool multiply(const ChunkParams& p, Smem& sm,
   volatile int* stop = &sm.abort_flag;
   Turn<S> kt, vt;                // the next tile's first stage
   Turn<kItems> it;
-  Turn<kMetas> mt;
+  Turn<kMetas> km, mt;           // K's unit, V's
   uint32_t q_phase = 0;
   uint32_t p_phase = 0;          // a bit per barrier
   const uint32_t ring = smem + C::kRing;
@@ -506,7 +510,8 @@ __device__ __forceinline__ bool multiply(const ChunkParams& p, Smem& sm,
         Turn<S> k = kt;
 #pragma unroll 1
         for (int s = 0; s < NS; ++s) {
-          if (begins && !warp_wait(&b.full[k.at], k.phase, stop)) return false;
+          if (begins && !warp_wait(&b.full[km.at][0][s], km.phase, stop))
+            return false;
           tc_fence_after();
           const uint32_t bd = desc_base(ring + k.at * C::kStage);
           const uint32_t ad = desc_base(smem + (dual ? buf : 0) *
@@ -522,6 +527,7 @@ __device__ __forceinline__ bool multiply(const ChunkParams& p, Smem& sm,
         }
         tc_commit_one(&b.s_full[buf]);
         if (ends) {
+          km.next();
           for (int s = 0; s < NS; ++s) {
             tc_commit_one(&b.empty[kt.at]);
             kt.next();
@@ -566,7 +572,7 @@ __device__ __forceinline__ bool clean(const ChunkParams& p, Smem& sm,
       uint32_t found[4] = {0, 0, 0, 0};
 #pragma unroll
       for (int s = 0; s < NS; ++s) {
-        if (!warp_wait(&b.full[st.at], st.phase, stop)) return false;
+        if (!warp_wait(&b.full[mt.at][1][s], mt.phase, stop)) return false;
         if (mixed) {
           uint8_t* tile = smem + C::kRing + st.at * C::kStage;
           // four tokens at a time, eight lanes each
@@ -979,10 +985,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   Bars& b = sm.bars;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
-    for (int i = 0; i < C::S; ++i) {
-      mbar_init(&b.full[i], 1);
-      mbar_init(&b.empty[i], 1);
-    }
+    for (int i = 0; i < kMetas * 4; ++i)
+      mbar_init(&b.full[i / 4][i / 2 % 2][i % 2], 1);
+    for (int i = 0; i < C::S; ++i) mbar_init(&b.empty[i], 1);
     mbar_init(&b.q_full, 1);
     mbar_init(&b.q_empty, 1);
     for (int i = 0; i < kItems; ++i) {

@@ -492,3 +492,66 @@ def test_joins_with_the_single_token_call(kv):
     # scores off by 2^-21 or so each: the statistics agree far closer than
     # the outputs' rounding
     assert (lse - a.lse[:4]).abs().max() < 1e-4
+
+
+@pytest.mark.parametrize("heads,kv_heads,hd", [
+    (16, 16, 128), (8, 8, 256), (24, 12, 64), (28, 4, 128)])
+def test_single_rows_over_scattered_pools(kv, heads, kv_heads, hd):
+    """Many single rows over long contexts whose pages lie far apart, so that
+    loads land in another order than they were asked for: against the plain
+    form, and call after call to the same bits."""
+    import torch
+    if torch.cuda.mem_get_info()[0] < 60 << 30:
+        pytest.skip("needs 60 GB")
+    R, D = 64, kv_heads * hd
+    rng = np.random.default_rng(hd + heads)
+    lens = rng.permutation(1 + 8191 * np.arange(R) // (R - 1))
+    blocks = -(-lens // BLOCK)
+    cols, total = int(blocks.max()), (8 << 30) // (2 * BLOCK * D)
+    table = np.full((R, cols), -1, np.int32)
+    table[np.arange(cols)[None, :] < blocks[:, None]] = rng.permutation(
+        total)[:blocks.sum()]
+    k, v = (torch.empty((total, BLOCK, D), dtype=torch.bfloat16,
+                        device="cuda").normal_() for _ in range(2))
+    q = torch.randn((R, heads * hd), device="cuda").bfloat16()
+    d_table, d_lens = torch.from_numpy(table).cuda(), torch.from_numpy(
+        lens.astype(np.int32)).cuda()
+    cu = torch.arange(R + 1, device="cuda")
+    flags = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ws = torch.empty(kv.kvtc_paged_attend_chunks_workspace_bytes(
+        R, R, heads, kv_heads, hd), dtype=torch.uint8, device="cuda")
+    first = None
+    for _ in range(4):
+        other = torch.zeros(4 << 30, dtype=torch.uint8, device="cuda")
+        out = torch.zeros_like(q)
+        lse = torch.zeros((R, heads), device="cuda")
+        kv.kvtc_paged_attend_chunks(
+            R, R, heads, kv_heads, hd, kv.KVTC_DTYPE_BF16, q, q.stride(0), k,
+            v, total, BLOCK, d_table, cols, cu, d_lens, 0, 0, hd ** -0.5,
+            out, out.stride(0), lse, ws, ws.numel(), flags=flags)
+        torch.cuda.synchronize()
+        del other
+        assert int(flags) == 0
+        if first is None:
+            first = out, lse
+        assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
+    group = heads // kv_heads
+    for r in range(0, R, 3):
+        t = torch.arange(int(lens[r]), device="cuda")
+        at = d_table[r].long()[t // BLOCK] * BLOCK + t % BLOCK
+        keys = k.view(-1, kv_heads, hd)[at].double()
+        vals = v.view(-1, kv_heads, hd)[at].double()
+        rows = q[r].double().view(kv_heads, group, hd)
+        x = torch.einsum("jgd,tjd->jgt", rows, keys) * hd ** -0.5
+        top = torch.logsumexp(x, -1)
+        p = torch.exp(x - top[..., None])
+        o = torch.einsum("jgt,tjd->jgd", p, vals)
+        # weights and outputs rounded to bf16 (2^-8 each); a score is a sum
+        # of hd products in fp32, off by less than hd 2^-24 sum |q k| scale,
+        # here below 2^-24 hd^1.5 < 2^-12
+        most = torch.einsum("jgt,tjd->jgd", p, vals.abs())
+        tol = (2.0 ** -8 + 2.0 ** -11) * most + 2.0 ** -8 * o.abs() * 1.01
+        off = (out[r].double().view(kv_heads, group, hd) - o).abs()
+        assert (off <= tol).all(), (r, float((off - tol).max()))
+        assert (lse[r].double().view(kv_heads, group) - top).abs().max() < (
+            2.0 ** -11)
