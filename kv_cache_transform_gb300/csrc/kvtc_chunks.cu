@@ -86,6 +86,7 @@ struct ChunkParams {
   int32_t R, heads, kv_heads, max_blocks, sink, window;
   int32_t group, tq;        // query heads a KV head; tokens per row tile
   int32_t whole;            // a block per item: nothing to be joined
+  int32_t split;            // items, where there are few; or 0
 };
 
 template <int HD_>
@@ -1112,68 +1113,121 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kMma) tmem_dealloc(tmem, 512);
 }
 
-// Parts of items that cross blocks: block x joins the one begun in block x,
-// row tile y, 32 channels z; a thread per row.
-template <class T, int HD>
-__global__ void __launch_bounds__(kRows)
-    chunk_join_kernel(const __grid_constant__ ChunkParams p) {
-  using C = Cfg<HD>;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int c = blockIdx.x, tile = blockIdx.y, ch = blockIdx.z * 32;
-  const JoinDesc d = p.desc[c];
-  if (d.r < 0) return;
-  const int row = threadIdx.x;
-  const int tok = row / p.group, head = row - tok * p.group;
-  const int32_t mine = tile * p.tq + tok;
-  if (tok >= p.tq || mine >= d.ntok) return;
-  auto part_of = [&](int i) {
-    return p.slots +
-           ((int64_t)((c + i) * 2 + (i == 0 ? 1 : 0)) * C::QT + tile) *
-               C::kPart;
-  };
-  const int parts = d.last - c + 1;
-  float m = -INFINITY, l = 0.f, o[32];
-#pragma unroll
-  for (int e = 0; e < 32; ++e) o[e] = 0.f;
-  for (int i = 0; i < parts; ++i) {
-    const float* part = part_of(i);
-    const float mi = part[HD * kRows + row];
-    const float li = part[HD * kRows + kRows + row];
-    float4 x[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      x[e] = reinterpret_cast<const float4*>(part)[(ch / 4 + e) * kRows + row];
+// Parts of items that cross blocks: block x joins the one begun in block x (or
+// where there are few, the x-th of them), row tile y, 16 channels z.  A thread
+// has a row and every kSplit-th part; the threads of a row then join theirs by
+// halves.
+constexpr int kJoinCh = 16;
+struct Joined {
+  float m, l, o[kJoinCh];
+  __device__ __forceinline__ void add(float mi, float li,
+                                      const float (&x)[kJoinCh]) {
     const float top = fmaxf(m, mi);
     const float base = top == -INFINITY ? 0.f : top;
     const float fo = exp2_fast(m - base), fi = exp2_fast(mi - base);
     m = top;
     l = l * fo + li * fi;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      o[4 * e] = o[4 * e] * fo + x[e].x * fi;
-      o[4 * e + 1] = o[4 * e + 1] * fo + x[e].y * fi;
-      o[4 * e + 2] = o[4 * e + 2] * fo + x[e].z * fi;
-      o[4 * e + 3] = o[4 * e + 3] * fo + x[e].w * fi;
-    }
+    for (int e = 0; e < kJoinCh; ++e) o[e] = o[e] * fo + x[e] * fi;
   }
-  const float inv = l == 0.f ? 0.f : rcp_fast(l);
+};
+template <class T, int HD, int kSplit>
+__global__ void __launch_bounds__(kRows * kSplit)
+    chunk_join_kernel(const __grid_constant__ ChunkParams p) {
+  using C = Cfg<HD>;
+  constexpr int kHalf = kSplit > 1 ? kSplit / 2 : 1;
+  __shared__ float other[kHalf][kJoinCh + 2][kRows];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int tile = blockIdx.y, ch = blockIdx.z * kJoinCh;
+  int c = blockIdx.x;
+  if (kSplit > 1) {
+    // the c-th block that began an item that is to be joined
+    constexpr int kEach = (kCtas + 31) / 32;
+    uint32_t began[kEach];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int at = 32 * i + (int)lane_id();
+      began[i] = __ballot_sync(~0u, at < kCtas && p.desc[at].r >= 0);
+    }
+    int left = c;
+    c = -1;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int n = __popc(began[i]);
+      if (left >= 0 && left < n) c = 32 * i + (int)__fns(began[i], 0, left + 1);
+      left -= n;
+    }
+    if (c < 0) return;
+  }
+  const JoinDesc d = p.desc[c];
+  if (d.r < 0) return;
+  const int row = threadIdx.x % kRows, group = threadIdx.x / kRows;
+  const int tok = row / p.group, head = row - tok * p.group;
+  const int32_t mine = tile * p.tq + tok;
+  const bool valid = tok < p.tq && mine < d.ntok;
+  const int parts = valid ? d.last - c + 1 : 0;
+  Joined a;
+  a.m = -INFINITY;
+  a.l = 0.f;
+#pragma unroll
+  for (int e = 0; e < kJoinCh; ++e) a.o[e] = 0.f;
+#pragma unroll 2
+  for (int i = group; i < parts; i += kSplit) {
+    const float* part =
+        p.slots +
+        ((int64_t)((c + i) * 2 + (i == 0 ? 1 : 0)) * C::QT + tile) * C::kPart;
+    const float mi = part[HD * kRows + row];
+    const float li = part[HD * kRows + kRows + row];
+    float x[kJoinCh];
+#pragma unroll
+    for (int e = 0; e < kJoinCh; e += 4) {
+      const float4 w = reinterpret_cast<const float4*>(
+          part)[(ch + e) / 4 * kRows + row];
+      x[e] = w.x;
+      x[e + 1] = w.y;
+      x[e + 2] = w.z;
+      x[e + 3] = w.w;
+    }
+    a.add(mi, li, x);
+  }
+#pragma unroll
+  for (int half = kSplit / 2; half; half /= 2) {
+    if (group >= half && group < 2 * half) {
+      float(&to)[kJoinCh + 2][kRows] = other[group - half];
+      to[kJoinCh][row] = a.m;
+      to[kJoinCh + 1][row] = a.l;
+#pragma unroll
+      for (int e = 0; e < kJoinCh; ++e) to[e][row] = a.o[e];
+    }
+    __syncthreads();
+    if (group < half) {
+      const float(&from)[kJoinCh + 2][kRows] = other[group];
+      float x[kJoinCh];
+#pragma unroll
+      for (int e = 0; e < kJoinCh; ++e) x[e] = from[e][row];
+      a.add(from[kJoinCh][row], from[kJoinCh + 1][row], x);
+    }
+    __syncthreads();
+  }
+  if (!valid || group) return;
+  const float inv = a.l == 0.f ? 0.f : rcp_fast(a.l);
   const int64_t n = d.row0 + mine;
   const int h = d.j * p.group + head;
   T* out = static_cast<T*>(p.out) + n * p.out_ld + (int64_t)h * HD + ch;
 #pragma unroll
-  for (int e = 0; e < 32; e += 8) {
+  for (int e = 0; e < kJoinCh; e += 8) {
     uint32_t w[4];
 #pragma unroll
     for (int f = 0; f < 4; ++f)
-      w[f] = Elem<T>::pack(l == 0.f ? 0.f : o[e + 2 * f] * inv,
-                           l == 0.f ? 0.f : o[e + 2 * f + 1] * inv);
+      w[f] = Elem<T>::pack(a.l == 0.f ? 0.f : a.o[e + 2 * f] * inv,
+                           a.l == 0.f ? 0.f : a.o[e + 2 * f + 1] * inv);
     *reinterpret_cast<uint4*>(out + e) = make_uint4(w[0], w[1], w[2], w[3]);
   }
   if (p.lse && ch == 0)
     p.lse[n * p.heads + h] =
-        l == 0.f ? -INFINITY
-                 : (m + (log2f(l) - Elem<T>::kShift)) * kLn2;
+        a.l == 0.f ? -INFINITY
+                   : (a.m + (log2f(a.l) - Elem<T>::kShift)) * kLn2;
 }
 
 template <class T, int HD>
@@ -1187,8 +1241,11 @@ cudaError_t launch_as(const ChunkParams& p, int device, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   count_launch();
   if (p.whole) return e;
-  e = launch_kernel(chunk_join_kernel<T, HD>, dim3(kCtas, C::QT, HD / 32),
-                    kRows, 0, st, true, 0, p);
+  const dim3 grid(p.split ? p.split : kCtas, C::QT, HD / kJoinCh);
+  e = p.split ? launch_kernel(chunk_join_kernel<T, HD, 8>, grid, kRows * 8, 0,
+                              st, true, 0, p)
+              : launch_kernel(chunk_join_kernel<T, HD, 1>, grid, kRows, 0, st,
+                              true, 0, p);
   if (e == cudaSuccess) count_launch();
   return e;
 }
@@ -1297,6 +1354,11 @@ int kvtc_paged_attend_chunks(
   const int per = p.tq * (head_dim == 256 ? 1 : 2);
   const int64_t items = (int64_t)kv_heads * ((N + per - 1) / per + R);
   p.whole = items <= kCtas && max_blocks <= 8 * 128 / kBlock;
+  // Few items are cut into many parts each, which eight threads a row join (64
+  // rows behind 128K tokens, one head: 95 us a call with one thread a row, 31 with
+  // eight; 36 items 43 and 40).  More items have few parts, and so many threads
+  // cost more than they save (68 items 60 and 66, 144 items 43 and 67).
+  p.split = items <= kCtas / 4 ? (int32_t)items : 0;
   cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
   const cudaError_t e = dtype == KVTC_DTYPE_BF16
                             ? launch<__nv_bfloat16>(p, head_dim, cuda_device, st)
