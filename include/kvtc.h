@@ -613,8 +613,8 @@ int64_t kvtc_paged_weigh_workspace_bytes(int cuda_device, int R, int64_t N,
  * device give equal bits.  Two kernel launches.  workspace: device scratch of
  * kvtc_paged_weigh_workspace_bytes bytes, used only while the call's work runs
  * on cuda_stream; calls that may run at the same time need one each.  No output
- * may overlap an input other than as said.  acc, acc_out, q, k_cache and workspace 16-byte
- * aligned, cu 8, the others 4.
+ * may overlap an input other than as said.  acc, acc_out, q, k_cache and
+ * workspace 16-byte aligned, cu 8, the others 4.
  * Errors: EINVAL, ESIZE, EALIGN, ENOTSUP, ECUDA.
  */
 int kvtc_paged_weigh(int cuda_device, int R, int64_t N, int heads,

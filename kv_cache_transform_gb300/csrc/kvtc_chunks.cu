@@ -20,8 +20,8 @@
 //   producer   goes through the run: item descriptors, Q, and the pages of K
 //              and V by TMA into a ring of stages (128 tokens x up to 128
 //              channels each);
-//   MMA        a thread issues S = Q K^T and O += P V (tcgen05, S, P and O in
-//              TMEM, P over the S that it came from);
+//   MMA        issues S = Q K^T and O += P V (tcgen05, S, P and O in TMEM, P
+//              over the S that it came from);
 //   softmax    two warpgroups, a thread per row;
 //   cleaner    rows of V in units that not every row attends to whole: those
 //              that none attends to are zeroed, and infinities and NaN taken
@@ -104,7 +104,7 @@ struct Cfg {
   static constexpr int kQ = QT * kRows * HD * 2;
   static constexpr int kRing = kQ;
   static constexpr int kMisc = kRing + S * kStage;
-  static constexpr int kBytes = kMisc + 3072;
+  static constexpr int kBytes = kMisc + 2560;
   static_assert(kBytes <= 232448 && kMisc % 1024 == 0, "shared memory of a block");
   static_assert(S * kStage >= 8 * (kMaxReq + 1), "prefix of the requests");
   // TMEM columns
@@ -199,7 +199,7 @@ struct Smem {
   uint32_t tmem;
   int abort_flag;
 };
-static_assert(sizeof(Smem) <= 3072, "the kernels' shared variables");
+static_assert(sizeof(Smem) <= 2560, "the kernels' shared variables");
 
 // --------------------------------------------------------------- producer
 template <class T, class C>
@@ -314,7 +314,7 @@ __device__ __forceinline__ bool produce(const ChunkParams& p, Smem& sm,
       }
       it.next();
       const int32_t* row = p.table + (int64_t)r * p.max_blocks;
-      // lane l: page l % 8, slab l / 8
+      // a lane has a page and a slab of K
       const int page = lane % kPages, slab = lane / kPages;
       const int slab_all = j * (HD / 64) + slab;
       auto id_at = [&](int64_t k) -> int32_t {

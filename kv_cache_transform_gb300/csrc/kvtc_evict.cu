@@ -1,9 +1,9 @@
 // Eviction from paged pools by weights per token: of a request longer than
 // `keep`, the first `sink`, the last `window` and, of the others, those of the
 // greatest weight stay, in their order.
-//   select_kernel  a block per request finds the smallest weight that stays
-//     by its bits, eight at a time (histograms), then lists the tokens in
-//     order by sums over the block, and moves their weights.
+//   select_kernel  one to eight blocks per request find the smallest weight
+//     that stays by its bits, eleven at a time (histograms), then list the
+//     tokens in order by sums over the blocks, and move their weights.
 //   move_kernel    rows of all pools by that list.
 #include <cuda_runtime.h>
 

@@ -6,8 +6,8 @@
 //
 // The products are formed transposed, S^T = K Q^T: 128 tokens (eight of each of
 // 16 pages) fill the 128 lanes of TMEM and the (row, head) pairs of a KV head
-// the columns, so that a thread owns a token, adds up its columns in a register, and nothing is
-// summed across threads.  Few pairs (a decode step: the heads of one row) make
+// the columns, so that a thread owns a token, adds up its columns in a
+// register, and nothing is summed across threads.  Few pairs (a decode step: the heads of one row) make
 // a narrow product, down to 16 columns.
 //
 // Work.  An item is (request, 256 tokens), a unit one KV head of an item.  All
