@@ -610,7 +610,9 @@ int64_t kvtc_paged_weigh_workspace_bytes(int cuda_device, int R, int64_t N,
  * with a cu of their own, if they are the requests' last).  Tokens in blocks
  * whose id is out of range receive nothing and, where attended, flag
  * KVTC_FLAG_BLOCK.  Sums are in fp32, in a fixed order: equal calls on one
- * device give equal bits.  Two kernel launches.  workspace: device scratch of
+ * device give equal bits.  A weight is off, relative, by its score's error (a
+ * sum of head_dim products in fp32) and by 2^-22 (1 + |lse|).  Two kernel
+ * launches.  workspace: device scratch of
  * kvtc_paged_weigh_workspace_bytes bytes, used only while the call's work runs
  * on cuda_stream; calls that may run at the same time need one each.  No output
  * may overlap an input other than as said.  acc, acc_out, q, k_cache and

@@ -10,6 +10,14 @@
 // register, and nothing is summed across threads.  Few pairs (a decode step: the heads of one row) make
 // a narrow product, down to 16 columns.
 //
+// Rounding.  Scores are summed by the tensor cores in fp32, which cut a sum off
+// where others round it, so that weights are too small by half a step of the
+// score (one of 20 in natural units: 5e-7) rather than off to either side;
+// scale s - lse is formed in one instruction, in log2, the sums in fp32.  (The
+// difference formed before the factor log2 e, and half a step given back: 1.4
+// times as far from 64 bits as fp32 throughout instead of 1.9 times, and 99 us
+// instead of 93 for 16 requests of 32 rows.)
+//
 // Work.  An item is (request, 256 tokens), a unit one KV head of an item.  All
 // units are dealt out to one block per SM in equal runs; a block whose run
 // begins or ends inside an item leaves its part of the sums, which
