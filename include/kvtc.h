@@ -665,8 +665,9 @@ int64_t kvtc_paged_evict_workspace_bytes(int R, int max_blocks);
  * of kvtc_paged_evict_workspace_bytes bytes (8 for each token that the table
  * has place for), used only while the call's work runs on cuda_stream; calls
  * that may run at the same time need one each.  One kernel launch, and one per
- * 64 pools.  cache, acc, acc_out and workspace 16-byte aligned, acc_ld % 4 == 0, the others 4.  Other than as
- * said no output may overlap an input or another output.
+ * 64 pools.  cache, acc, acc_out and workspace 16-byte aligned, acc_ld % 4 ==
+ * 0, the others 4.  Other than as said no output may overlap an input or
+ * another output.
  * Errors: EINVAL, ESIZE, EALIGN, ENOTSUP, ECUDA.
  */
 int kvtc_paged_evict(int cuda_device, int R, const float* acc, int64_t acc_ld,
