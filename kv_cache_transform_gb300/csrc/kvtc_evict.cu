@@ -113,8 +113,8 @@ __global__ void __launch_bounds__(kSelThreads)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int tid = threadIdx.x;
-  const int blocks = kMany ? (int)cluster_blocks() : 1;
-  const int rank = kMany ? (int)cluster_ctarank() : 0;
+  const uint32_t blocks = kMany ? cluster_blocks() : 1;
+  const uint32_t rank = kMany ? cluster_ctarank() : 0;
   const auto sync = [] {
     if (kMany) cluster_sync(); else __syncthreads();
   };
@@ -131,11 +131,14 @@ __global__ void __launch_bounds__(kSelThreads)
   const int32_t lo = len > p.keep ? p.sink : len;
   const int32_t hi = len > p.keep ? len - p.window : len;
   const int32_t want = len > p.keep ? p.keep - p.sink - p.window : 0;
-  // this block's tokens
-  const int32_t each = (len / (int32_t)blocks / 16 + 1) * 16;
-  const int32_t from = (int32_t)min((int64_t)rank * each, (int64_t)len);
-  const int32_t upto = min(from + each, len);
-  const int32_t from_mid = max(from, lo), upto_mid = min(upto, hi);
+  // This block's tokens.  (Places of tokens are unsigned: a request may have up
+  // to 2^31 - 32 of them, and a stretch or a step of the block's threads that
+  // begins before that may end behind 2^31.)
+  const uint32_t each = ((uint32_t)len / blocks / 16 + 1) * 16;
+  const uint32_t from = min(rank * each, (uint32_t)len);
+  const uint32_t upto = min(from + each, (uint32_t)len);
+  const uint32_t from_mid = max(from, (uint32_t)lo);
+  const uint32_t upto_mid = min(upto, (uint32_t)hi);
   // the smallest key that stays, and how many of those equal to it
   uint32_t least = want ? 0u : ~0u;
   int equal = want;
@@ -147,7 +150,7 @@ __global__ void __launch_bounds__(kSelThreads)
       for (int i = tid; i < kBins; i += kSelThreads) sm.hist[i] = 0;
       __syncthreads();
       constexpr int kAhead = 4;
-      for (int32_t t0 = from_mid + tid; t0 < upto_mid;
+      for (uint32_t t0 = from_mid + tid; t0 < upto_mid;
            t0 += kAhead * kSelThreads) {
         float w[kAhead];
 #pragma unroll
@@ -194,14 +197,14 @@ __global__ void __launch_bounds__(kSelThreads)
     }
   }
   // 2 bits a token: 1 above, 2 equal, 3 stays in any case; four from t on
-  const auto classify = [&](int32_t t, const float (&w)[4], uint64_t* count) {
+  const auto classify = [&](uint32_t t, const float (&w)[4], uint64_t* count) {
     uint32_t what = 0;
     *count = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (t + i >= upto) continue;
       uint32_t x = 3;
-      if (t + i >= lo && t + i < hi) {
+      if (t + i >= (uint32_t)lo && t + i < (uint32_t)hi) {
         const uint32_t key = key_of(w[i]);
         x = key > least ? 1u : key == least && equal ? 2u : 0u;
       }
@@ -211,7 +214,7 @@ __global__ void __launch_bounds__(kSelThreads)
     return what;
   };
   // (rows of acc are as long as the table, a multiple of 16)
-  const auto load = [&](int32_t t, float (&w)[4]) {
+  const auto load = [&](uint32_t t, float (&w)[4]) {
     const float4 x = t < upto ? *reinterpret_cast<const float4*>(acc + t)
                               : make_float4(0.f, 0.f, 0.f, 0.f);
     w[0] = x.x;
@@ -223,7 +226,7 @@ __global__ void __launch_bounds__(kSelThreads)
   uint32_t gone_above = 0, gone_same = 0;
   if (kMany && want) {
     uint64_t mine = 0, all;
-    for (int32_t t0 = from; t0 < upto; t0 += 4 * kSelThreads) {
+    for (uint32_t t0 = from; t0 < upto; t0 += 4 * kSelThreads) {
       float w[4];
       uint64_t count;
       load(t0 + 4 * tid, w);
@@ -249,8 +252,8 @@ __global__ void __launch_bounds__(kSelThreads)
   float* weights = p.weights + r * (int64_t)most;
   float* acc_out = p.acc_out + r * p.acc_ld;
   bool bad = false;
-  for (int32_t t0 = from; t0 < upto; t0 += 4 * kSelThreads) {
-    const int32_t t = t0 + 4 * tid;
+  for (uint32_t t0 = from; t0 < upto; t0 += 4 * kSelThreads) {
+    const uint32_t t = t0 + 4 * tid;
     float w[4];
     uint64_t count, all;
     load(t, w);
@@ -267,14 +270,14 @@ __global__ void __launch_bounds__(kSelThreads)
       const uint32_t x = (what >> (2 * i)) & 3;
       int32_t to = -1;
       if (x == 3)
-        to = t + i < lo ? t + i : t + i - (hi - lo) + want;
+        to = (int32_t)(t + i < (uint32_t)lo ? t + i : t + i - (hi - lo) + want);
       else if (x == 1 || (x == 2 && same < (uint32_t)equal))
         to = lo + (int32_t)(above + min(same, (uint32_t)equal));
       above += x == 1;
       same += x == 2;
       if (to < 0) continue;
       bad |= !ok;
-      kept[to] = t + i;
+      kept[to] = (int32_t)(t + i);
       ids[to] = ok ? id : -1;
       if (kMany) weights[to] = w[i]; else acc_out[to] = w[i];
     }
@@ -285,11 +288,11 @@ __global__ void __launch_bounds__(kSelThreads)
   if (kMany) __threadfence();
   sync();
   const int32_t step = (int32_t)blocks * kSelThreads;
-  for (int64_t t = (kMany ? 0 : after) + (int64_t)rank * kSelThreads + tid;
+  const int32_t first = (int32_t)rank * kSelThreads + tid;
+  for (int64_t t = (int64_t)(kMany ? 0 : after) + first;
        t < len; t += step)
     acc_out[t] = t < after ? __ldcg(weights + t) : 0.f;
-  for (int64_t j = (int64_t)after + rank * kSelThreads + tid; j < p.keep;
-       j += step)
+  for (int64_t j = (int64_t)after + first; j < p.keep; j += step)
     kept[j] = -1;
   if (tid == 0 && rank == 0) p.lens_out[r] = after;
   if (bad && p.flags) atomicOr(p.flags, KVTC_FLAG_BLOCK);

@@ -453,3 +453,67 @@ def test_evict_twice_in_place(kv):
     b.d_kept = torch.full((3, 100), 55, dtype=torch.int32, device="cuda")
     b.call()
     b.check()
+
+
+@pytest.mark.parametrize("short", [0, 100, 4000])
+def test_evict_the_widest_table(kv, short):
+    """A request of up to 2^31 - 32 tokens, whose columns share one block but
+    for those of the tokens that stay."""
+    import torch
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB")
+    cols, sink, window, D = 2 ** 27 - 2, 3, 40, 16
+    n = cols * BLOCK - short
+    rng = np.random.default_rng(short)
+    # weights below 1 but for 300 heavier ones, and 50 of exactly 1, of which
+    # the first 20 stay; around the ends of the blocks' stretches and of the
+    # widest 32-bit numbers
+    near = [e for c in range(1, 8) for e in (c * (n // 8) - 9,
+                                             c * (n // 8) + 60)]
+    near += [sink, n - window - 1, n - 4200, n - 4096]
+    some = np.unique(np.concatenate([near, rng.integers(sink, n - window,
+                                                        400)]))
+    some = np.sort(rng.permutation(some)[:350])
+    same = np.sort(rng.permutation(350)[:50])
+    heavy = np.delete(some, same)
+    keep = sink + window + 300 + 20
+    kept = np.sort(np.concatenate([np.arange(sink), heavy, some[same][:20],
+                                   np.arange(n - window, n)]))
+    acc = torch.empty(cols * BLOCK, device="cuda").uniform_(0, 0.999)
+    weight = 2 + rng.random(300).astype(np.float32)
+    acc[torch.from_numpy(heavy).cuda()] = torch.from_numpy(weight).cuda()
+    acc[torch.from_numpy(some[same]).cuda()] = 1.0
+    # token t in column t / 16; the columns of the tokens that stay have
+    # blocks of their own
+    used = np.unique(kept // BLOCK)
+    new = blocks_of(keep)
+    total = 1 + len(used) + new
+    table = torch.zeros(cols, dtype=torch.int32, device="cuda")
+    table[torch.from_numpy(used).cuda()] = torch.arange(
+        1, 1 + len(used), dtype=torch.int32, device="cuda")
+    out_table = torch.full_like(table, -1)
+    out_table[:new] = torch.arange(total - new, total, dtype=torch.int32,
+                                   device="cuda")
+    pool = rng.integers(-30000, 30000, (total, BLOCK, D)).astype(np.int16)
+    d_pool = torch.from_numpy(pool).cuda()
+    lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+    d_kept = torch.full((1, keep), 55, dtype=torch.int32, device="cuda")
+    flags = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ws = torch.empty(kv.kvtc_paged_evict_workspace_bytes(1, cols),
+                     dtype=torch.uint8, device="cuda")
+    moved = acc[torch.from_numpy(kept).cuda()]
+    tail = acc[n:].clone()
+    kv.kvtc_paged_evict(1, acc, cols * BLOCK, lens, keep, sink, window, table,
+                        out_table, cols, BLOCK, [d_pool], D, total, d_kept,
+                        acc, lens, ws, ws.numel(), flags)
+    torch.cuda.synchronize()
+    assert int(flags) == 0 and int(lens) == keep
+    np.testing.assert_array_equal(d_kept[0].cpu().numpy(), kept)
+    assert torch.equal(acc[:keep], moved)
+    for a in range(keep, n, 1 << 28):
+        assert not acc[a:min(a + (1 << 28), n)].any()
+    assert torch.equal(acc[n:], tail)
+    j = np.arange(keep)
+    pool[total - new + j // BLOCK, j % BLOCK] = pool[
+        1 + np.searchsorted(used, kept // BLOCK), kept % BLOCK]
+    np.testing.assert_array_equal(d_pool.cpu().numpy(), pool)
