@@ -112,6 +112,11 @@ __device__ __forceinline__ uint32_t odd_of(uint32_t w) {
   return ((w & Elem<T>::kExp) + Elem<T>::kOne) & 0x80008000u;
 }
 
+// Parts of up to `of` that n >= 0 falls into.  (n + of - 1 may lie behind
+// 2^31.)
+__device__ __forceinline__ int32_t parts_of(int32_t n, int32_t of) {
+  return n / of + (n % of != 0);
+}
 // A request's rows and length.
 struct Request {
   int64_t c0;

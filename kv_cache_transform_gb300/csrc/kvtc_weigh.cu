@@ -124,10 +124,10 @@ static_assert(sizeof(Smem) <= 2048, "the kernel's shared variables");
 struct Tiles {
   int32_t all, live, front, gap, steps;
   __device__ __forceinline__ Tiles(const WeighParams& p, const Request& q) {
-    all = (q.len + kTile - 1) / kTile;
+    all = parts_of(q.len, kTile);
     front = live = q.n ? all : 0;
     gap = 0;
-    steps = (q.n + p.tq - 1) / p.tq;
+    steps = parts_of(q.n, p.tq);
     if (p.window && q.n) {
       const int64_t lo = (int64_t)q.len - q.n - p.window + 1;
       const int32_t back = lo > 0 ? (int32_t)min(lo / kTile, (int64_t)all) : 0;

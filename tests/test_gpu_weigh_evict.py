@@ -248,6 +248,44 @@ def test_weigh_equal_bits_and_graph(kv):
     a.check()
 
 
+@pytest.mark.parametrize("last", [64, 61])
+def test_weigh_the_widest_table(kv, last):
+    """A request of about 2^31 tokens: its first and last blocks receive what
+    those of a short one do, the tokens between them decay."""
+    import torch
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB")
+    a = Weigh(kv, 8, [20, 3], [last, 50], 4, 2, 64, sink=3, window=20,
+              decay=0.5)
+    ref, tol = _chunks.weigh(a.q, a.k, a.table, a.cu, a.lens, a.sink,
+                             a.window, a.scale, a.lse, a.decay, a.acc)
+    cols = 2 ** 27 - 2
+    end = BLOCK * cols                       # of the last block
+    n = end - 64 + last
+    wide = torch.zeros((2, cols), dtype=torch.int32, device="cuda")
+    wide[0, 0] = a.d_table[0, 0]
+    wide[0, cols - 3:] = a.d_table[0, 1:4]
+    wide[1, :5] = a.d_table[1, :5]
+    a.d_table, a.ld = wide, end
+    acc = torch.full((2, end), 0.75, device="cuda")
+    acc[0, :16] = a.d_acc[0, :16]
+    acc[0, end - 48:] = a.d_acc[0, 16:64]
+    acc[1, :50] = a.d_acc[1, :50]
+    behind = acc[0, n:].clone()
+    a.d_acc = a.d_out = acc
+    a.d_lens.copy_(torch.tensor([n, 50]))
+    a.call()
+    torch.cuda.synchronize()
+    assert int(a.flags) == 0
+    got = torch.cat([acc[0, :16], acc[0, end - 48:n]]).double().cpu().numpy()
+    assert (np.abs(got - ref[0, :last]) <= tol[0, :last]).all()
+    got = acc[1, :50].double().cpu().numpy()
+    assert (np.abs(got - ref[1, :50]) <= tol[1, :50]).all()
+    for at in range(16, end - 48, 1 << 28):
+        assert (acc[0, at:min(at + (1 << 28), end - 48)] == 0.375).all()
+    assert torch.equal(acc[0, n:], behind) and (acc[1, 50:4096] == 0.75).all()
+
+
 # ------------------------------------------------------------------ evict
 class Evict:
     def __init__(self, kv, seed, lens, keep, sink, window, D=64, streams=2,
