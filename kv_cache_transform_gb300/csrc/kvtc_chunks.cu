@@ -160,7 +160,7 @@ __device__ __noinline__ int64_t item_cost(const ChunkParams& p,
                                              int32_t n, int32_t len, int32_t i,
                                              int32_t per) {
   if (p.whole) return 1;
-  const int32_t first = i * per, last = min(first + per, n) - 1;
+  const int32_t first = i * per, last = first + min(per, n - first) - 1;
   return Span<U>(p, len - n + first, len - n + last).units + kItemCost;
 }
 // Which of the tokens t0 + 32 w .. + 31 the row at `pos` attends to.
@@ -236,7 +236,7 @@ __device__ __forceinline__ bool produce(const ChunkParams& p, Smem& sm,
     j = (int)(y / head);
     y -= j * head;
     // the item, 32 at a time
-    const int items = (q.n + per - 1) / per;
+    const int items = parts_of(q.n, per);
     for (;;) {
       const int64_t cost =
           i + lane < items ? item_cost<C::U>(p, q.n, q.len, i + lane, per) : 0;
@@ -271,7 +271,7 @@ __device__ __forceinline__ bool produce(const ChunkParams& p, Smem& sm,
     const Request q(__shfl_sync(~0u, batch.c0, r - base),
                     __shfl_sync(~0u, batch.n, r - base),
                     __shfl_sync(~0u, batch.len, r - base));
-    const int items = (q.n + per - 1) / per;
+    const int items = parts_of(q.n, per);
     if (items == 0) {
       ++r;
       continue;
@@ -1025,7 +1025,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int32_t per = C::QT * p.tq;
   for (int r0 = warp * 32; r0 < p.R; r0 += kThreads) {
     const Request q = request(p, r0 + lane);
-    const int items = (q.n + per - 1) / per;
+    const int items = parts_of(q.n, per);
     int64_t cost = 0;
     constexpr int kOwn = 4;             // items that a lane sums itself
     if (items <= kOwn)
@@ -1036,7 +1036,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int32_t n = __shfl_sync(~0u, q.n, l);
       const int32_t len = __shfl_sync(~0u, q.len, l);
       int64_t part = 0;
-      for (int i = lane; i < (n + per - 1) / per; i += 32)
+      for (int i = lane; i < parts_of(n, per); i += 32)
         part += item_cost<C::U>(p, n, len, i, per);
 #pragma unroll
       for (int d = 16; d; d >>= 1) part += __shfl_xor_sync(~0u, part, d);
