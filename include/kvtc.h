@@ -570,9 +570,13 @@ int64_t kvtc_paged_attend_chunks_workspace_bytes(int cuda_device, int R,
  * enters its product with v as one `dtype` number (half a step of it, relative;
  * in fp16 to 2^-32 of the largest weight at least), the sum of the weights is of
  * the unrounded ones; exponentials and the reciprocal of their sum are the
- * hardware's approximate ones (2^-22); out is rounded once.  The error against
- * 64 bits is that of the output's own rounding, to a tenth.  Equal calls on one
- * device give equal bits.
+ * hardware's approximate ones (2^-22); out is rounded once.  Against 64 bits the
+ * weights' rounding adds up to half a step of `dtype`, relative, of
+ * sum_t e^(s_t - lse) |v_t| to the half step of out.  In the 2-norm the error is
+ * that of out's own rounding, to a tenth, where V's mean outweighs its spread,
+ * and 1.4 times that where V has no mean and many tokens share the weight
+ * (kvtc_paged_attend, whose weights have two terms, stays at 1.0 there).  Equal
+ * calls on one device give equal bits.
  *   head_dim 64, 128 or 256; kv_heads * head_dim <= 8192; at most 128 query
  * heads a KV head.  Alignment and overlap as for kvtc_paged_attend, cu 8.
  * workspace: device scratch of kvtc_paged_attend_chunks_workspace_bytes

@@ -555,3 +555,33 @@ def test_single_rows_over_scattered_pools(kv, heads, kv_heads, hd):
         assert (off <= tol).all(), (r, float((off - tol).max()))
         assert (lse[r].double().view(kv_heads, group) - top).abs().max() < (
             2.0 ** -11)
+
+
+@pytest.mark.parametrize("mean,most", [(0.0, 1.5), (2.0, 1.1)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_error_beside_the_output_rounding(kv, dtype, mean, most):
+    """The error against 64 bits in the 2-norm, over that of rounding the
+    64-bit result once.  A weight's rounding to 16 bits is as large, relative,
+    as the output's.  Where V has no mean, so that its products cancel as they
+    add up, the two count alike: sqrt(2), to a few percent by where in a binade
+    the outputs lie.  Where V's mean is twice its spread, the weights' errors
+    cancel instead: against the output they fall by the root of the number of
+    tokens."""
+    import torch
+    new, n = 200, 1900
+    case = paged_case(41, [n], 4, 2, 128)
+    _, _, v, table, _ = case
+    t = np.arange(n)
+    rng = np.random.default_rng(42)
+    v[table[0, t // BLOCK], t % BLOCK] = bits7(
+        rng.standard_normal((n, v.shape[2])) + mean)
+    a = Chunks(kv, 43, [new], [n], 4, 2, 128, dtype, case=case)
+    a.call()
+    ref = a.reference()
+    a.check(ref)
+    exact = torch.from_numpy(ref[0][:new])
+    t = {"bf16": torch.bfloat16, "fp16": torch.float16}[dtype]
+    once = float((exact.to(t).double() - exact).norm())
+    off = float((a.out[:new, :a.width].cpu().double().view(exact.shape) -
+                 exact).norm())
+    assert off <= most * once
