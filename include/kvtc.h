@@ -493,7 +493,7 @@ enum kvtc_rotary_scaling {
  *   context, low, high : for KVTC_ROTARY_BANDS alone: context > 0,
  *             0 <= low < high, all finite.
  * rotary_dim is even and positive (above 2 for KVTC_ROTARY_BASE).
- * Errors: EINVAL.
+ * Errors: EINVAL (where a frequency is not finite too; nothing is written then).
  */
 int kvtc_rotary_frequencies(int rotary_dim, double base, int scaling,
                             double factor, double context, double low,

@@ -321,21 +321,25 @@ int kvtc_rotary_frequencies(int rotary_dim, double base, int scaling,
       !(context > 0 && std::isfinite(context) && low >= 0 && high > low &&
         std::isfinite(high)))
     return KVTC_EINVAL;
-  if (scaling == KVTC_ROTARY_BASE) {
-    if (rotary_dim == 2) return KVTC_EINVAL;    // its one frequency is 1
-    base *= std::pow(factor, rotary_dim / (rotary_dim - 2.0));
-  }
-  for (int i = 0; i < rotary_dim / 2; ++i) {
+  if (scaling == KVTC_ROTARY_BASE && rotary_dim == 2)
+    return KVTC_EINVAL;                         // its one frequency is 1
+  const auto frequency = [&](int i) {
     double f = std::pow(base, -2.0 * i / rotary_dim);
     if (scaling == KVTC_ROTARY_LINEAR) f /= factor;
+    // (a factor of its own: the stretched base may lie out of range)
+    if (scaling == KVTC_ROTARY_BASE)
+      f *= std::pow(factor, -2.0 * i / (rotary_dim - 2.0));
     if (scaling == KVTC_ROTARY_BANDS) {
       const double turns = context * f / 6.283185307179586477;
       const double keep =
           std::min(1.0, std::max(0.0, (turns - low) / (high - low)));
       f *= keep + (1.0 - keep) / factor;
     }
-    inv_freq[i] = f;
-  }
+    return f;
+  };
+  for (int i = 0; i < rotary_dim / 2; ++i)
+    if (!std::isfinite(frequency(i))) return KVTC_EINVAL;
+  for (int i = 0; i < rotary_dim / 2; ++i) inv_freq[i] = frequency(i);
   return KVTC_OK;
 }
 

@@ -205,3 +205,21 @@ def test_frequency_refusals(kv, args):
     with pytest.raises(kv.KvtcError) as e:
         kv.kvtc_rotary_frequencies(*args)
     assert e.value.code == kv.KVTC_EINVAL
+
+
+def test_frequencies_out_of_range(kv):
+    """Frequencies beyond the range of numbers are refused, and nothing is
+    written; a stretched base beyond it is no obstacle."""
+    for args in ((8, 1e4, kv.KVTC_ROTARY_LINEAR, 1e-310),
+                 (8, 1e4, kv.KVTC_ROTARY_BANDS, 1e-310, 100.0, 1.0, 4.0),
+                 (256, 5e-324), (4, 1e-300, kv.KVTC_ROTARY_BASE, 1e-200)):
+        with pytest.raises(kv.KvtcError) as e:
+            kv.kvtc_rotary_frequencies(*args)
+        assert e.value.code == kv.KVTC_EINVAL
+    out = (ctypes.c_double * 4)(*[77.0] * 4)
+    assert kv.lib().kvtc_rotary_frequencies(
+        8, 1e4, kv.KVTC_ROTARY_LINEAR, 1e-310, 0.0, 0.0, 0.0,
+        out) == kv.KVTC_EINVAL
+    assert list(out) == [77.0] * 4
+    f = kv.kvtc_rotary_frequencies(4, 1e300, kv.KVTC_ROTARY_BASE, 1e10)
+    assert f == pytest.approx([1, 1e-160], rel=1e-12)
