@@ -585,3 +585,28 @@ def test_error_beside_the_output_rounding(kv, dtype, mean, most):
     off = float((a.out[:new, :a.width].cpu().double().view(exact.shape) -
                  exact).norm())
     assert off <= most * once
+
+
+@pytest.mark.parametrize("heads,kv_heads,hd,news,cols,launches", [
+    (2, 2, 64, [16], 16, 1), (2, 2, 64, [16], 64, 1),
+    (2, 2, 64, [16], 65, 2),
+    # 18 tokens of 7 heads to a tile, two tiles an item (one at head_dim 256):
+    # 4 (12 + 26) items, and one request more
+    (28, 4, 128, [16] * 26, 8, 1), (28, 4, 128, [16] * 26 + [0], 8, 2),
+    (1, 1, 256, [128] * 76, 8, 1), (1, 1, 256, [128] * 76 + [1], 8, 2),
+    (1, 1, 64, [256] * 76, 16, 1), (1, 1, 64, [256] * 76 + [1], 16, 2)])
+def test_launches_by_items_and_columns(kv, heads, kv_heads, hd, news, cols,
+                                       launches):
+    """One launch where the table has at most 64 columns and there are at most
+    as many items, kv_heads (ceil(N / rows of an item) + R), as SMs."""
+    rows = 128 // (heads // kv_heads) * (1 if hd == 256 else 2)
+    items = kv_heads * (-(-sum(news) // rows) + len(news))
+    assert launches == (1 if items <= 152 and cols <= 64 else 2)
+    most = -(-max(news) // BLOCK)
+    case = paged_case(5, news, heads, kv_heads, hd, extra_cols=cols - most)
+    a = Chunks(kv, 6, news, news, heads, kv_heads, hd, case=case, behind=0)
+    assert a.d_table.shape[1] == cols
+    before = kv.kvtc_launch_count()
+    a.call()
+    assert kv.kvtc_launch_count() - before == launches
+    a.check()

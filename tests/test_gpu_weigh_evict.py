@@ -555,3 +555,61 @@ def test_evict_the_widest_table(kv, short):
     pool[total - new + j // BLOCK, j % BLOCK] = pool[
         1 + np.searchsorted(used, kept // BLOCK), kept % BLOCK]
     np.testing.assert_array_equal(d_pool.cpu().numpy(), pool)
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("weights", [ties, equal, odd])
+@pytest.mark.parametrize("n,R", [(5000, 3), (10000, 3), (20000, 3),
+                                 (20000, 20), (20000, 39)])
+def test_evict_ties_over_several_blocks(kv, n, R, weights, in_place):
+    """Equal and odd weights where two, four and eight blocks choose for a
+    request (by the table's width and the number of requests)."""
+    for keep in (40, 3000, n - 5):
+        lens = [39, n, n // 2 + 7] + [0, 41, 700] * R
+        a = Evict(kv, keep + n, lens[:R], keep, 3, 5, D=8, streams=1,
+                  weights=weights, in_place=in_place)
+        a.call()
+        a.check()
+
+
+def test_weigh_pools_past_32_bits(kv):
+    """Blocks past 2^32 elements of the pool."""
+    import torch
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB")
+    a = Weigh(kv, 36, [40, 1], [200, 90], 32, 8, 128)
+    few = a.k.shape[0]
+    blocks = (1 << 32) // (16 * 1024) + few
+    wide = torch.zeros((blocks, 16, 1024), dtype=a.d_k.dtype, device="cuda")
+    wide[blocks - few:] = a.d_k
+    a.d_k = wide
+    a.d_table.copy_(torch.where(a.d_table < few, a.d_table + blocks - few,
+                                a.d_table))
+    a.call()
+    a.check()
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+def test_evict_pools_past_32_bits(kv, in_place):
+    """Blocks past 2^32 elements of the pools, and others before them."""
+    import torch
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB")
+    a = Evict(kv, 14, [200, 70, 3], 64, 2, 9, D=1024, in_place=in_place)
+    few = a.num_blocks
+    blocks = (1 << 32) // (16 * 1024) + few
+    small, wide = a.d_pools, []
+    # every second block far away
+    at = torch.arange(few, device="cuda")
+    at = torch.where(at % 2 == 0, at, at + blocks - few)
+    for p in small:
+        w = torch.zeros((blocks, 16, 1024), dtype=p.dtype, device="cuda")
+        w[at] = p
+        wide.append(w)
+    for t in {id(x): x for x in (a.d_table, a.d_out_table)}.values():
+        t.copy_(torch.where(t < few, at[t.clamp_max(few - 1).long()].int(),
+                            t))
+    a.d_pools, a.num_blocks = wide, blocks
+    a.call()
+    a.d_pools = [w[at] for w in wide]
+    a.check()
