@@ -582,7 +582,8 @@ int64_t kvtc_paged_attend_chunks_workspace_bytes(int cuda_device, int R,
  * workspace: device scratch of kvtc_paged_attend_chunks_workspace_bytes
  * bytes (20 to 41 MB), used only while the call's work runs on cuda_stream:
  * calls that may run at the same time need one each.  Two kernel launches; one
- * where the table has at most 64 columns and there are few rows.
+ * where the table has at most 64 columns (at head_dim 256 mostly 32) and there
+ * are few rows.
  * Errors: EINVAL, ESIZE, EALIGN, ENOTSUP, ECUDA.
  */
 int kvtc_paged_attend_chunks(

@@ -1352,11 +1352,20 @@ int kvtc_paged_attend_chunks(
   p.sink = window ? sink : 0;
   p.window = window;
   // Few items that are short whatever the lengths are (the table is narrow) go to
-  // a block each, without the second launch (16 rows behind 240 tokens 14.5 and
-  // 13.5 us a call).
+  // a block each, without the second launch, which is worth about eight units of
+  // one block: 8 x 128 tokens (8 KV heads, 16 rows, lengths of 128, 512 and 1024:
+  // 12.2, 16.7 and 22.0 us from a graph against 19.7, 21.7 and 24.7 in runs that
+  // are joined; at head_dim 64 11.3, 14.7 and 19.2 against 17.0, 18.8 and 21.0),
+  // at head_dim 256 8 x 64 (256, 512, 768 and 1024 tokens: 18.2, 24.3, 30.2 and
+  // 36.3 against 23.1, 26.1, 25.9 and 26.7).  Where more than half of the blocks
+  // have an item, longer ones too: runs cut few of them (136 items at head_dim
+  // 256, 768 and 1024 tokens: 29.5 and 35.4 against 33.6 and 39.7; 60 items 27.7
+  // and 33.8 against 23.5 and 24.3).
   const int per = p.tq * (head_dim == 256 ? 1 : 2);
   const int64_t items = (int64_t)kv_heads * ((N + per - 1) / per + R);
-  p.whole = items <= kCtas && max_blocks <= 8 * 128 / kBlock;
+  const int unit = head_dim == 256 ? 64 : 128;
+  p.whole = items <= kCtas && max_blocks <= 8 * 128 / kBlock &&
+            (max_blocks <= 8 * unit / kBlock || items > kCtas / 2);
   // Few items are cut into many parts each, which eight threads a row join (64
   // rows behind 128K tokens, one head: 95 us a call with one thread a row, 31 with
   // eight; 36 items 43 and 40).  More items have few parts, and so many threads

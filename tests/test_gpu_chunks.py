@@ -610,3 +610,19 @@ def test_launches_by_items_and_columns(kv, heads, kv_heads, hd, news, cols,
     a.call()
     assert kv.kvtc_launch_count() - before == launches
     a.check()
+
+
+@pytest.mark.parametrize("news,lens,launches", [
+    ([16], 500, 1), ([16], 512, 1), ([16], 528, 2), ([16], 1000, 2),
+    # 75, 77 and 153 items
+    ([1] * 74, 1000, 2), ([1] * 76, 1000, 1), ([1] * 152, 300, 2)])
+def test_launches_at_head_dim_256(kv, news, lens, launches):
+    """A block takes units of 64 tokens there: one launch up to 32 columns, up
+    to 64 where more than 76 items keep the SMs busy."""
+    lens = [lens] + [40] * (len(news) - 1)
+    case = paged_case(7, lens, 1, 1, 256, extra_cols=0)
+    a = Chunks(kv, 8, news, lens, 1, 1, 256, case=case, behind=0)
+    before = kv.kvtc_launch_count()
+    a.call()
+    assert kv.kvtc_launch_count() - before == launches
+    a.check()
