@@ -612,8 +612,10 @@ int64_t kvtc_paged_weigh_workspace_bytes(int cuda_device, int R, int64_t N,
  *   acc, acc_out : DEVICE fp32 [R][acc_ld], acc_ld >= 16 * max_blocks,
  *                  % 4 == 0; acc_out may be acc itself.
  * The others are kvtc_paged_attend_chunks' (a few of its rows may be given,
- * with a cu of their own, if they are the requests' last).  Tokens in blocks
- * whose id is out of range receive nothing and, where attended, flag
+ * with a cu of their own, if they are the requests' last).  Every row is
+ * multiplied with every tile of 256 tokens that any row of its request attends
+ * to, so the last rows of a prompt cost far less than all of them.  Tokens in
+ * blocks whose id is out of range receive nothing and, where attended, flag
  * KVTC_FLAG_BLOCK.  Sums are in fp32, in a fixed order: equal calls on one
  * device give equal bits.  A weight is off, relative, by its score's error (a
  * sum of head_dim products in fp32) and by 2^-22 (1 + |lse|).  Two kernel
@@ -666,7 +668,8 @@ int64_t kvtc_paged_evict_workspace_bytes(int R, int max_blocks);
  *   lens_out     : DEVICE int32 [R], written: min(lens[r], keep); may be lens
  *                  itself.
  * A token whose old or new block id is out of range stays in the list, its
- * rows are not written, and KVTC_FLAG_BLOCK is set.  workspace: device scratch
+ * rows are not written, and KVTC_FLAG_BLOCK is set (new ids are looked at where
+ * there are pools).  workspace: device scratch
  * of kvtc_paged_evict_workspace_bytes bytes (8 for each token that the table
  * has place for), used only while the call's work runs on cuda_stream; calls
  * that may run at the same time need one each.  One kernel launch, and one per
